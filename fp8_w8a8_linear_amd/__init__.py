@@ -14,7 +14,8 @@ __all__ = ["lib", "LIB_PATH", "NhmError", "Geometry", "Layout", "WsLayout", "Fp8
            "GEOMETRY", "mixer_layout", "quantize_static", "fp8_linear", "fp8_linear_workspace_bytes",
            "decode_ws_layout", "prefill_ws_layout", "mixer_decode", "mixer_prefill", "NHM_BF16", "NHM_E4M3",
            "NHM_F32", "fp8_dequant_channel_bf16", "mixer_decode_noalloc", "mixer_decode_q",
-           "dispatch_counters"]
+           "dispatch_counters", "Lora", "fp8_linear_lora", "fp8_linear_lora_workspace_bytes", "beam_select",
+           "beam_select_workspace_bytes", "beam_reorder", "BatchPlan", "batch_plan"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnhm.so")
 if not os.path.exists(LIB_PATH):
@@ -63,6 +64,15 @@ class _MixerParams(C.Structure):
                 ("dt_bias", C.c_void_p)]
 
 
+class _Lora(C.Structure):
+    _fields_ = [("a", C.c_void_p), ("b", C.c_void_p), ("scale", C.c_void_p), ("n_adapters", C.c_int32),
+                ("rank", C.c_int32)]
+
+
+class _StatePool(C.Structure):
+    _fields_ = [("ssm", C.c_void_p), ("conv", C.c_void_p)]
+
+
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
 _SIGS = {
     "nhm_status_str": (C.c_char_p, [C.c_int]),
@@ -89,6 +99,14 @@ _SIGS = {
     "nhm_mixer_decode_noalloc": (C.c_int, [C.POINTER(_MixerParams), _p, _i32, _p, _p, C.c_int, _p, _i32, _p, _p]),
     "nhm_mixer_prefill_ex": (C.c_int, [C.POINTER(_MixerParams), _p, _i64, _p, _i32, _p, _p, _i32, _p, C.c_int, _p,
                                        _i32, _p, _p, _sz, _p]),
+    "nhm_fp8_linear_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, C.c_int, _i32]),
+    "nhm_fp8_linear_lora": (C.c_int, [_p, C.c_int, _i64, _i64, C.POINTER(_Fp8Weight), C.POINTER(_Lora), _p, _p, C.c_int,
+                                      _i64, _i32, _p, _sz, _p]),
+    "nhm_beam_select_workspace_bytes": (_sz, [_i64, _i32, _i64, _i32]),
+    "nhm_beam_select": (C.c_int, [_p, C.c_int, _i64, _i64, _i32, _i64, _p, _p, _i32, _i32, _p, _p, _p, _p, _sz, _p]),
+    "nhm_beam_reorder": (C.c_int, [C.POINTER(Geometry), _p, _p, _i64, _i32, C.POINTER(_StatePool), _i32, C.c_int, _i32,
+                                   _p, _p]),
+    "nhm_batch_plan": (C.c_int, [_p, _p, _p, _i32, _i64, _p, _p, _p, _p, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -297,3 +315,191 @@ def mixer_prefill(params: MixerParams, hidden, cu_seqlens, slot_idx, has_initial
                                     _ptr(conv_pool), int(ssm_pool.shape[0]), _ptr(out), _ptr(ws), ws.numel(),
                                     _stream(stream)))
     return out
+
+
+# ---- serving operators (include/nhm_serving.h)
+
+def _on(dev, shapes):
+    """Checks (tensor, name, dtypes, shape) entries: contiguous, on `dev`, of one of the dtypes and of the shape
+    (None: not checked). Optional tensors may be None."""
+    for t, name, dtypes, shape in shapes:
+        if t is None:
+            continue
+        _dev_tensor(t, name)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} of dtype {t.dtype}: expected {' or '.join(str(d) for d in dtypes)}")
+        if shape is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} of shape {tuple(t.shape)}: expected {shape}")
+
+
+def _call(dev, stream, fn, *args):
+    """One library call on `stream` (default: the current stream of `dev`) with `dev` current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream.cuda_stream))
+
+
+def _bf16_types():
+    import torch
+    return (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _workspace(ws, need, dev):
+    import torch
+    if ws is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _on(dev, [(ws, "ws", (torch.uint8,), None)])
+    return ws
+
+
+class Lora:
+    """The low-rank adapters of one projection [n, k] on the device: a [n_adapters, rank, k] and b
+    [n_adapters, n, rank] as bf16 (bits or bfloat16), scale f32 [n_adapters] or None (1)."""
+
+    def __init__(self, a, b, scale=None):
+        import torch
+        if a.dim() != 3 or b.dim() != 3 or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+            raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)}: expected [e, rank, k] and [e, n, rank]")
+        self.n_adapters, self.rank, self.k = (int(v) for v in a.shape)
+        self.n = int(b.shape[1])
+        _on(a.device, [(a, "a", _bf16_types(), None), (b, "b", _bf16_types(), None),
+                       (scale, "scale", (torch.float32,), (self.n_adapters,))])
+        self.a, self.b, self.scale = a, b, scale
+        self._s = _Lora(a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr(), self.n_adapters, self.rank)
+
+    @property
+    def struct(self):
+        return self._s
+
+
+def fp8_linear_lora_workspace_bytes(m, n, k, a_type, rank):
+    return int(lib.nhm_fp8_linear_lora_workspace_bytes(m, n, k, a_type, rank))
+
+
+def fp8_linear_lora(a, weight: Fp8Weight, lora: Lora, row_adapter, out=None, ws=None, out_type=None, exact=False,
+                    stream=None):
+    """[m, n] = W8A8(a [m, k], weight) + each row's adapter (row_adapter int32 [m]; a value outside
+    [0, lora.n_adapters): none). a: bf16 (bits or bfloat16) or e4m3 codes (uint8).
+
+    The output is bf16 bits (int16) unless out_type is NHM_F32 (or out is a float32 tensor)."""
+    import torch
+    dev = a.device
+    _on(dev, [(a, "a", _bf16_types() + (torch.uint8,), None), (row_adapter, "row_adapter", (torch.int32,), (a.shape[0],)),
+              (weight.w, "weight", (weight.w.dtype,), None), (lora.a, "lora", (lora.a.dtype,), None)])
+    a_type = NHM_E4M3 if a.dtype == torch.uint8 else NHM_BF16
+    if out_type is None:
+        out_type = NHM_F32 if out is not None and out.dtype == torch.float32 else NHM_BF16
+    m = int(a.shape[0])
+    if a.dim() != 2 or a.shape[1] != weight.k:
+        raise ValueError(f"a of shape {tuple(a.shape)}: expected [m, {weight.k}]")
+    if (lora.n, lora.k) != (weight.n, weight.k):
+        raise ValueError(f"adapters of a [{lora.n}, {lora.k}] projection beside a [{weight.n}, {weight.k}] weight")
+    if out is None:
+        out = torch.empty((m, weight.n), dtype=torch.float32 if out_type == NHM_F32 else torch.int16, device=dev)
+    else:
+        _on(dev, [(out, "out", (torch.float32,) if out_type == NHM_F32 else _bf16_types(), (m, weight.n))])
+    ws = _workspace(ws, 0 if ws is not None else fp8_linear_lora_workspace_bytes(m, weight.n, weight.k, a_type, lora.rank),
+                    dev)
+    _call(dev, stream, lib.nhm_fp8_linear_lora, a.data_ptr(), a_type, m, weight.k, C.byref(weight.struct),
+          C.byref(lora.struct), row_adapter.data_ptr(), out.data_ptr(), out_type, weight.n, 1 if exact else 0,
+          ws.data_ptr(), ws.numel())
+    return out
+
+
+def beam_select_workspace_bytes(n_groups, n_beams, vocab, n_cand):
+    return int(lib.nhm_beam_select_workspace_bytes(n_groups, n_beams, vocab, n_cand))
+
+
+def beam_select(logits, cum, n_cand, finished=None, eos=0, scores=None, parents=None, tokens=None, ws=None, stream=None):
+    """(scores f32, parents int32, tokens int32), each [groups, n_cand]: the n_cand best continuations of each
+    group's beams, best first. logits: bf16 (bits or bfloat16) or float32 [groups * beams, vocab] (or [groups, beams,
+    vocab]); cum: float32 [groups, beams]; finished: int32 [groups, beams], non-zero for beams that go on by eos alone."""
+    import torch
+    dev = logits.device
+    if cum.dim() != 2:
+        raise ValueError(f"cum of shape {tuple(cum.shape)}: expected [groups, beams]")
+    G, K = (int(v) for v in cum.shape)
+    V = int(logits.shape[-1])
+    if logits.numel() != G * K * V:
+        raise ValueError(f"logits of shape {tuple(logits.shape)}: expected [{G} * {K}, vocab]")
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _on(dev, [(logits, "logits", _bf16_types() + f32, None), (cum, "cum", f32, None), (finished, "finished", i32, (G, K)),
+              (scores, "scores", f32, (G, n_cand)), (parents, "parents", i32, (G, n_cand)),
+              (tokens, "tokens", i32, (G, n_cand))])
+    if scores is None:
+        scores = torch.empty((G, n_cand), dtype=torch.float32, device=dev)
+    if parents is None:
+        parents = torch.empty((G, n_cand), dtype=torch.int32, device=dev)
+    if tokens is None:
+        tokens = torch.empty((G, n_cand), dtype=torch.int32, device=dev)
+    ws = _workspace(ws, 0 if ws is not None else beam_select_workspace_bytes(G, K, V, n_cand), dev)
+    _call(dev, stream, lib.nhm_beam_select, logits.data_ptr(), NHM_F32 if logits.dtype == torch.float32 else NHM_BF16, V,
+          G, K, V, cum.data_ptr(), None if finished is None else finished.data_ptr(), int(eos), n_cand,
+          scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), ws.data_ptr(), ws.numel())
+    return scores, parents, tokens
+
+
+def beam_reorder(parents, slots, ssm_pools, conv_pools, new_slots=None, g=GEOMETRY, stream=None):
+    """The slots of each group's beams after a selection (int32 [groups, beams]); the states of beams that share a
+    parent are copied between the pools' rows in place. parents, slots: int32 [groups, beams]; ssm_pools, conv_pools:
+    one tensor per layer, as mixer_decode takes them."""
+    import torch
+    dev = parents.device
+    ssm_pools, conv_pools = list(ssm_pools), list(conv_pools)
+    if len(ssm_pools) != len(conv_pools) or not ssm_pools:
+        raise ValueError(f"{len(ssm_pools)} SSM pools and {len(conv_pools)} conv pools: one of each per layer")
+    if parents.dim() != 2:
+        raise ValueError(f"parents of shape {tuple(parents.shape)}: expected [groups, beams]")
+    geom = _geom(g)
+    S = int(ssm_pools[0].shape[0])
+    conv_dim = geom.n_heads * geom.head_dim + 2 * geom.n_groups * geom.d_state
+    st = _ssm_type(ssm_pools[0])
+    row, win = geom.n_heads * geom.head_dim * geom.d_state, (geom.conv_width - 1) * conv_dim
+    for i, (sp, cp) in enumerate(zip(ssm_pools, conv_pools)):
+        _on(dev, [(sp, f"ssm_pools[{i}]", (ssm_pools[0].dtype,), None), (cp, f"conv_pools[{i}]", _bf16_types(), None)])
+        if sp.shape[0] != S or sp.numel() != S * row or cp.numel() != S * win:
+            raise ValueError(f"layer {i}: pools of shapes {tuple(sp.shape)} and {tuple(cp.shape)} do not hold {S} rows")
+    i32, shape = (torch.int32,), tuple(parents.shape)
+    _on(dev, [(parents, "parents", i32, None), (slots, "slots", i32, shape), (new_slots, "new_slots", i32, shape)])
+    if new_slots is None:
+        new_slots = torch.empty_like(slots)
+    arr = (_StatePool * len(ssm_pools))(*[(sp.data_ptr(), cp.data_ptr()) for sp, cp in zip(ssm_pools, conv_pools)])
+    _call(dev, stream, lib.nhm_beam_reorder, C.byref(geom), parents.data_ptr(), slots.data_ptr(), shape[0], shape[1], arr,
+          len(arr), st, S, new_slots.data_ptr())
+    return new_slots
+
+
+class BatchPlan:
+    """The index tensors of a packed batch of up to n_tokens tokens in n_seqs sequences (int32, filled by
+    batch_plan): cu_seqlens [n_seqs + 1], has_initial [n_seqs], and per token token_seq, token_pos, token_adapter."""
+
+    def __init__(self, n_seqs, n_tokens, device="cuda"):
+        import torch
+        self.n_seqs, self.n_tokens = int(n_seqs), int(n_tokens)
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
+        self.cu_seqlens, self.has_initial = new(self.n_seqs + 1), new(self.n_seqs)
+        self.token_seq, self.token_pos, self.token_adapter = new(self.n_tokens), new(self.n_tokens), new(self.n_tokens)
+
+
+def batch_plan(lengths, plan: BatchPlan, past=None, adapters=None, stream=None):
+    """Fills plan from lengths int32 [n_seqs] (this batch's tokens of each sequence), past (tokens its state holds
+    already) and adapters (its adapter), both int32 [n_seqs] or None. Returns plan."""
+    import torch
+    dev, n = lengths.device, (plan.n_seqs,)
+    i32 = (torch.int32,)
+    _on(dev, [(lengths, "lengths", i32, n), (past, "past", i32, n), (adapters, "adapters", i32, n),
+              (plan.cu_seqlens, "plan", i32, None)])
+    opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _call(dev, stream, lib.nhm_batch_plan, lengths.data_ptr(), opt(past), opt(adapters), plan.n_seqs, plan.n_tokens,
+          plan.cu_seqlens.data_ptr(), plan.has_initial.data_ptr(), plan.token_seq.data_ptr(), plan.token_pos.data_ptr(),
+          plan.token_adapter.data_ptr())
+    return plan

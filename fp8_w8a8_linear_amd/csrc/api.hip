@@ -26,9 +26,12 @@ static const char* const kKernNames[(int)Kern::kCount] = {
     "quant_vec8", "quant_scalar", "dequant_channel", "gemv", "gemm_ring192x128", "gemm_ring192x128_exact",
     "gemm_ring256x128", "gemm_ring256x128_exact", "gemm_ring256x256", "gemm_ring256x256_exact", "gemm_panel64x128",
     "gemm_panel64x128_exact", "gemm_tile128", "gemm_tile128_exact", "gemm_splitk_reduce", "decode_ssm",
-    "gnorm_quant", "clear", "conv_fwd", "ssd_state", "ssd_pass", "ssd_out"};
+    "gnorm_quant", "clear", "conv_fwd", "ssd_state", "ssd_pass", "ssd_out", "lora_down", "lora_up", "beam_rows",
+    "beam_pick", "beam_reorder", "batch_plan"};
 static std::atomic<uint64_t> g_launches[(int)Kern::kCount];
 static std::atomic<uint64_t> g_rows[(int)Kern::kCount];
+
+void clear_error() { g_err[0] = 0; }
 
 void count_launch(Kern k, int64_t rows) {
     g_launches[(int)k].fetch_add(1, std::memory_order_relaxed);
@@ -43,7 +46,7 @@ nhm_status check_launch(const char* what) {
 
 static bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-static nhm_status check_geometry(const nhm_geometry* g) {
+nhm_status check_geometry(const nhm_geometry* g) {
     if (!g) return fail(NHM_ERR_NULL, "geometry is NULL");
     if (g->hidden <= 0 || g->n_heads <= 0 || g->n_groups <= 0)
         return fail(NHM_ERR_UNSUPPORTED, "hidden, n_heads and n_groups must be positive");
@@ -63,7 +66,7 @@ static nhm_status check_geometry(const nhm_geometry* g) {
     return NHM_OK;
 }
 
-static void fill_layout(const nhm_geometry* g, nhm_layout* l) {
+void fill_layout(const nhm_geometry* g, nhm_layout* l) {
     const int32_t inner = g->n_heads * g->head_dim;
     const int32_t gs = g->n_groups * g->d_state;
     l->d_inner = inner;
@@ -122,7 +125,7 @@ static size_t proj_part_bytes(int64_t m, int64_t n, int64_t k) { return use_gemv
 
 // The linear's workspace: the activation codes of a bf16 input (required), then the split-k
 // partials of the shapes that take a split (optional: without them those shapes run unsplit).
-static size_t linear_codes_ws(int64_t m, int64_t k, nhm_dtype t) {
+size_t linear_codes_ws(int64_t m, int64_t k, nhm_dtype t) {
     return t == NHM_BF16 ? align_up((size_t)m * (size_t)k, 256) : 0;
 }
 static size_t linear_ws(int64_t m, int64_t n, int64_t k, nhm_dtype t) {
@@ -191,15 +194,9 @@ static MixerWs prefill_ws(const nhm_geometry* g, int64_t T, int32_t n, int32_t c
 }
 
 
-// One projection on an e4m3 activation [m, lda]; out_f32 non-null: f32 output instead of out.
-// part / part_bytes: scratch for the GEMM's split-k partials (nullptr: no split).
-// exact: every product summed in f32 on the tiled path too (the GEMV always is).
-// out_q: also the e4m3 codes of the bf16 output under *q_scale (GEMV path only; callers of the
-// tiled path quantize its output themselves).
-static nhm_status project(const uint8_t* a, int64_t lda, int64_t m, const nhm_fp8_weight& w, uint16_t* out,
-                          int64_t ld_out, hipStream_t st, float* out_f32 = nullptr, float* part = nullptr,
-                          size_t part_bytes = 0, bool exact = false, uint8_t* out_q = nullptr, int64_t ld_q = 0,
-                          const float* q_scale = nullptr) {
+nhm_status project(const uint8_t* a, int64_t lda, int64_t m, const nhm_fp8_weight& w, uint16_t* out, int64_t ld_out,
+                   hipStream_t st, float* out_f32, float* part, size_t part_bytes, bool exact, uint8_t* out_q,
+                   int64_t ld_q, const float* q_scale) {
     if (use_gemv(m, w.n, w.k))
         return launch_gemv(a, lda, (int)m, w.w, w.w_scale, w.a_scale, w.n, w.k, out, ld_out, st, out_f32, out_q, ld_q,
                            q_scale, nullptr, 0, ws_step(w));
@@ -304,10 +301,11 @@ nhm_status nhm_fp8_linear(const void* a, nhm_dtype a_type, int64_t m, int64_t ld
     return nhm_fp8_linear_ex(a, a_type, m, ld_a, w, out, NHM_BF16, ld_out, ws, ws_bytes, stream);
 }
 
-static nhm_status linear_call(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
-                              void* out, nhm_dtype out_type, int64_t ld_out, void* ws, size_t ws_bytes, void* stream,
-                              bool exact) {
-    g_err[0] = 0;
+}  // extern "C"
+
+nhm_status nhm::linear_check(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
+                             const void* out, nhm_dtype out_type, int64_t ld_out, const void* ws, size_t ws_bytes,
+                             size_t need) {
     if (out_type != NHM_BF16 && out_type != NHM_F32)
         return fail(NHM_ERR_UNSUPPORTED, "output dtype %d: bf16 or f32", (int)out_type);
     if (!w) return fail(NHM_ERR_NULL, "weight is NULL");
@@ -327,11 +325,21 @@ static nhm_status linear_call(const void* a, nhm_dtype a_type, int64_t m, int64_
         return fail(NHM_ERR_ALIGN, "a must be 16-byte aligned with 16-byte row stride");
     if (!aligned(out, out_type == NHM_F32 ? 4 : 2))
         return fail(NHM_ERR_ALIGN, "out must be aligned to its element size");
-    const size_t need = linear_codes_ws(m, w->k, a_type);
     if (need > 0 && (!ws || ws_bytes < need))
         return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
     if (ws && !aligned(ws, 256)) return fail(NHM_ERR_ALIGN, "ws must be 256-byte aligned");
-    if ((s = check_offsets(m, a_type == NHM_BF16 ? w->k : ld_a, w->n, w->k, "linear")) != NHM_OK) return s;
+    return check_offsets(m, a_type == NHM_BF16 ? w->k : ld_a, w->n, w->k, "linear");
+}
+
+extern "C" {
+
+static nhm_status linear_call(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
+                              void* out, nhm_dtype out_type, int64_t ld_out, void* ws, size_t ws_bytes, void* stream,
+                              bool exact) {
+    g_err[0] = 0;
+    const size_t need = w && m > 0 ? linear_codes_ws(m, w->k, a_type) : 0;
+    nhm_status s = linear_check(a, a_type, m, ld_a, w, out, out_type, ld_out, ws, ws_bytes, need);
+    if (s != NHM_OK || m == 0) return s;
     hipStream_t st = (hipStream_t)stream;
     const uint8_t* aq = static_cast<const uint8_t*>(a);
     int64_t lda = ld_a;

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/nhm.h"
+#include "../../include/nhm_serving.h"
 
 namespace nhm {
 
@@ -15,6 +16,9 @@ nhm_status fail(nhm_status s, const char* fmt, ...);
 // Returns NHM_ERR_HIP (with the runtime's message) if the last launch failed.
 nhm_status check_launch(const char* what);
 
+// Empties the calling thread's failure detail (nhm_last_error), as every entry point does first.
+void clear_error();
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Path-taken counters (nhm_dispatch_counters): one per kernel the library launches, counting
@@ -23,9 +27,28 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 enum class Kern : int {
     kQuantVec8, kQuantScalar, kDequantChannel, kGemv, kRing192x128, kRing192x128Exact, kRing256x128,
     kRing256x128Exact, kRing256x256, kRing256x256Exact, kPanel64x128, kPanel64x128Exact, kTile128,
-    kTile128Exact, kSplitkReduce, kDecodeSsm, kGnormQuant, kClear, kConvFwd, kSsdState, kSsdPass, kSsdOut, kCount
+    kTile128Exact, kSplitkReduce, kDecodeSsm, kGnormQuant, kClear, kConvFwd, kSsdState, kSsdPass, kSsdOut,
+    kLoraDown, kLoraUp, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan, kCount
 };
 void count_launch(Kern k, int64_t rows);
+
+// ---- host checks and the projection shared by the entry points (api.hip)
+nhm_status check_geometry(const nhm_geometry* g);
+void fill_layout(const nhm_geometry* g, nhm_layout* l);
+// Every check of nhm_fp8_linear_ex's arguments; need: workspace bytes the call cannot do without.
+nhm_status linear_check(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
+                        const void* out, nhm_dtype out_type, int64_t ld_out, const void* ws, size_t ws_bytes,
+                        size_t need);
+// bytes of the e4m3 copy of a bf16 activation
+size_t linear_codes_ws(int64_t m, int64_t k, nhm_dtype t);
+// One projection on an e4m3 activation [m, lda]; out_f32 non-null: f32 output instead of out.
+// part / part_bytes: scratch for the GEMM's split-k partials (nullptr: no split).
+// exact: every product summed in f32 on the tiled path too (the GEMV always is).
+// out_q: also the e4m3 codes of the bf16 output under *q_scale (GEMV path only; callers of the
+// tiled path quantize its output themselves).
+nhm_status project(const uint8_t* a, int64_t lda, int64_t m, const nhm_fp8_weight& w, uint16_t* out, int64_t ld_out,
+                   hipStream_t st, float* out_f32 = nullptr, float* part = nullptr, size_t part_bytes = 0,
+                   bool exact = false, uint8_t* out_q = nullptr, int64_t ld_q = 0, const float* q_scale = nullptr);
 
 // ---- activation quant (quant.hip)
 void launch_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, const float* scale,
@@ -151,5 +174,71 @@ nhm_status launch_prefill_mid(const PrefillArgs& a, hipStream_t st);
 // log-decay and the chunk's own state; then, after the state pass, the outputs.
 void launch_ssd_state(const PrefillArgs& a, hipStream_t st);
 void launch_ssd_out(const PrefillArgs& a, hipStream_t st);
+
+// ---- low-rank adapters (lora.hip)
+struct LoraArgs {
+    const uint16_t* x;         // bf16 [m, ld_x], or nullptr with x_codes
+    const uint8_t* x_codes;    // e4m3 [m, ld_x], worth code * *a_scale
+    int64_t ld_x, m, n, k;
+    const float* a_scale;      // [1]
+    const uint16_t* a;         // bf16 [n_adapters, rank, k]
+    const uint16_t* b;         // bf16 [n_adapters, n, rank]
+    const float* scale;        // [n_adapters] or nullptr
+    int32_t n_adapters, rank;
+    const int32_t* row_adapter;   // [m]
+    float* t;                  // [m, rank]
+    float* base;               // f32 projection [m, n]
+    uint16_t* out;             // bf16 [m, ld_out], or nullptr with out_f32
+    float* out_f32;
+    int64_t ld_out;
+};
+nhm_status launch_lora_down(const LoraArgs& g, hipStream_t st);
+nhm_status launch_lora_up(const LoraArgs& g, hipStream_t st);
+
+// ---- beam search (beam.hip)
+struct BeamArgs {
+    const uint16_t* logits_bf16;   // [n_groups * n_beams, ld], or nullptr with logits_f32
+    const float* logits_f32;
+    int64_t ld, n_groups;
+    int32_t n_beams;
+    int64_t vocab;
+    const float* cum;              // [n_groups, n_beams]
+    const int32_t* finished;       // [n_groups, n_beams] or nullptr
+    int32_t eos, n_cand;
+    float* scores;                 // [n_groups, n_cand]
+    int32_t* parents;
+    int32_t* tokens;
+    float* row_top;                // workspace: each row's largest logit
+    double* row_log;               // and log(sum exp(x - top))
+};
+size_t beam_ws_bytes(int64_t rows, int64_t vocab, int32_t n_cand);
+nhm_status launch_beam_select(BeamArgs g, void* ws, hipStream_t st);
+
+constexpr int kMaxStatePools = 64;
+struct ReorderArgs {
+    nhm_state_pool pools[kMaxStatePools];
+    const int32_t* parents;
+    const int32_t* slots;
+    int32_t* new_slots;
+    int32_t n_beams, n_slots;
+    int64_t ssm_bytes, conv_bytes;   // of one row; multiples of 16
+};
+nhm_status launch_beam_reorder(const ReorderArgs& g, int64_t n_groups, int32_t n_layers, hipStream_t st);
+
+// ---- batch plan (plan.hip)
+constexpr int kMaxPlanSeqs = 8192;
+struct PlanArgs {
+    const int32_t* lengths;
+    const int32_t* past;        // or nullptr
+    const int32_t* adapters;    // or nullptr
+    int32_t n_seqs;
+    int64_t n_tokens;
+    int32_t* cu_seqlens;
+    int32_t* has_initial;
+    int32_t* token_seq;         // each of the three may be nullptr
+    int32_t* token_pos;
+    int32_t* token_adapter;
+};
+nhm_status launch_batch_plan(const PlanArgs& g, hipStream_t st);
 
 }  // namespace nhm

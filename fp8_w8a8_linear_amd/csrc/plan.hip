@@ -1,0 +1,83 @@
+// The index tensors of a packed batch from request lengths (nhm_batch_plan).
+//
+// cu_seqlens is a prefix sum over the sequences; each token then finds its sequence in it. Every
+// workgroup forms the whole prefix sum itself (at most 8,192 lengths, a few reads per thread, all
+// from L2 after the first) and keeps it in LDS, so one launch without communication between
+// workgroups does both; each then fills its own run of tokens. A token's sequence is the last one
+// that starts at or before it, found by halving the prefix sums in LDS.
+#include "nhm_device.h"
+#include "nhm_internal.h"
+
+namespace nhm {
+
+constexpr int kPlanThreads = 1024;
+
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void batch_plan_kernel(const PlanArgs g) {
+    __shared__ int32_t s_cu[kMaxPlanSeqs + 1];
+    __shared__ int64_t s_wave[kPlanThreads / 64];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int n = g.n_seqs;
+    int64_t carry = 0;
+    if (t == 0) s_cu[0] = 0;
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + t;
+        const int64_t len = i < n ? (int64_t)max(g.lengths[i], 0) : 0;
+        int64_t v = wave_scan(len, lane);
+        if (lane == 63) s_wave[wave] = v;
+        __syncthreads();
+        int64_t before = carry, total = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 64; ++w) {
+            if (w < wave) before += s_wave[w];
+            total += s_wave[w];
+        }
+        // sequences end at n_tokens at the latest (n_tokens < 2^31)
+        if (i < n) s_cu[i + 1] = (int32_t)min(before + v, g.n_tokens);
+        carry += total;
+        __syncthreads();
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int i = t; i <= n; i += kPlanThreads) g.cu_seqlens[i] = s_cu[i];
+        for (int i = t; i < n; i += kPlanThreads) g.has_initial[i] = g.past && g.past[i] > 0 ? 1 : 0;
+    }
+    const int64_t end = s_cu[n];
+    for (int64_t tok = (int64_t)blockIdx.x * kPlanThreads + t; tok < g.n_tokens; tok += (int64_t)gridDim.x * kPlanThreads) {
+        int seq = -1, pos = -1, ad = -1;
+        if (tok < end) {
+            // the last i with s_cu[i] <= tok; its sequence is not empty, since s_cu[i + 1] > tok
+            int lo = 0, hi = n;     // s_cu[lo] <= tok < s_cu[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_cu[mid] <= tok) lo = mid;
+                else hi = mid;
+            }
+            seq = lo;
+            pos = (int)((uint32_t)(g.past ? g.past[lo] : 0) + (uint32_t)(tok - s_cu[lo]));
+            ad = g.adapters ? g.adapters[lo] : -1;
+        }
+        if (g.token_seq) g.token_seq[tok] = seq;
+        if (g.token_pos) g.token_pos[tok] = pos;
+        if (g.token_adapter) g.token_adapter[tok] = ad;
+    }
+}
+
+nhm_status launch_batch_plan(const PlanArgs& g, hipStream_t st) {
+    int64_t blocks = (g.n_tokens + kPlanThreads - 1) / kPlanThreads;
+    blocks = blocks < 1 ? 1 : blocks > 256 ? 256 : blocks;
+    batch_plan_kernel<<<dim3((unsigned)blocks), dim3(kPlanThreads), 0, st>>>(g);
+    count_launch(Kern::kBatchPlan, g.n_tokens);
+    return check_launch("batch plan");
+}
+
+}  // namespace nhm

@@ -1,0 +1,186 @@
+// Entry points of the serving operators (nhm_serving.h): host validation and launch order.
+#include <limits.h>
+
+#include "nhm_internal.h"
+
+using namespace nhm;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool rank_ok(int32_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
+
+// Regions of the adapter call's workspace: the activation codes, the f32 projection, the low-rank product.
+struct LoraWs { size_t codes, base, t, total; };
+LoraWs lora_ws(int64_t m, int64_t n, int64_t k, nhm_dtype a_type, int32_t rank) {
+    LoraWs w{};
+    w.codes = 0;
+    w.base = align_up(linear_codes_ws(m, k, a_type), 256);
+    w.t = w.base + align_up((size_t)m * (size_t)n * sizeof(float), 256);
+    w.total = w.t + align_up((size_t)m * (size_t)rank * sizeof(float), 256);
+    return w;
+}
+
+nhm_status check_lora(const nhm_lora* l) {
+    if (!l) return fail(NHM_ERR_NULL, "lora is NULL");
+    if (!l->a || !l->b) return fail(NHM_ERR_NULL, "lora: a or b is NULL");
+    if (l->n_adapters < 1) return fail(NHM_ERR_SHAPE, "lora: n_adapters %d must be positive", l->n_adapters);
+    if (!rank_ok(l->rank)) return fail(NHM_ERR_UNSUPPORTED, "lora: rank %d: a multiple of 8 in 8 .. 128", l->rank);
+    if (!aligned(l->a, 16) || !aligned(l->b, 16) || !aligned(l->scale, 4))
+        return fail(NHM_ERR_ALIGN, "lora: a and b must be 16-byte aligned, scale 4-byte aligned");
+    return NHM_OK;
+}
+
+constexpr int kMaxBeams = 32, kMaxCand = 64;
+constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxRows = int64_t(1) << 24;
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nhm_fp8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, nhm_dtype a_type, int32_t rank) {
+    if (m <= 0 || n <= 0 || k <= 0 || !rank_ok(rank)) return 0;
+    return lora_ws(m, n, k, a_type, rank).total;
+}
+
+nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
+                               const nhm_lora* lora, const int32_t* row_adapter, void* out, nhm_dtype out_type,
+                               int64_t ld_out, int32_t exact, void* ws, size_t ws_bytes, void* stream) {
+    clear_error();
+    nhm_status s = check_lora(lora);
+    if (s != NHM_OK) return s;
+    const size_t need = w && m > 0 && w->n > 0 && w->k > 0 ? lora_ws(m, w->n, w->k, a_type, lora->rank).total : 0;
+    s = linear_check(a, a_type, m, ld_a, w, out, out_type, ld_out, ws, ws_bytes, need);
+    if (s != NHM_OK || m == 0) return s;
+    if (m > INT_MAX) return fail(NHM_ERR_SHAPE, "m %lld out of range", (long long)m);
+    if (!row_adapter) return fail(NHM_ERR_NULL, "row_adapter is NULL");
+    if (!aligned(row_adapter, 4)) return fail(NHM_ERR_ALIGN, "row_adapter must be 4-byte aligned");
+    hipStream_t st = (hipStream_t)stream;
+    const LoraWs l = lora_ws(m, w->n, w->k, a_type, lora->rank);
+    char* wsb = static_cast<char*>(ws);
+    const uint8_t* q = static_cast<const uint8_t*>(a);
+    int64_t ld_q = ld_a;
+    if (a_type == NHM_BF16) {
+        uint8_t* qb = reinterpret_cast<uint8_t*>(wsb + l.codes);
+        launch_quantize(static_cast<const uint16_t*>(a), m, w->k, ld_a, w->a_scale, qb, w->k, st);
+        if ((s = check_launch("lora quant")) != NHM_OK) return s;
+        q = qb;
+        ld_q = w->k;
+    }
+    LoraArgs g{};
+    g.x = a_type == NHM_BF16 ? static_cast<const uint16_t*>(a) : nullptr;
+    g.x_codes = a_type == NHM_BF16 ? nullptr : q;
+    g.ld_x = ld_a;
+    g.m = m; g.n = w->n; g.k = w->k;
+    g.a_scale = w->a_scale;
+    g.a = lora->a; g.b = lora->b; g.scale = lora->scale;
+    g.n_adapters = lora->n_adapters; g.rank = lora->rank;
+    g.row_adapter = row_adapter;
+    g.t = reinterpret_cast<float*>(wsb + l.t);
+    g.base = reinterpret_cast<float*>(wsb + l.base);
+    g.out = out_type == NHM_BF16 ? static_cast<uint16_t*>(out) : nullptr;
+    g.out_f32 = out_type == NHM_F32 ? static_cast<float*>(out) : nullptr;
+    g.ld_out = ld_out;
+    if ((s = launch_lora_down(g, st)) != NHM_OK) return s;
+    if ((s = project(q, ld_q, m, *w, nullptr, w->n, st, reinterpret_cast<float*>(wsb + l.base), nullptr, 0, exact != 0)) != NHM_OK)
+        return s;
+    return launch_lora_up(g, st);
+}
+
+size_t nhm_beam_select_workspace_bytes(int64_t n_groups, int32_t n_beams, int64_t vocab, int32_t n_cand) {
+    if (n_groups <= 0 || n_beams < 1 || n_beams > kMaxBeams || vocab < 1 || vocab > kMaxVocab || n_cand < 1 ||
+        n_cand > kMaxCand || n_groups > kMaxRows / n_beams)
+        return 0;
+    return beam_ws_bytes(n_groups * n_beams, vocab, n_cand);
+}
+
+nhm_status nhm_beam_select(const void* logits, nhm_dtype type, int64_t ld, int64_t n_groups, int32_t n_beams,
+                           int64_t vocab, const float* cum, const int32_t* finished, int32_t eos, int32_t n_cand,
+                           float* scores, int32_t* parents, int32_t* tokens, void* ws, size_t ws_bytes, void* stream) {
+    clear_error();
+    if (type != NHM_BF16 && type != NHM_F32) return fail(NHM_ERR_UNSUPPORTED, "logits dtype %d: bf16 or f32", (int)type);
+    if (n_groups < 0 || vocab < 1 || n_cand < 1 || n_beams < 1 || ld < vocab)
+        return fail(NHM_ERR_SHAPE, "groups %lld, beams %d, vocab %lld (ld %lld), candidates %d out of range",
+                    (long long)n_groups, n_beams, (long long)vocab, (long long)ld, n_cand);
+    if (n_beams > kMaxBeams || n_cand > kMaxCand || vocab > kMaxVocab || n_groups > kMaxRows / n_beams)
+        return fail(NHM_ERR_UNSUPPORTED, "at most %d beams, %d candidates, a vocabulary of 2^24 and 2^24 rows", kMaxBeams,
+                    kMaxCand);
+    if (n_groups == 0) return NHM_OK;
+    if (!logits || !cum || !scores || !parents || !tokens)
+        return fail(NHM_ERR_NULL, "logits, cum, scores, parents or tokens is NULL");
+    if (finished && (eos < 0 || eos >= vocab)) return fail(NHM_ERR_SHAPE, "eos %d outside the vocabulary", eos);
+    if (!aligned(logits, type == NHM_F32 ? 4 : 2) || !aligned(cum, 4) || !aligned(finished, 4) || !aligned(scores, 4) ||
+        !aligned(parents, 4) || !aligned(tokens, 4))
+        return fail(NHM_ERR_ALIGN, "every tensor must be aligned to its element size");
+    const size_t need = beam_ws_bytes(n_groups * n_beams, vocab, n_cand);
+    if (!ws || ws_bytes < need)
+        return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
+    if (!aligned(ws, 256)) return fail(NHM_ERR_ALIGN, "ws must be 256-byte aligned");
+    BeamArgs g{};
+    g.logits_bf16 = type == NHM_BF16 ? static_cast<const uint16_t*>(logits) : nullptr;
+    g.logits_f32 = type == NHM_F32 ? static_cast<const float*>(logits) : nullptr;
+    g.ld = ld; g.n_groups = n_groups; g.n_beams = n_beams; g.vocab = vocab;
+    g.cum = cum; g.finished = finished; g.eos = eos; g.n_cand = n_cand;
+    g.scores = scores; g.parents = parents; g.tokens = tokens;
+    return launch_beam_select(g, ws, (hipStream_t)stream);
+}
+
+nhm_status nhm_beam_reorder(const nhm_geometry* geo, const int32_t* parents, const int32_t* slots, int64_t n_groups,
+                            int32_t n_beams, const nhm_state_pool* pools, int32_t n_layers, nhm_dtype ssm_type,
+                            int32_t n_slots, int32_t* new_slots, void* stream) {
+    clear_error();
+    nhm_status s = check_geometry(geo);
+    if (s != NHM_OK) return s;
+    if (ssm_type != NHM_F32 && ssm_type != NHM_BF16)
+        return fail(NHM_ERR_UNSUPPORTED, "SSM state dtype %d: f32 or bf16", (int)ssm_type);
+    if (n_groups < 0 || n_beams < 1 || n_layers < 1 || n_slots < 1)
+        return fail(NHM_ERR_SHAPE, "groups %lld, beams %d, layers %d, slots %d out of range", (long long)n_groups, n_beams,
+                    n_layers, n_slots);
+    if (n_beams > kMaxBeams || n_layers > kMaxStatePools || n_groups > kMaxRows / n_beams)
+        return fail(NHM_ERR_UNSUPPORTED, "at most %d beams, %d layers and 2^24 rows", kMaxBeams, kMaxStatePools);
+    if (n_groups == 0) return NHM_OK;
+    if (!parents || !slots || !pools || !new_slots) return fail(NHM_ERR_NULL, "parents, slots, pools or new_slots is NULL");
+    if (!aligned(parents, 4) || !aligned(slots, 4) || !aligned(new_slots, 4))
+        return fail(NHM_ERR_ALIGN, "parents, slots and new_slots must be 4-byte aligned");
+    const size_t nb = (size_t)n_groups * n_beams * 4;
+    if (overlap(new_slots, nb, parents, nb) || overlap(new_slots, nb, slots, nb))
+        return fail(NHM_ERR_UNSUPPORTED, "new_slots must not overlap parents or slots");
+    nhm_layout l;
+    fill_layout(geo, &l);
+    ReorderArgs g{};
+    for (int32_t i = 0; i < n_layers; ++i) {
+        if (!pools[i].ssm || !pools[i].conv) return fail(NHM_ERR_NULL, "layer %d: a pool is NULL", i);
+        if (!aligned(pools[i].ssm, 16) || !aligned(pools[i].conv, 16))
+            return fail(NHM_ERR_ALIGN, "layer %d: pools must be 16-byte aligned", i);
+        g.pools[i] = pools[i];
+    }
+    g.parents = parents; g.slots = slots; g.new_slots = new_slots;
+    g.n_beams = n_beams; g.n_slots = n_slots;
+    g.ssm_bytes = (int64_t)geo->n_heads * geo->head_dim * geo->d_state * (ssm_type == NHM_F32 ? 4 : 2);
+    g.conv_bytes = (int64_t)(geo->conv_width - 1) * l.conv_dim * 2;
+    return launch_beam_reorder(g, n_groups, n_layers, (hipStream_t)stream);
+}
+
+nhm_status nhm_batch_plan(const int32_t* lengths, const int32_t* past, const int32_t* adapters, int32_t n_seqs,
+                          int64_t n_tokens, int32_t* cu_seqlens, int32_t* has_initial, int32_t* token_seq,
+                          int32_t* token_pos, int32_t* token_adapter, void* stream) {
+    clear_error();
+    if (n_seqs < 0 || n_tokens < 0 || n_tokens > INT_MAX)
+        return fail(NHM_ERR_SHAPE, "n_seqs %d or n_tokens %lld out of range", n_seqs, (long long)n_tokens);
+    if (n_seqs > kMaxPlanSeqs) return fail(NHM_ERR_UNSUPPORTED, "%d sequences: at most %d", n_seqs, kMaxPlanSeqs);
+    if (!cu_seqlens || (n_seqs > 0 && (!lengths || !has_initial)))
+        return fail(NHM_ERR_NULL, "lengths, cu_seqlens or has_initial is NULL");
+    if (!aligned(lengths, 4) || !aligned(past, 4) || !aligned(adapters, 4) || !aligned(cu_seqlens, 4) ||
+        !aligned(has_initial, 4) || !aligned(token_seq, 4) || !aligned(token_pos, 4) || !aligned(token_adapter, 4))
+        return fail(NHM_ERR_ALIGN, "every tensor must be 4-byte aligned");
+    const PlanArgs g{lengths, past, adapters, n_seqs, n_tokens, cu_seqlens, has_initial, token_seq, token_pos, token_adapter};
+    return launch_batch_plan(g, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,131 @@
+// Host-only driver for an AddressSanitizer / UndefinedBehaviorSanitizer build of the serving
+// operators' validation (csrc/serving.hip with csrc/api.hip). Every call below fails validation
+// before anything is enqueued, is an empty call or a pure host query, so no GPU is needed; the
+// kernel launchers of the other translation units are replaced by stubs that abort if reached.
+#include <limits.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <stdlib.h>
+
+#include <hip/hip_runtime.h>
+
+#include "../../fp8_w8a8_linear_amd/csrc/nhm_internal.h"   // the launchers' declarations
+
+namespace nhm {
+[[noreturn]] static void reached(const char* f) {
+    fprintf(stderr, "kernel launcher %s reached from a call that should have failed validation\n", f);
+    abort();
+}
+void launch_quantize(const uint16_t*, int64_t, int64_t, int64_t, const float*, uint8_t*, int64_t, hipStream_t) {
+    reached("launch_quantize");
+}
+void launch_dequant_channel(const uint8_t*, int64_t, int64_t, int64_t, const float*, uint16_t*, int64_t, hipStream_t) {
+    reached("launch_dequant_channel");
+}
+nhm_status launch_gemv(const uint8_t*, int64_t, int, const uint8_t*, const float*, const float*, int64_t, int64_t,
+                       uint16_t*, int64_t, hipStream_t, float*, uint8_t*, int64_t, const float*, uint32_t*, int, int) {
+    reached("launch_gemv");
+}
+size_t gemm_part_bytes(int64_t, int64_t, int64_t) { return 0; }
+nhm_status launch_gemm(const uint8_t*, int64_t, int64_t, const uint8_t*, const float*, const float*, int64_t, int64_t,
+                       uint16_t*, int64_t, hipStream_t, float*, float*, size_t, bool, int) {
+    reached("launch_gemm");
+}
+nhm_status launch_decode_ssm(const DecodeSsmArgs&, int, hipStream_t) { reached("launch_decode_ssm"); }
+void launch_clear(uint32_t*, int, hipStream_t) { reached("launch_clear"); }
+nhm_status launch_gnorm_quant(const GnormArgs&, hipStream_t) { reached("launch_gnorm_quant"); }
+nhm_status launch_prefill_mid(const PrefillArgs&, hipStream_t) { reached("launch_prefill_mid"); }
+nhm_status launch_lora_down(const LoraArgs&, hipStream_t) { reached("launch_lora_down"); }
+nhm_status launch_lora_up(const LoraArgs&, hipStream_t) { reached("launch_lora_up"); }
+size_t beam_ws_bytes(int64_t rows, int64_t, int32_t) { return (size_t)rows * 16; }
+nhm_status launch_beam_select(BeamArgs, void*, hipStream_t) { reached("launch_beam_select"); }
+nhm_status launch_beam_reorder(const ReorderArgs&, int64_t, int32_t, hipStream_t) { reached("launch_beam_reorder"); }
+nhm_status launch_batch_plan(const PlanArgs&, hipStream_t) { reached("launch_batch_plan"); }
+}  // namespace nhm
+
+static int failures = 0;
+#define EXPECT(call, want)                                                                        \
+    do {                                                                                          \
+        const int got_ = (int)(call);                                                             \
+        if (got_ != (int)(want)) {                                                                \
+            fprintf(stderr, "line %d: %s -> %d, expected %d (%s)\n", __LINE__, #call, got_, (int)(want), \
+                    nhm_last_error());                                                            \
+            ++failures;                                                                           \
+        }                                                                                         \
+    } while (0)
+
+template <typename T>
+static T* P(uintptr_t v) { return reinterpret_cast<T*>(v); }
+
+int main() {
+    // adapters
+    const nhm_fp8_weight w = {P<uint8_t>(0x1000), P<float>(0x2000), P<float>(0x3000), 64, 128, 0};
+    const nhm_lora l = {P<uint16_t>(0x4000), P<uint16_t>(0x5000), nullptr, 4, 16};
+    const size_t need = nhm_fp8_linear_lora_workspace_bytes(32, 64, 128, NHM_BF16, 16);
+    EXPECT(need > 0, 1);
+    EXPECT(nhm_fp8_linear_lora_workspace_bytes(INT64_MIN, 64, 128, NHM_BF16, 16), 0);
+    auto lora = [&](int64_t m, const nhm_fp8_weight* wp, const nhm_lora* lp, void* ws, size_t wsb, nhm_dtype t = NHM_BF16) {
+        return nhm_fp8_linear_lora(P<void>(0x10000), t, m, 128, wp, lp, P<int32_t>(0x6000), P<void>(0x20000), NHM_BF16, 64,
+                                   0, ws, wsb, nullptr);
+    };
+    EXPECT(lora(0, &w, &l, nullptr, 0), NHM_OK);
+    EXPECT(lora(32, nullptr, &l, P<void>(0x40000), need), NHM_ERR_NULL);
+    EXPECT(lora(32, &w, nullptr, P<void>(0x40000), need), NHM_ERR_NULL);
+    EXPECT(lora(32, &w, &l, P<void>(0x40000), need - 1), NHM_ERR_WORKSPACE);
+    EXPECT(lora(32, &w, &l, P<void>(0x40010), need), NHM_ERR_ALIGN);
+    EXPECT(lora(-5, &w, &l, P<void>(0x40000), need), NHM_ERR_SHAPE);
+    EXPECT(lora(32, &w, &l, P<void>(0x40000), need, (nhm_dtype)-77), NHM_ERR_UNSUPPORTED);
+    nhm_fp8_weight bad = w;
+    bad.k = -16;
+    EXPECT(lora(32, &bad, &l, P<void>(0x40000), need), NHM_ERR_SHAPE);
+    bad.k = INT64_MAX;
+    EXPECT(lora(32, &bad, &l, P<void>(0x40000), need), NHM_ERR_SHAPE);
+    nhm_lora lb = l;
+    lb.rank = INT_MIN;
+    EXPECT(lora(32, &w, &lb, P<void>(0x40000), need), NHM_ERR_UNSUPPORTED);
+    lb = l;
+    lb.n_adapters = INT_MIN;
+    EXPECT(lora(32, &w, &lb, P<void>(0x40000), need), NHM_ERR_SHAPE);
+
+    // selection
+    auto select = [&](nhm_dtype t, int64_t ld, int64_t G, int32_t K, int64_t V, int32_t n, void* ws, size_t wsb) {
+        return nhm_beam_select(P<void>(0x1000), t, ld, G, K, V, P<float>(0x2000), nullptr, 0, n, P<float>(0x3000),
+                               P<int32_t>(0x4000), P<int32_t>(0x5000), ws, wsb, nullptr);
+    };
+    EXPECT(nhm_beam_select_workspace_bytes(2, 4, 1000, 8) > 0, 1);
+    EXPECT(nhm_beam_select_workspace_bytes(INT64_MAX, 4, 1000, 8), 0);
+    EXPECT(nhm_beam_select_workspace_bytes(2, 4, INT64_MAX, 8), 0);
+    EXPECT(select(NHM_F32, 1000, 0, 4, 1000, 8, nullptr, 0), NHM_OK);
+    EXPECT(select(NHM_F32, INT64_MAX, 2, 4, INT64_MAX, 8, P<void>(0x40000), SIZE_MAX), NHM_ERR_UNSUPPORTED);
+    EXPECT(select(NHM_F32, 1000, INT64_MAX, 4, 1000, 8, P<void>(0x40000), SIZE_MAX), NHM_ERR_UNSUPPORTED);
+    EXPECT(select(NHM_F32, 1000, 2, INT_MIN, 1000, 8, P<void>(0x40000), SIZE_MAX), NHM_ERR_SHAPE);
+    EXPECT(select(NHM_F32, 1000, 2, 4, 1000, 8, P<void>(0x40000), 1), NHM_ERR_WORKSPACE);
+    EXPECT(select((nhm_dtype)INT_MAX, 1000, 2, 4, 1000, 8, P<void>(0x40000), SIZE_MAX), NHM_ERR_UNSUPPORTED);
+
+    // reorder
+    nhm_geometry g = {2688, 64, 64, 128, 8, 4, 1e-5f};
+    nhm_state_pool pools[65];
+    for (auto& p : pools) p = nhm_state_pool{P<void>(0x100000), P<uint16_t>(0x200000)};
+    auto reorder = [&](int64_t G, int32_t K, int32_t layers, int32_t* out, int32_t S = 16) {
+        return nhm_beam_reorder(&g, P<int32_t>(0x1000), P<int32_t>(0x2000), G, K, pools, layers, NHM_F32, S, out, nullptr);
+    };
+    EXPECT(reorder(0, 4, 2, P<int32_t>(0x3000)), NHM_OK);
+    EXPECT(reorder(2, 4, 65, P<int32_t>(0x3000)), NHM_ERR_UNSUPPORTED);
+    EXPECT(reorder(INT64_MAX, 4, 2, P<int32_t>(0x3000)), NHM_ERR_UNSUPPORTED);
+    EXPECT(reorder(2, 4, INT_MIN, P<int32_t>(0x3000)), NHM_ERR_SHAPE);
+    EXPECT(reorder(2, 4, 2, P<int32_t>(0x201c)), NHM_ERR_UNSUPPORTED);
+    EXPECT(reorder(2, 4, 2, P<int32_t>(0x3000), 0), NHM_ERR_SHAPE);
+    pools[63].conv = nullptr;
+    EXPECT(reorder(2, 4, 64, P<int32_t>(0x3000)), NHM_ERR_NULL);
+
+    // plan
+    EXPECT(nhm_batch_plan(nullptr, nullptr, nullptr, 4, 10, P<int32_t>(0x1000), P<int32_t>(0x2000), nullptr, nullptr, nullptr,
+                          nullptr), NHM_ERR_NULL);
+    EXPECT(nhm_batch_plan(P<int32_t>(0x1000), nullptr, nullptr, INT_MAX, 10, P<int32_t>(0x2000), P<int32_t>(0x3000), nullptr,
+                          nullptr, nullptr, nullptr), NHM_ERR_UNSUPPORTED);
+    EXPECT(nhm_batch_plan(P<int32_t>(0x1000), nullptr, nullptr, 4, INT64_MIN, P<int32_t>(0x2000), P<int32_t>(0x3000), nullptr,
+                          nullptr, nullptr, nullptr), NHM_ERR_SHAPE);
+    if (failures) return 1;
+    printf("serving validation ok\n");
+    return 0;
+}
