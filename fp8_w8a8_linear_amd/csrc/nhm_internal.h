@@ -208,8 +208,11 @@ struct BeamArgs {
     float* scores;                 // [n_groups, n_cand]
     int32_t* parents;
     int32_t* tokens;
-    float* row_top;                // workspace: each row's largest logit
-    double* row_log;               // and log(sum exp(x - top))
+    // workspace: per strip (a run of a row) its n_cand best entries, sum of exp(x - top) and top
+    uint64_t* strip_keys;          // [rows, n_strips, n_cand]
+    double* strip_sum;             // [rows, n_strips]
+    float* strip_top;
+    int32_t n_strips, strip_pieces;
 };
 size_t beam_ws_bytes(int64_t rows, int64_t vocab, int32_t n_cand);
 nhm_status launch_beam_select(BeamArgs g, void* ws, hipStream_t st);
