@@ -26,60 +26,97 @@ namespace nhm {
 // x as the selection reads it: NaN counts as -inf.
 __device__ __forceinline__ float clean_logit(float x) { return x == x ? x : -INFINITY; }
 
-template <typename K>
-__device__ __forceinline__ K lane_xor(const K& v, int mask);
-template <typename K>
-__device__ __forceinline__ K lane_get(const K& v, int src);
+// The value of lane ^ M, by lane moves in the VALU (an LDS permute takes a round trip per step):
+// within quads, then mirrored halves of a row of 16 (xor 7, undone by xor 3), a rotation by 8, and
+// the swaps of rows and of halves of the wave.
+template <int M>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+    if constexpr (M == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);
+    if constexpr (M == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);
+    if constexpr (M == 4) {
+        const uint32_t m = __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);
+        return __builtin_amdgcn_update_dpp(0, m, 0x1B, 0xF, 0xF, true);
+    }
+    if constexpr (M == 8) return __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, true);
+    if constexpr (M == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);   // even rows twice, odd rows twice
+        return threadIdx.x & 16 ? r[0] : r[1];
+    }
+    if constexpr (M == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? r[0] : r[1];
+    }
+}
+// The value of lane 63 - lane.
+__device__ __forceinline__ uint32_t lane_flip(uint32_t v) {
+    return lane_xor<32>(lane_xor<16>(__builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true)));   // row_mirror
+}
+__device__ __forceinline__ float wave_max(float v) {
+    auto step = [&](uint32_t o) { v = fmaxf(v, __uint_as_float(o)); };
+    step(lane_xor<1>(__float_as_uint(v)));
+    step(lane_xor<2>(__float_as_uint(v)));
+    step(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x141, 0xF, 0xF, true));
+    step(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x140, 0xF, 0xF, true));
+    step(lane_xor<16>(__float_as_uint(v)));
+    step(lane_xor<32>(__float_as_uint(v)));
+    return v;
+}
+__device__ __forceinline__ uint32_t take(uint32_t v, int src) { return (uint32_t)__builtin_amdgcn_readlane((int)v, src); }
 
 // Entries of the lists. Strips: ordered logit bits over the complement of the index (larger is
-// better; 0: none). Groups: score, then flat index.
-typedef uint64_t StripKey;
-template <>
-__device__ __forceinline__ StripKey lane_xor(const StripKey& v, int mask) {
-    return (uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), mask) << 32 | (uint32_t)__shfl_xor((int)(uint32_t)v, mask);
-}
-template <>
-__device__ __forceinline__ StripKey lane_get(const StripKey& v, int src) {
-    return (uint64_t)(uint32_t)__shfl((int)(v >> 32), src) << 32 | (uint32_t)__shfl((int)(uint32_t)v, src);
-}
-__device__ __forceinline__ bool better(const StripKey& a, const StripKey& b) { return a > b; }
+// better; 0: none). Groups: score, then flat index. each() applies a lane move to every word.
+struct StripKey {
+    uint64_t v;
+    template <typename F>
+    __device__ __forceinline__ StripKey each(F f) const {
+        return StripKey{(uint64_t)f((uint32_t)(v >> 32)) << 32 | f((uint32_t)v)};
+    }
+};
+__device__ __forceinline__ bool better(const StripKey& a, const StripKey& b) { return a.v > b.v; }
 
-struct GroupKey { double score; uint32_t flat; };
-template <>
-__device__ __forceinline__ GroupKey lane_xor(const GroupKey& v, int mask) {
-    return GroupKey{__shfl_xor(v.score, mask), (uint32_t)__shfl_xor((int)v.flat, mask)};
-}
-template <>
-__device__ __forceinline__ GroupKey lane_get(const GroupKey& v, int src) {
-    return GroupKey{__shfl(v.score, src), (uint32_t)__shfl((int)v.flat, src)};
-}
+struct GroupKey {
+    double score;
+    uint32_t flat;
+    template <typename F>
+    __device__ __forceinline__ GroupKey each(F f) const {
+        const uint64_t u = __builtin_bit_cast(uint64_t, score);
+        return GroupKey{__builtin_bit_cast(double, (uint64_t)f((uint32_t)(u >> 32)) << 32 | f((uint32_t)u)), f(flat)};
+    }
+};
 __device__ __forceinline__ bool better(const GroupKey& a, const GroupKey& b) {
     return a.score > b.score || (a.score == b.score && a.flat < b.flat);
 }
 
+// One exchange over lanes J apart; lanes with a clear bit K of their number end with the better one
+// in the lower lane.
+template <int K, int J, typename T>
+__device__ __forceinline__ void exchange(T& v, int lane) {
+    const T o = v.each([](uint32_t w) { return lane_xor<J>(w); });
+    const bool want = ((lane & J) == 0) == ((lane & K) == 0);
+    if (want == better(o, v)) v = o;
+}
 // The wave's 64 entries sorted, best in lane 0 (bitonic).
-template <typename K>
-__device__ __forceinline__ void sort64(K& v, int lane) {
-#pragma unroll
-    for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            const K o = lane_xor(v, j);
-            const bool want = ((lane & j) == 0) == ((lane & k) == 0);   // this lane keeps the better one
-            if (want == better(o, v)) v = o;
-        }
+template <int K, int J, typename T>
+__device__ __forceinline__ void halve(T& v, int lane) {
+    exchange<K, J>(v, lane);
+    if constexpr (J > 1) halve<K, J / 2>(v, lane);
+}
+template <typename T>
+__device__ __forceinline__ void sort64(T& v, int lane) {
+    halve<2, 1>(v, lane);
+    halve<4, 2>(v, lane);
+    halve<8, 4>(v, lane);
+    halve<16, 8>(v, lane);
+    halve<32, 16>(v, lane);
+    halve<64, 32>(v, lane);
 }
 // The 64 best of two sorted lists, sorted: the better of entry i and entry 63 - i of the other
 // list are those 64, in an order that halves into place.
-template <typename K>
-__device__ __forceinline__ void merge64(K& list, const K& sorted, int lane) {
-    const K o = lane_get(sorted, 63 - lane);
+template <typename T>
+__device__ __forceinline__ void merge64(T& list, const T& sorted, int lane) {
+    const T o = sorted.each([](uint32_t w) { return lane_flip(w); });
     if (better(o, list)) list = o;
-#pragma unroll
-    for (int j = 32; j > 0; j >>= 1) {
-        const K p = lane_xor(list, j);
-        if (((lane & j) == 0) == better(p, list)) list = p;
-    }
+    halve<64, 32>(list, lane);
 }
 
 // Between a wave's LDS writes and its reads of other lanes' entries: LDS serves a wave's accesses
@@ -148,8 +185,25 @@ struct Piece {
     }
 };
 
+// x[i] of an index that differs by lane: a tree of bitwise selects on the index's bits (selects of
+// array elements become a dynamic index, through scratch memory).
+__device__ __forceinline__ uint32_t bit_select(int take_b, uint32_t a, uint32_t b) {
+    const uint32_t m = (uint32_t)-take_b;
+    return (b & m) | (a & ~m);
+}
+__device__ __forceinline__ float pick32(const float (&x)[32], int i) {
+    uint32_t a[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a[j] = bit_select(i & 1, __float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1]));
+#pragma unroll
+    for (int n = 8, sh = 1; n > 0; n >>= 1, ++sh)
+#pragma unroll
+        for (int j = 0; j < n; ++j) a[j] = bit_select((i >> sh) & 1, a[2 * j], a[2 * j + 1]);
+    return __uint_as_float(a[0]);
+}
+
 template <bool F32>
-__global__ __launch_bounds__(kStripWaves * 64) void beam_strip_kernel(const BeamArgs g) {
+__global__ __launch_bounds__(kStripWaves * 64, 4) void beam_strip_kernel(const BeamArgs g) {
     __shared__ StripKey s_new[kStripWaves][128];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t id = (int64_t)blockIdx.x * kStripWaves + wave;
@@ -161,19 +215,19 @@ __global__ __launch_bounds__(kStripWaves * 64) void beam_strip_kernel(const Beam
     const char* const base = (F32 ? reinterpret_cast<const char*>(g.logits_f32)
                                   : reinterpret_cast<const char*>(g.logits_bf16)) + row * g.ld * kSize;
 
-    StripKey list = 0;              // lane i: the strip's i-th best so far
-    float last = -INFINITY;         // the n_cand-th best's logit and index (none yet)
-    uint32_t last_at = 0;
+    StripKey list{0};               // lane i: the strip's i-th best so far
+    float last = -INFINITY;         // what a logit has to beat: a bar that n_cand logits reach (-inf: none
+    uint32_t last_at = 0xffffffffu; // yet), and the index below which an equal one still does
     int pending = 0;                // entries waiting in LDS
     StripKey* const buf = s_new[wave];
     float top = -INFINITY;
     double sum = 0.0;               // this lane's sum of exp(x - top)
     auto flush = [&](int n) {       // the first n (<= 64) waiting entries into the list
         wave_lds_order();
-        StripKey k = lane < n ? buf[lane] : 0;
+        StripKey k{lane < n ? buf[lane].v : 0};
         sort64(k, lane);
         merge64(list, k, lane);
-        const StripKey t = lane_get(list, g.n_cand - 1);
+        const uint64_t t = (uint64_t)take((uint32_t)(list.v >> 32), g.n_cand - 1) << 32 | take((uint32_t)list.v, g.n_cand - 1);
         if (t != 0) {
             last = unordered((uint32_t)(t >> 32));
             last_at = ~(uint32_t)t;
@@ -192,9 +246,7 @@ __global__ __launch_bounds__(kStripWaves * 64) void beam_strip_kernel(const Beam
             x[i] = cur.get(i);
             mx = fmaxf(mx, x[i]);
         }
-        float piece_top = mx;
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) piece_top = fmaxf(piece_top, __shfl_xor(piece_top, d));
+        const float piece_top = wave_max(mx);
         if (piece_top > -INFINITY) {
             if (piece_top > top) {
                 sum *= (double)__expf(top - piece_top);      // 0 from -inf
@@ -210,34 +262,24 @@ __global__ __launch_bounds__(kStripWaves * 64) void beam_strip_kernel(const Beam
             }
             sum += (double)part;
 
-            float least = last;      // entries below it cannot be among the n_cand best
-            if (last == -INFINITY) {
-                StripKey k = mx > -INFINITY ? (uint64_t)ordered(mx) << 32 : 0;
+            if (last == -INFINITY) { // the bar before the first n_cand entries: as many lanes' maxima reach it
+                StripKey k{mx > -INFINITY ? (uint64_t)ordered(mx) << 32 : 0};
                 sort64(k, lane);
-                k = lane_get(k, g.n_cand - 1);
-                if (k != 0) least = unordered((uint32_t)(k >> 32));
+                const uint32_t t = take((uint32_t)(k.v >> 32), g.n_cand - 1);
+                if (t != 0) last = unordered(t);
             }
-            if (__ballot(mx >= least && mx > -INFINITY)) {
+            if (__ballot(mx >= last && mx > -INFINITY)) {
                 uint32_t hits = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) hits |= (x[i] >= least && x[i] > -INFINITY ? 1u : 0u) << i;
-                while (__ballot(hits != 0)) {
-                    // each lane's next one, read again (an index into registers would have to be a constant)
-                    bool in = hits != 0;
-                    StripKey k = 0;
-                    if (in) {
-                        const int i = __ffs((int)hits) - 1;
-                        hits &= hits - 1;
-                        const int64_t pos = p + ((i / E) * 64 + lane) * E + i % E;
-                        const char* at = base + pos * kSize;
-                        const float v = clean_logit(F32 ? *reinterpret_cast<const float*>(at)
-                                                        : bf16_to_f32(*reinterpret_cast<const uint16_t*>(at)));
-                        const uint32_t idx = (uint32_t)pos;
-                        in = v > last || (v == last && idx < last_at);
-                        k = (uint64_t)ordered(v) << 32 | (uint32_t)~idx;
-                    }
+                for (int i = 0; i < 32; ++i) hits |= (x[i] >= last && x[i] > -INFINITY ? 1u : 0u) << i;
+                while (__ballot(hits != 0)) {                // each lane's next one
+                    const int i = hits != 0 ? __ffs((int)hits) - 1 : 0;
+                    const float v = pick32(x, i);
+                    const uint32_t idx = (uint32_t)(p + ((i / E) * 64 + lane) * E + i % E);
+                    const bool in = hits != 0 && (v > last || (v == last && idx < last_at));
+                    hits &= hits - 1;
                     const uint64_t m = __ballot(in);
-                    if (in) buf[pending + lanes_below(m)] = k;
+                    if (in) buf[pending + lanes_below(m)].v = (uint64_t)ordered(v) << 32 | (uint32_t)~idx;
                     pending += __popcll(m);
                     if (pending >= 64) {
                         flush(64);
@@ -253,17 +295,18 @@ __global__ __launch_bounds__(kStripWaves * 64) void beam_strip_kernel(const Beam
     if (pending > 0) flush(pending);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-    if (lane < g.n_cand) g.strip_keys[id * g.n_cand + lane] = list;
+    if (lane < g.n_cand) g.strip_keys[id * g.n_cand + lane] = list.v;
     if (lane == 0) {
         g.strip_top[id] = top;
         g.strip_sum[id] = sum;
     }
 }
 
-// One workgroup per group: each row's lse from its strips, then the best continuations. The strips'
-// lists are sorted, so they are walked by place: first every strip's best, then every strip's
-// second best, until at some place none of them beats the list's last used entry.
-constexpr int kPickWaves = 4;
+// One workgroup per group: each row's lse from its strips, then the best continuations. Each lane
+// takes a strip's sorted list, kPlaces entries at a time. The strips' best entries make the first
+// list; of the others only those that beat its last used entry are merged in, and once none of
+// a strip's last entries read does, the rest of the lists is left.
+constexpr int kPickWaves = 8, kPlaces = 8;
 
 __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamArgs g) {
     __shared__ double s_lse[32];                    // each beam's log(sum exp(x - top)) (finished: not used)
@@ -272,16 +315,26 @@ __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamAr
     __shared__ GroupKey s_list[kPickWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row0 = (int64_t)blockIdx.x * g.n_beams;
-    const int S = g.n_strips, K = g.n_beams;
+    const int S = g.n_strips, K = g.n_beams, all = K * S;
+    // entries of places c .. c + kPlaces - 1 of strip i of the group (0: none)
+    auto load = [&](int i, int c, uint64_t (&e)[kPlaces]) {
+        const bool on = i < all && !(g.finished && g.finished[row0 + i / S] != 0);
+        const uint64_t* src = g.strip_keys + (row0 * S + i) * g.n_cand + c;
+#pragma unroll
+        for (int j = 0; j < kPlaces; ++j) e[j] = on && c + j < g.n_cand ? src[j] : 0;
+    };
+    uint64_t e[kPlaces];
+    load(wave * 64 + lane, 0, e);                   // in flight while the sums are joined
     for (int b = wave; b < K; b += kPickWaves) {
         if (g.finished && g.finished[row0 + b] != 0) continue;
         const int64_t id0 = (row0 + b) * S;
-        float top = -INFINITY;
-        for (int s = lane; s < S; s += 64) top = fmaxf(top, g.strip_top[id0 + s]);
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-        double sum = 0.0;
-        for (int s = lane; s < S; s += 64) {
+        float t0 = lane < S ? g.strip_top[id0 + lane] : -INFINITY;
+        const double s0 = lane < S ? g.strip_sum[id0 + lane] : 0.0;
+        float top = t0;
+        for (int s = lane + 64; s < S; s += 64) top = fmaxf(top, g.strip_top[id0 + s]);
+        top = wave_max(top);
+        double sum = t0 > -INFINITY ? s0 * (t0 == top ? 1.0 : exp((double)t0 - (double)top)) : 0.0;
+        for (int s = lane + 64; s < S; s += 64) {
             const float t = g.strip_top[id0 + s];
             if (t > -INFINITY) sum += g.strip_sum[id0 + s] * (t == top ? 1.0 : exp((double)t - (double)top));
         }
@@ -294,69 +347,68 @@ __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamAr
     }
     __syncthreads();
 
-    GroupKey list{-INFINITY, 0xffffffffu};
-    GroupKey last{-INFINITY, 0xffffffffu};
+    const GroupKey none{-INFINITY, 0xffffffffu};
+    GroupKey list = none, last = none;
     int pending = 0;
     GroupKey* const buf = s_new[wave];
     auto flush = [&](int n) {
         wave_lds_order();
-        GroupKey k = lane < n ? buf[lane] : GroupKey{-INFINITY, 0xffffffffu};
+        GroupKey k = lane < n ? buf[lane] : none;
         sort64(k, lane);
         merge64(list, k, lane);
-        last = lane_get(list, g.n_cand - 1);
+        last = list.each([&](uint32_t w) { return (uint32_t)__shfl((int)w, g.n_cand - 1); });
     };
-    const int all = K * S;
-    for (int place = 0; place < g.n_cand; ++place) {
-        bool any = false;
-        for (int i0 = wave * 64; i0 < all; i0 += kPickWaves * 64) {
-            const int i = i0 + lane;
-            GroupKey k{-INFINITY, 0xffffffffu};
-            if (i < all) {
-                const int b = i / S, s = i - b * S;
-                if (g.finished && g.finished[row0 + b] != 0) {
-                    if (s == 0 && place == 0) k = GroupKey{(double)g.cum[row0 + b], (uint32_t)(b * g.vocab + g.eos)};
-                } else {
-                    const StripKey e = g.strip_keys[((row0 + b) * S + s) * g.n_cand + place];
-                    if (e != 0) {
-                        // x - top first: +inf entries score cum - log(their number). cum + (x - top) is
-                        // exact in f64 for f32 values within 29 bits of each other, so equal rows
-                        // whose scores tie do so bit for bit, whatever lse's last bits are
-                        const float x = unordered((uint32_t)(e >> 32)), top = s_top[b];
-                        const double d = x == top ? 0.0 : (double)x - (double)top;
-                        k = GroupKey{((double)g.cum[row0 + b] + d) - s_lse[b], (uint32_t)(b * g.vocab + (uint32_t)~(uint32_t)e)};
-                    }
+    for (int i0 = wave * 64; i0 < all; i0 += kPickWaves * 64) {
+        const int i = i0 + lane, b = i < all ? i / S : 0;
+        const double cum = g.cum[row0 + b];
+        const float top = s_top[b];
+        const double lse = s_lse[b];
+        const bool fin = g.finished && g.finished[row0 + b] != 0;
+        const uint32_t flat0 = (uint32_t)(b * g.vocab);
+        for (int c = 0; c < g.n_cand; c += kPlaces) {
+            if (i0 != wave * 64 || c != 0) load(i, c, e);
+            bool more = false;
+#pragma unroll
+            for (int j = 0; j < kPlaces; ++j) {
+                GroupKey k = none;
+                if (e[j] != 0) {
+                    // x - top first: +inf entries score cum - log(their number). cum + (x - top) is
+                    // exact in f64 for f32 values within 29 bits of each other, so equal rows
+                    // whose scores tie do so bit for bit, whatever lse's last bits are
+                    const float x = unordered((uint32_t)(e[j] >> 32));
+                    const double d = x == top ? 0.0 : (double)x - (double)top;
+                    k = GroupKey{(cum + d) - lse, flat0 + (uint32_t)~(uint32_t)e[j]};
+                } else if (fin && c + j == 0 && i < all && i == b * S) {
+                    k = GroupKey{cum, flat0 + (uint32_t)g.eos};      // a finished beam's one continuation
+                }
+                const bool in = k.score > -INFINITY && better(k, last);
+                const uint64_t m = __ballot(in);
+                if (j == kPlaces - 1) more = m != 0;
+                if (m == 0) continue;
+                if (in) buf[pending + lanes_below(m)] = k;
+                pending += __popcll(m);
+                if (pending >= 64 || (c == 0 && j == 0)) {           // the strips' best at once: the first bar
+                    flush(pending < 64 ? pending : 64);
+                    pending = pending < 64 ? 0 : pending - 64;
+                    if (lane < pending) buf[lane] = buf[64 + lane];
+                    wave_lds_order();
                 }
             }
-            const bool in = k.score > -INFINITY && better(k, last);
-            const uint64_t m = __ballot(in);
-            if (m == 0) continue;
-            any = true;
-            if (in) buf[pending + lanes_below(m)] = k;
-            pending += __popcll(m);
-            if (pending >= 64) {
-                flush(64);
-                pending -= 64;
-                if (lane < pending) buf[lane] = buf[64 + lane];
-                wave_lds_order();
-            }
-        }
-        if (!any) break;
-        if (pending > 0) {
-            flush(pending);
-            pending = 0;
+            if (!more) break;        // the lists are sorted: what follows is no better
         }
     }
-    s_list[wave][lane] = list;
-    __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int w = 1; w < kPickWaves; ++w) merge64(list, s_list[w][lane], lane);
-    if (lane < g.n_cand) {
+    if (pending > 0) flush(pending);
+    for (int half = kPickWaves / 2; half > 0; half >>= 1) {
+        if (wave >= half && wave < 2 * half) s_list[wave][lane] = list;
+        __syncthreads();
+        if (wave < half) merge64(list, s_list[wave + half][lane], lane);
+    }
+    if (wave == 0 && lane < g.n_cand) {
         const int64_t o = (int64_t)blockIdx.x * g.n_cand + lane;
-        const bool none = list.flat == 0xffffffffu;
+        const bool empty = list.flat == 0xffffffffu;
         g.scores[o] = (float)list.score;
-        g.parents[o] = none ? -1 : (int32_t)(list.flat / (uint32_t)g.vocab);
-        g.tokens[o] = none ? -1 : (int32_t)(list.flat % (uint32_t)g.vocab);
+        g.parents[o] = empty ? -1 : (int32_t)(list.flat / (uint32_t)g.vocab);
+        g.tokens[o] = empty ? -1 : (int32_t)(list.flat % (uint32_t)g.vocab);
     }
 }
 
@@ -377,7 +429,7 @@ static BeamWs beam_ws(int64_t rows, int64_t vocab, int32_t n_cand) {
     const size_t n = (size_t)rows * strips;
     BeamWs w;
     w.keys = 0;
-    w.sum = align_up(n * n_cand * sizeof(StripKey), 256);
+    w.sum = align_up(n * n_cand * sizeof(uint64_t), 256);
     w.top = w.sum + align_up(n * sizeof(double), 256);
     w.total = w.top + align_up(n * sizeof(float), 256);
     return w;
@@ -412,7 +464,8 @@ nhm_status launch_beam_select(BeamArgs g, void* ws, hipStream_t st) {
 // copies one piece of one layer's row for every beam of the group that has a copy to receive.
 
 constexpr int kReorderThreads = 256;
-constexpr int kReorderPiece = 64 * 1024;    // bytes of a row per workgroup
+constexpr int kReorderLoads = 4;                                        // 16-byte loads in flight per thread
+constexpr int kReorderPiece = kReorderThreads * 16 * kReorderLoads;      // bytes of a row per workgroup
 
 __global__ __launch_bounds__(kReorderThreads) void beam_reorder_kernel(const ReorderArgs g) {
     __shared__ int s_src[32], s_dst[32];
@@ -456,12 +509,23 @@ __global__ __launch_bounds__(kReorderThreads) void beam_reorder_kernel(const Reo
     for (int j = 0; j < K; ++j) {
         if (s_src[j] < 0) continue;
         const int64_t src = s_src[j], dst = s_dst[j];
-        for (int64_t b = off + t * 16; b < off + kReorderPiece && b < g.ssm_bytes + g.conv_bytes; b += kReorderThreads * 16) {
-            const bool win = b >= g.ssm_bytes;
-            char* pool = static_cast<char*>(win ? g.pools[blockIdx.z].conv : g.pools[blockIdx.z].ssm);
-            const int64_t row = win ? g.conv_bytes : g.ssm_bytes, at = win ? b - g.ssm_bytes : b;
-            *reinterpret_cast<uint4*>(pool + dst * row + at) = *reinterpret_cast<const uint4*>(pool + src * row + at);
+        uint4 v[kReorderLoads];
+        char* to[kReorderLoads];
+#pragma unroll
+        for (int u = 0; u < kReorderLoads; ++u) {
+            const int64_t b = off + (u * kReorderThreads + t) * 16;
+            to[u] = nullptr;
+            if (b < g.ssm_bytes + g.conv_bytes) {
+                const bool win = b >= g.ssm_bytes;
+                char* pool = static_cast<char*>(win ? g.pools[blockIdx.z].conv : g.pools[blockIdx.z].ssm);
+                const int64_t row = win ? g.conv_bytes : g.ssm_bytes, at = win ? b - g.ssm_bytes : b;
+                v[u] = *reinterpret_cast<const uint4*>(pool + src * row + at);
+                to[u] = pool + dst * row + at;
+            }
         }
+#pragma unroll
+        for (int u = 0; u < kReorderLoads; ++u)
+            if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];
     }
 }
 
