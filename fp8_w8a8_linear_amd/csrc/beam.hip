@@ -480,7 +480,7 @@ __global__ __launch_bounds__(kReorderThreads) void beam_reorder_kernel(const Reo
         // first: no earlier beam continues the same parent; used: some beam continues this one
         bool first = has, used = false;
         for (int j = 0; j < K; ++j) {
-            const int pj = __shfl(has ? par : -1, j);
+            const int pj = __builtin_amdgcn_readlane(has ? par : -1, j);
             if (j < t && has && pj == par) first = false;
             if (pj == t) used = true;
         }
@@ -506,26 +506,29 @@ __global__ __launch_bounds__(kReorderThreads) void beam_reorder_kernel(const Reo
     }
     __syncthreads();
     const int64_t off = (int64_t)blockIdx.x * kReorderPiece;   // within the layer's row: state, then window
+    const int64_t end = g.ssm_bytes + g.conv_bytes;
+    char* const ssm = static_cast<char*>(g.pools[blockIdx.z].ssm);
+    char* const conv = reinterpret_cast<char*>(g.pools[blockIdx.z].conv);
     for (int j = 0; j < K; ++j) {
         if (s_src[j] < 0) continue;
         const int64_t src = s_src[j], dst = s_dst[j];
-        uint4 v[kReorderLoads];
+        // straight-line loads (a piece past the row's end reads its last 16 bytes again), so that
+        // all of them are in flight before the first store waits
+        v4u v[kReorderLoads];
         char* to[kReorderLoads];
 #pragma unroll
         for (int u = 0; u < kReorderLoads; ++u) {
-            const int64_t b = off + (u * kReorderThreads + t) * 16;
-            to[u] = nullptr;
-            if (b < g.ssm_bytes + g.conv_bytes) {
-                const bool win = b >= g.ssm_bytes;
-                char* pool = static_cast<char*>(win ? g.pools[blockIdx.z].conv : g.pools[blockIdx.z].ssm);
-                const int64_t row = win ? g.conv_bytes : g.ssm_bytes, at = win ? b - g.ssm_bytes : b;
-                v[u] = *reinterpret_cast<const uint4*>(pool + src * row + at);
-                to[u] = pool + dst * row + at;
-            }
+            const int64_t b = min(off + (u * kReorderThreads + t) * 16, end - 16);
+            const bool win = b >= g.ssm_bytes;
+            char* const pool = win ? conv : ssm;
+            const int64_t row = win ? g.conv_bytes : g.ssm_bytes, at = win ? b - g.ssm_bytes : b;
+            v[u] = *reinterpret_cast<const v4u*>(pool + src * row + at);
+            to[u] = pool + dst * row + at;
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < kReorderLoads; ++u)
-            if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];
+            if (off + (u * kReorderThreads + t) * 16 < end) *reinterpret_cast<v4u*>(to[u]) = v[u];
     }
 }
 
