@@ -63,6 +63,26 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 __device__ __forceinline__ uint32_t take(uint32_t v, int src) { return (uint32_t)__builtin_amdgcn_readlane((int)v, src); }
 
+// max3: quiet NaN passed over; a signalling one comes out as NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    auto step = [&](auto move) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        v += __builtin_bit_cast(double, (uint64_t)move((uint32_t)(u >> 32)) << 32 | move((uint32_t)u));
+    };
+    step([](uint32_t w) { return lane_xor<1>(w); });
+    step([](uint32_t w) { return lane_xor<2>(w); });
+    step([](uint32_t w) { return lane_xor<4>(w); });
+    step([](uint32_t w) { return lane_xor<8>(w); });
+    step([](uint32_t w) { return lane_xor<16>(w); });
+    step([](uint32_t w) { return lane_xor<32>(w); });
+    return v;
+}
+
 // Entries of the lists. Strips: ordered logit bits over the complement of the index (larger is
 // better; 0: none). Groups: score, then flat index. each() applies a lane move to every word.
 struct StripKey {
@@ -73,6 +93,13 @@ struct StripKey {
     }
 };
 __device__ __forceinline__ bool better(const StripKey& a, const StripKey& b) { return a.v > b.v; }
+
+struct BarKey {      // an ordered logit alone
+    uint32_t v;
+    template <typename F>
+    __device__ __forceinline__ BarKey each(F f) const { return BarKey{f(v)}; }
+};
+__device__ __forceinline__ bool better(const BarKey& a, const BarKey& b) { return a.v > b.v; }
 
 struct GroupKey {
     double score;
@@ -180,8 +207,8 @@ struct Piece {
         const uint4 v = raw[i / E];
         const int j = i % E;
         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        if constexpr (F32) return clean_logit(__uint_as_float(w4[j]));
-        else return clean_logit(bf16_to_f32(j & 1 ? w4[j >> 1] >> 16 : w4[j >> 1] & 0xffffu));
+        if constexpr (F32) return __uint_as_float(w4[j]);
+        else return __uint_as_float(j & 1 ? w4[j >> 1] & 0xffff0000u : w4[j >> 1] << 16);
     }
 };
 
@@ -242,9 +269,26 @@ __global__ __launch_bounds__(kStripWaves * 64, 4) void beam_strip_kernel(const B
         if (p + kPiece < p_end) nxt.load(base, p + kPiece, g.vocab, lane);
         float x[32], mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            x[i] = cur.get(i);
-            mx = fmaxf(mx, x[i]);
+        for (int i = 0; i < 32; ++i) x[i] = cur.get(i);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mx = max3(mx, x[i], x[i + 1]);
+        float part = 0.f;            // 32 terms in f32, the strip's sum in f64
+        auto add_up = [&](float t) {
+            part = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) part += __builtin_amdgcn_exp2f((x[i] - t) * 1.44269504088896341f);
+        };
+        // The maximum passes over quiet NaN and the sum does not: where either is NaN the piece is
+        // cleaned and taken again. Other pieces pay one comparison for it.
+        add_up(fmaxf(top, wave_max(mx)));
+        if (__ballot(part != part || mx != mx)) {
+            mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                x[i] = clean_logit(x[i]);
+                mx = fmaxf(mx, x[i]);
+            }
+            add_up(fmaxf(top, wave_max(mx)));
         }
         const float piece_top = wave_max(mx);
         if (piece_top > -INFINITY) {
@@ -252,32 +296,30 @@ __global__ __launch_bounds__(kStripWaves * 64, 4) void beam_strip_kernel(const B
                 sum *= (double)__expf(top - piece_top);      // 0 from -inf
                 top = piece_top;
             }
-            float part = 0.f;        // 32 terms in f32, the strip's sum in f64
-            if (top < INFINITY) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) part += __builtin_amdgcn_exp2f((x[i] - top) * 1.44269504088896341f);
-            } else {                 // +inf entries share the probability
+            if (top == INFINITY) {   // +inf entries share the probability
+                part = 0.f;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) part += x[i] == INFINITY ? 1.0f : 0.0f;
             }
             sum += (double)part;
 
             if (last == -INFINITY) { // the bar before the first n_cand entries: as many lanes' maxima reach it
-                StripKey k{mx > -INFINITY ? (uint64_t)ordered(mx) << 32 : 0};
+                BarKey k{mx > -INFINITY ? ordered(mx) : 0};
                 sort64(k, lane);
-                const uint32_t t = take((uint32_t)(k.v >> 32), g.n_cand - 1);
+                const uint32_t t = take(k.v, g.n_cand - 1);
                 if (t != 0) last = unordered(t);
             }
-            if (__ballot(mx >= last && mx > -INFINITY)) {
-                uint32_t hits = 0;
+            const float bar = fmaxf(last, -3.402823466e38f);     // -inf never enters
+            if (__ballot(mx >= bar)) {
+                uint32_t hits = 0;                               // element i at bit 31 - i
 #pragma unroll
-                for (int i = 0; i < 32; ++i) hits |= (x[i] >= last && x[i] > -INFINITY ? 1u : 0u) << i;
+                for (int i = 0; i < 32; ++i) hits = hits + hits + (x[i] >= bar ? 1u : 0u);
                 while (__ballot(hits != 0)) {                // each lane's next one
-                    const int i = hits != 0 ? __ffs((int)hits) - 1 : 0;
+                    const int i = hits != 0 ? __clz((int)hits) : 0;
                     const float v = pick32(x, i);
                     const uint32_t idx = (uint32_t)(p + ((i / E) * 64 + lane) * E + i % E);
                     const bool in = hits != 0 && (v > last || (v == last && idx < last_at));
-                    hits &= hits - 1;
+                    hits &= ~(0x80000000u >> i);
                     const uint64_t m = __ballot(in);
                     if (in) buf[pending + lanes_below(m)].v = (uint64_t)ordered(v) << 32 | (uint32_t)~idx;
                     pending += __popcll(m);
@@ -293,8 +335,7 @@ __global__ __launch_bounds__(kStripWaves * 64, 4) void beam_strip_kernel(const B
         cur = nxt;
     }
     if (pending > 0) flush(pending);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    sum = wave_sum_f64(sum);
     if (lane < g.n_cand) g.strip_keys[id * g.n_cand + lane] = list.v;
     if (lane == 0) {
         g.strip_top[id] = top;
@@ -338,8 +379,7 @@ __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamAr
             const float t = g.strip_top[id0 + s];
             if (t > -INFINITY) sum += g.strip_sum[id0 + s] * (t == top ? 1.0 : exp((double)t - (double)top));
         }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+        sum = wave_sum_f64(sum);
         if (lane == 0) {
             s_top[b] = top;
             s_lse[b] = log(sum);
@@ -350,12 +390,15 @@ __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamAr
     const GroupKey none{-INFINITY, 0xffffffffu};
     GroupKey list = none, last = none;
     int pending = 0;
+    bool first = true;
     GroupKey* const buf = s_new[wave];
     auto flush = [&](int n) {
         wave_lds_order();
         GroupKey k = lane < n ? buf[lane] : none;
         sort64(k, lane);
-        merge64(list, k, lane);
+        if (first) list = k;
+        else merge64(list, k, lane);
+        first = false;
         last = list.each([&](uint32_t w) { return (uint32_t)__shfl((int)w, g.n_cand - 1); });
     };
     for (int i0 = wave * 64; i0 < all; i0 += kPickWaves * 64) {
@@ -398,7 +441,10 @@ __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamAr
         }
     }
     if (pending > 0) flush(pending);
-    for (int half = kPickWaves / 2; half > 0; half >>= 1) {
+    // the waves' lists in pairs; waves past the last strip hold none
+    int half = kPickWaves / 2;
+    while (half > 0 && half * 64 >= all) half >>= 1;
+    for (; half > 0; half >>= 1) {
         if (wave >= half && wave < 2 * half) s_list[wave][lane] = list;
         __syncthreads();
         if (wave < half) merge64(list, s_list[wave + half][lane], lane);
