@@ -15,13 +15,15 @@ namespace nhm {
 // largest logits. A second kernel joins each row's strips into its lse and picks each group's best
 // from the strips' lists. The pass is bound by the logits' bytes; 512 rows of 131,072 bf16 logits.
 //
-// A wave's list is sorted, one entry per lane. A logit enters it only if it beats the list's last
-// used entry, so after the first piece of a strip almost every piece is dismissed by one
-// comparison of each lane's maximum; the others collect in LDS until 64 of them (or the strip's
-// end) are sorted and merged in. Before the first piece the n_cand-th largest of the 64 lane maxima
-// stands in for that entry: at least n_cand logits of the piece reach it.
-// Any number of entering logits is handled (ascending rows merge all the time): only speed depends
-// on the data.
+// A lane's share of a 2,048-logit piece is a cell of 32; the pass keeps each cell's maximum in LDS.
+// After a span of 8 pieces the n_cand-th largest of the 64 lanes' maxima is a bar that at least
+// n_cand logits reach, and so (once there are n_cand entries) is the list's last used entry: only
+// cells that reach the bar, about n_cand of 512, are read again, two at a time with a lane per logit.
+// The logits that enter collect in LDS until 64 of them are sorted and merged into the list, which
+// is sorted with one entry per lane. Any number of entering logits is handled: equal and ascending
+// rows cost time, not correctness.
+// An earlier form looked for entering logits in every piece as it passed: 583 vector instructions
+// per piece against about 200, 41 us for those 512 rows.
 
 // x as the selection reads it: NaN counts as -inf.
 __device__ __forceinline__ float clean_logit(float x) { return x == x ? x : -INFINITY; }
@@ -178,10 +180,18 @@ struct __attribute__((packed, aligned(2))) Loose16 { uint32_t w[4]; };
 template <bool F32>
 struct Piece {
     static constexpr int E = F32 ? 4 : 8, NV = 32 / E;
-    uint4 raw[NV];
+    v4u raw[NV];
     __device__ __forceinline__ void load(const char* row, int64_t p0, int64_t vocab, int lane) {
+        if (p0 + kPiece <= vocab) {                          // the same branch for the whole wave
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
+            for (int u = 0; u < NV; ++u) {
+                const Loose16 v = *reinterpret_cast<const Loose16*>(row + (p0 + (u * 64 + lane) * E) * (F32 ? 4 : 2));
+                raw[u] = v4u{v.w[0], v.w[1], v.w[2], v.w[3]};
+            }
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {                       // the row's last piece: its own logits only, element by element
             const int64_t p = p0 + (u * 64 + lane) * E;
             constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;    // -inf
             uint32_t w[4] = {kNone, kNone, kNone, kNone};
@@ -189,7 +199,7 @@ struct Piece {
                 const Loose16 v = *reinterpret_cast<const Loose16*>(row + p * (F32 ? 4 : 2));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = v.w[j];
-            } else if (p < vocab) {                      // the row's last vector: its own elements only
+            } else if (p < vocab) {
 #pragma unroll
                 for (int j = 0; j < E; ++j)
                     if (p + j < vocab) {
@@ -200,38 +210,25 @@ struct Piece {
                         }
                     }
             }
-            raw[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            raw[u] = v4u{w[0], w[1], w[2], w[3]};
         }
     }
     __device__ __forceinline__ float get(int i) const {   // i a constant: element i % E of vector i / E
-        const uint4 v = raw[i / E];
         const int j = i % E;
-        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        if constexpr (F32) return __uint_as_float(w4[j]);
-        else return __uint_as_float(j & 1 ? w4[j >> 1] & 0xffff0000u : w4[j >> 1] << 16);
+        if constexpr (F32) return __uint_as_float(raw[i / E][j]);
+        else return __uint_as_float(j & 1 ? raw[i / E][j >> 1] & 0xffff0000u : raw[i / E][j >> 1] << 16);
     }
 };
 
-// x[i] of an index that differs by lane: a tree of bitwise selects on the index's bits (selects of
-// array elements become a dynamic index, through scratch memory).
-__device__ __forceinline__ uint32_t bit_select(int take_b, uint32_t a, uint32_t b) {
-    const uint32_t m = (uint32_t)-take_b;
-    return (b & m) | (a & ~m);
-}
-__device__ __forceinline__ float pick32(const float (&x)[32], int i) {
-    uint32_t a[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) a[j] = bit_select(i & 1, __float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1]));
-#pragma unroll
-    for (int n = 8, sh = 1; n > 0; n >>= 1, ++sh)
-#pragma unroll
-        for (int j = 0; j < n; ++j) a[j] = bit_select((i >> sh) & 1, a[2 * j], a[2 * j + 1]);
-    return __uint_as_float(a[0]);
-}
+constexpr int kSpan = 8;            // pieces between two looks at the cells' maxima
+constexpr int kCells = 8;           // cells a half-wave reads at once
+constexpr float kLog2e = 1.44269504088896341f;
 
 template <bool F32>
-__global__ __launch_bounds__(kStripWaves * 64, 4) void beam_strip_kernel(const BeamArgs g) {
-    __shared__ StripKey s_new[kStripWaves][128];
+__global__ __launch_bounds__(kStripWaves * 64, F32 ? 3 : 4) void beam_strip_kernel(const BeamArgs g) {
+    __shared__ StripKey s_new[kStripWaves][64 * (kCells + 1)];
+    __shared__ float s_max[kStripWaves][kSpan * 64];         // the cells' maxima
+    __shared__ uint16_t s_cell[kStripWaves][kSpan * 64];     // the cells to read again
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t id = (int64_t)blockIdx.x * kStripWaves + wave;
     const int64_t row = id / g.n_strips;
@@ -247,11 +244,15 @@ __global__ __launch_bounds__(kStripWaves * 64, 4) void beam_strip_kernel(const B
     uint32_t last_at = 0xffffffffu; // yet), and the index below which an equal one still does
     int pending = 0;                // entries waiting in LDS
     StripKey* const buf = s_new[wave];
-    float top = -INFINITY;
-    double sum = 0.0;               // this lane's sum of exp(x - top)
-    auto flush = [&](int n) {       // the first n (<= 64) waiting entries into the list
+    float* const cmax = s_max[wave];
+    uint16_t* const cells = s_cell[wave];
+    float top = -INFINITY;          // this lane's largest logit and sum of exp(x - top)
+    double sum = 0.0;
+    auto flush = [&](int n) {       // the last n (<= 64) waiting entries into the list
         wave_lds_order();
-        StripKey k{lane < n ? buf[lane].v : 0};
+        pending -= n;
+        StripKey k{lane < n ? buf[pending + lane].v : 0};
+        wave_lds_order();
         sort64(k, lane);
         merge64(list, k, lane);
         const uint64_t t = (uint64_t)take((uint32_t)(list.v >> 32), g.n_cand - 1) << 32 | take((uint32_t)list.v, g.n_cand - 1);
@@ -263,82 +264,114 @@ __global__ __launch_bounds__(kStripWaves * 64, 4) void beam_strip_kernel(const B
 
     const int64_t p_beg = (int64_t)strip * g.strip_pieces * kPiece;
     const int64_t p_end = min(p_beg + (int64_t)g.strip_pieces * kPiece, g.vocab);
-    Piece<F32> cur, nxt;
+    Piece<F32> cur;
     cur.load(base, p_beg, g.vocab, lane);
-    for (int64_t p = p_beg; p < p_end; p += kPiece) {
-        if (p + kPiece < p_end) nxt.load(base, p + kPiece, g.vocab, lane);
-        float x[32], mx = -INFINITY;
+    for (int64_t span = p_beg; span < p_end; span += kSpan * kPiece) {
+        const int pieces = (int)min((int64_t)kSpan, (p_end - span + kPiece - 1) / kPiece);
+        float span_max = -INFINITY;
+        for (int q = 0; q < pieces; ++q) {
+            const int64_t p = span + (int64_t)q * kPiece;
+            float x[32], mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = cur.get(i);
+            for (int i = 0; i < 32; ++i) x[i] = cur.get(i);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) mx = max3(mx, x[i], x[i + 1]);
-        float part = 0.f;            // 32 terms in f32, the strip's sum in f64
-        auto add_up = [&](float t) {
-            part = 0.f;
+            for (int i = 0; i < 32; ++i) asm volatile("" : "+v"(x[i]));
+            // the next piece on its way while this one, now in x, is worked on (issued ahead of the
+            // unpacking it was waited for at once, at the join behind its branch)
+            if (p + kPiece < p_end) cur.load(base, p + kPiece, g.vocab, lane);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) part += __builtin_amdgcn_exp2f((x[i] - t) * 1.44269504088896341f);
-        };
-        // The maximum passes over quiet NaN and the sum does not: where either is NaN the piece is
-        // cleaned and taken again. Other pieces pay one comparison for it.
-        add_up(fmaxf(top, wave_max(mx)));
-        if (__ballot(part != part || mx != mx)) {
-            mx = -INFINITY;
+            for (int i = 0; i < 32; i += 2) mx = max3(mx, x[i], x[i + 1]);
+            float now = fmaxf(top, mx);
+            float ref = now > -INFINITY ? now : 0.f;
+            float part = 0.f;        // 32 terms in f32, the strip's sum in f64
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                x[i] = clean_logit(x[i]);
-                mx = fmaxf(mx, x[i]);
+            for (int i = 0; i < 32; i += 8) {                // eight at a time: no sum waits for its exponential
+                float e[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f((x[i + j] - ref) * kLog2e);
+                __builtin_amdgcn_sched_barrier(0);
+                part += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
             }
-            add_up(fmaxf(top, wave_max(mx)));
-        }
-        const float piece_top = wave_max(mx);
-        if (piece_top > -INFINITY) {
-            if (piece_top > top) {
-                sum *= (double)__expf(top - piece_top);      // 0 from -inf
-                top = piece_top;
-            }
-            if (top == INFINITY) {   // +inf entries share the probability
+            // The maximum passes over quiet NaN and the sum does not, and inf - inf is NaN: a piece with
+            // either is cleaned and taken again. Other pieces pay two comparisons for it.
+            if (__ballot(part != part || mx != mx)) {
+                mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    asm volatile("" : "+v"(x[i]));           // not to be done ahead of the branch
+                    x[i] = clean_logit(x[i]);
+                    mx = fmaxf(mx, x[i]);
+                }
+                now = fmaxf(top, mx);
+                ref = now > -INFINITY ? now : 0.f;
                 part = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) part += x[i] == INFINITY ? 1.0f : 0.0f;
+                for (int i = 0; i < 32; ++i)                 // +inf entries share the probability
+                    part += now < INFINITY ? __builtin_amdgcn_exp2f((x[i] - ref) * kLog2e) : x[i] == INFINITY ? 1.f : 0.f;
             }
-            sum += (double)part;
+            const float keep = top == now ? 1.f : __builtin_amdgcn_exp2f((top - ref) * kLog2e);   // 0 from -inf
+            sum = sum * (double)keep + (double)part;
+            top = now;
+            cmax[q * 64 + lane] = mx;
+            span_max = fmaxf(span_max, mx);
+        }
 
-            if (last == -INFINITY) { // the bar before the first n_cand entries: as many lanes' maxima reach it
-                BarKey k{mx > -INFINITY ? ordered(mx) : 0};
-                sort64(k, lane);
-                const uint32_t t = take(k.v, g.n_cand - 1);
-                if (t != 0) last = unordered(t);
-            }
-            const float bar = fmaxf(last, -3.402823466e38f);     // -inf never enters
-            if (__ballot(mx >= bar)) {
-                uint32_t hits = 0;                               // element i at bit 31 - i
+        BarKey k{span_max > -INFINITY ? ordered(span_max) : 0};
+        sort64(k, lane);
+        const uint32_t t = take(k.v, g.n_cand - 1);
+        if (t != 0 && unordered(t) > last) {     // as many lanes' maxima reach it; equal ones still enter
+            last = unordered(t);
+            last_at = 0xffffffffu;
+        }
+        const float bar = fmaxf(last, -3.402823466e38f);     // -inf never enters
+        wave_lds_order();
+        int n_cells = 0;
+        for (int q = 0; q < pieces; ++q) {
+            const bool in = cmax[q * 64 + lane] >= bar;
+            const uint64_t m = __ballot(in);
+            if (in) cells[n_cells + lanes_below(m)] = (uint16_t)(q * 64 + lane);
+            n_cells += __popcll(m);
+        }
+        wave_lds_order();
+        for (int c0 = 0; c0 < n_cells; c0 += 2 * kCells) {
+            float v[kCells];
+            uint32_t idx[kCells];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) hits = hits + hits + (x[i] >= bar ? 1u : 0u);
-                while (__ballot(hits != 0)) {                // each lane's next one
-                    const int i = hits != 0 ? __clz((int)hits) : 0;
-                    const float v = pick32(x, i);
-                    const uint32_t idx = (uint32_t)(p + ((i / E) * 64 + lane) * E + i % E);
-                    const bool in = hits != 0 && (v > last || (v == last && idx < last_at));
-                    hits &= ~(0x80000000u >> i);
-                    const uint64_t m = __ballot(in);
-                    if (in) buf[pending + lanes_below(m)].v = (uint64_t)ordered(v) << 32 | (uint32_t)~idx;
-                    pending += __popcll(m);
-                    if (pending >= 64) {
-                        flush(64);
-                        pending -= 64;
-                        if (lane < pending) buf[lane] = buf[64 + lane];
-                        wave_lds_order();
+            for (int s = 0; s < kCells; ++s) {
+                const int c = c0 + 2 * s + (lane >> 5);
+                v[s] = -INFINITY;
+                idx[s] = 0;
+                if (c < n_cells) {
+                    const int cell = cells[c], i = lane & 31;
+                    const int64_t at0 = span + (int64_t)(cell >> 6) * kPiece + (cell & 63) * E;     // its first logit
+                    const int64_t at = at0 + (i / E) * 64 * E + i % E;
+                    const float cm = cmax[cell];
+                    // a cell that no longer reaches the list is not read
+                    if ((cm > last || (cm == last && (uint32_t)at0 < last_at)) && at < p_end) {
+                        v[s] = F32 ? *reinterpret_cast<const float*>(base + at * 4)
+                                   : bf16_to_f32(*reinterpret_cast<const uint16_t*>(base + at * 2));
+                        idx[s] = (uint32_t)at;
                     }
                 }
             }
+#pragma unroll
+            for (int s = 0; s < kCells; ++s) {
+                const float x = clean_logit(v[s]);
+                const bool in = x > -INFINITY && (x > last || (x == last && idx[s] < last_at));
+                const uint64_t m = __ballot(in);
+                if (in) buf[pending + lanes_below(m)].v = (uint64_t)ordered(x) << 32 | (uint32_t)~idx[s];
+                pending += __popcll(m);
+            }
+            while (pending >= 64) flush(64);
         }
-        cur = nxt;
+        if (pending > 0) flush(pending);
+        wave_lds_order();
     }
-    if (pending > 0) flush(pending);
-    sum = wave_sum_f64(sum);
+    const float all_top = wave_max(top);
+    sum = wave_sum_f64(top == all_top ? sum : sum * (double)__expf(top - all_top));
     if (lane < g.n_cand) g.strip_keys[id * g.n_cand + lane] = list.v;
     if (lane == 0) {
-        g.strip_top[id] = top;
+        g.strip_top[id] = all_top;
         g.strip_sum[id] = sum;
     }
 }
