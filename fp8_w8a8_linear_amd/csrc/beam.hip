@@ -377,9 +377,9 @@ __global__ __launch_bounds__(kStripWaves * 64, F32 ? 3 : 4) void beam_strip_kern
 }
 
 // One workgroup per group: each row's lse from its strips, then the best continuations. Each lane
-// takes a strip's sorted list, kPlaces entries at a time. The strips' best entries make the first
-// list; of the others only those that beat its last used entry are merged in, and once none of
-// a strip's last entries read does, the rest of the lists is left.
+// takes a strip's sorted list, kPlaces entries at a time. The n_cand-th of 64 lists' best entries is a
+// bar for the others; what reaches it collects and is merged as in the strips, and once none of the
+// last entries read does, the rest of the lists is left.
 constexpr int kPickWaves = 8, kPlaces = 8;
 
 __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamArgs g) {
@@ -422,6 +422,7 @@ __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamAr
 
     const GroupKey none{-INFINITY, 0xffffffffu};
     GroupKey list = none, last = none;
+    double bar = -INFINITY;                         // n_cand scores are known to reach it
     int pending = 0;
     bool first = true;
     GroupKey* const buf = s_new[wave];
@@ -457,15 +458,24 @@ __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamAr
                 } else if (fin && c + j == 0 && i < all && i == b * S) {
                     k = GroupKey{cum, flat0 + (uint32_t)g.eos};      // a finished beam's one continuation
                 }
-                const bool in = k.score > -INFINITY && better(k, last);
+                if (c == 0 && j == 0) {
+                    // the n_cand-th of these 64 lists' best, rounded down to f32, is a bar
+                    float f = (float)k.score;
+                    if ((double)f > k.score) f = unordered(ordered(f) - 1);
+                    BarKey h{k.score > -INFINITY ? ordered(f) : 0};
+                    sort64(h, lane);
+                    const uint32_t t = take(h.v, g.n_cand - 1);
+                    if (t != 0) bar = fmax(bar, (double)unordered(t));
+                }
+                const bool in = k.score > -INFINITY && k.score >= bar && better(k, last);
                 const uint64_t m = __ballot(in);
                 if (j == kPlaces - 1) more = m != 0;
                 if (m == 0) continue;
                 if (in) buf[pending + lanes_below(m)] = k;
                 pending += __popcll(m);
-                if (pending >= 64 || (c == 0 && j == 0)) {           // the strips' best at once: the first bar
-                    flush(pending < 64 ? pending : 64);
-                    pending = pending < 64 ? 0 : pending - 64;
+                if (pending >= 64) {
+                    flush(64);
+                    pending -= 64;
                     if (lane < pending) buf[lane] = buf[64 + lane];
                     wave_lds_order();
                 }
