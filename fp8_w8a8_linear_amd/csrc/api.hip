@@ -26,7 +26,7 @@ static const char* const kKernNames[(int)Kern::kCount] = {
     "quant_vec8", "quant_scalar", "dequant_channel", "gemv", "gemm_ring192x128", "gemm_ring192x128_exact",
     "gemm_ring256x128", "gemm_ring256x128_exact", "gemm_ring256x256", "gemm_ring256x256_exact", "gemm_panel64x128",
     "gemm_panel64x128_exact", "gemm_tile128", "gemm_tile128_exact", "gemm_splitk_reduce", "decode_ssm",
-    "gnorm_quant", "clear", "conv_fwd", "ssd_state", "ssd_pass", "ssd_out", "lora_down", "lora_up", "beam_rows",
+    "gnorm_quant", "clear", "conv_fwd", "ssd_state", "ssd_pass", "ssd_out", "lora_down", "beam_rows",
     "beam_pick", "beam_reorder", "batch_plan"};
 static std::atomic<uint64_t> g_launches[(int)Kern::kCount];
 static std::atomic<uint64_t> g_rows[(int)Kern::kCount];
@@ -101,16 +101,9 @@ static nhm_status check_weight(const nhm_fp8_weight* w, int64_t n, int64_t k, co
     return NHM_OK;
 }
 
-// Index step of the weight scale: per channel (w_scale[n]) or one scale for every channel.
-static int ws_step(const nhm_fp8_weight& w) { return w.w_scale_per_tensor ? 0 : 1; }
-
 // ---------------------------------------------------------------- workspace layouts
 
 // bytes of the e4m3 copy of a bf16 activation (the only workspace nhm_fp8_linear needs)
-// The weight-streaming GEMV serves m <= 16 (k up to 16384, weights under 2 GiB: its buffer
-// descriptors take 32-bit offsets); the tiled GEMM the rest.
-static bool use_gemv(int64_t m, int64_t n, int64_t k) { return m <= 16 && k <= 16384 && n * k < (int64_t(1) << 31); }
-
 // Every kernel addresses its operands through buffer descriptors with 32-bit offsets: an
 // operand of 2 GiB or more is refused on the host before anything is enqueued.
 static nhm_status check_offsets(int64_t m, int64_t lda, int64_t n, int64_t k, const char* what) {

@@ -32,6 +32,7 @@
 //    double-buffered LDS, four waves of 64 x 64.
 #include <stdint.h>
 
+#include "lora_device.h"
 #include "nhm_device.h"
 #include "nhm_internal.h"
 
@@ -49,6 +50,7 @@ struct GemmArgs {
     float* part = nullptr;
     int ws_step = 1;    // weight scale index step: 1 per channel, 0 per tensor
     int panel_rows = 0; // panel kernel: weight rows per panel (0: all of its waves' rows)
+    LoraEpi lora;       // the kernels with adapters (kLora) only
 };
 
 // Row r of a 128-byte-wide LDS tile holds its 16-byte chunk c at slot c ^ (r & 7):
@@ -119,7 +121,7 @@ __device__ __forceinline__ uint4 bload(const __amdgpu_buffer_rsrc_t& r, uint32_t
 constexpr uint32_t kOutOfRange = 0x80000000u;   // past every buffer range used here (< 2^31 bytes)
 
 // D: weight k-steps in flight per wave (and activation tiles in registers).
-template <int BM, int WN, bool kExact, int D>
+template <int BM, int WN, bool kExact, int D, bool kLora>
 __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     constexpr int BN = 4 * WN, TN = WN / 16, TM = BM / 16;
     constexpr int U = D % 2 == 0 ? D : 2 * D;   // loop unroll: step kt's registers are slot kt % D
@@ -236,12 +238,21 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     }
 
     const float sa = *g.a_scale;
+    if constexpr (kLora) {   // scale first, then add the adapters' part (feature rows past the panel are not stored)
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] *= sa * wsc[i][r];
+        lora_add16(acc, g.lora, m0, g.m, nw0, g.n, lane);
+    }
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
         const bool full = g.vec_out && m0 + BM <= g.m && nw0 + 16 * (i + 1) <= pend;
         float sc[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sc[r] = sa * wsc[i][r];
+        for (int r = 0; r < 4; ++r) sc[r] = kLora ? 1.0f : sa * wsc[i][r];
 #pragma unroll
         for (int j = 0; j < TM; ++j)
             if (g.out_f32)
@@ -279,7 +290,7 @@ __device__ __forceinline__ v8i lds_operand(const uint8_t* s, int row, int q) {
     return cat8(*reinterpret_cast<const uint4*>(s + swz(row, 2 * q)), *reinterpret_cast<const uint4*>(s + swz(row, 2 * q + 1)));
 }
 
-template <bool kExact>
+template <bool kExact, bool kLora>
 __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t sW[2][kTile * kTile];
     __shared__ __attribute__((aligned(16))) uint8_t sA[2][kTile * kTile];
@@ -337,11 +348,20 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
 
     const float sa = *g.a_scale;
     const bool full = g.vec_out && m0 + wm * 64 + 64 <= g.m && n0 + wn * 64 + 64 <= g.n;
+    if constexpr (kLora) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] *= sa * wsc[i][r];
+        lora_add16(acc, g.lora, m0 + wm * 64, g.m, n0 + wn * 64, g.n, lane);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float sc[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sc[r] = sa * wsc[i][r];
+        for (int r = 0; r < 4; ++r) sc[r] = kLora ? 1.0f : sa * wsc[i][r];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (g.out_f32)
@@ -470,10 +490,71 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& g, int64_t& m0, int64_
     n0 = (int64_t)(within / gms) * TN;
 }
 
+// The adapters' part of a ring kernel's 32 x 32 tiles (already scaled): acc[i][jx] of a lane holds
+// row m0 + 32 jx + l % 32. Feature blocks in pairs, so that the copies that are selected from fit
+// beside the accumulators. Tiles past the weight or the rows stay as they are.
+template <int NI, int NJ>
+__device__ __forceinline__ void lora_add32(v16f (&acc)[NI][NJ], const LoraEpi& e, int64_t m0, int64_t m, int64_t n0,
+                                           int64_t n, int lane) {
+    if (n0 >= n || m0 >= m) return;
+    constexpr int kPair = NI > 1 ? 2 : 1;
+    const int r32 = lane & 31, q8 = 8 * (lane >> 5);
+    const char* const tb = reinterpret_cast<const char*>(e.t + m0 * e.parts * e.rp);
+    const uint32_t tpart = (uint32_t)e.rp * 2;
+    int id[NJ];
+    uint32_t toff[NJ], boff[NI];
+#pragma unroll
+    for (int jx = 0; jx < NJ; ++jx) {
+        const int64_t row = m0 + 32 * jx + r32;
+        id[jx] = lora_row(e, row, m);
+        toff[jx] = (uint32_t)((row < m ? row : m - 1) - m0) * e.parts * tpart + q8 * 2;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) boff[i] = lora_b_off(e, 32 * i + r32, n0, n) + q8 * 2;
+    lora_each(id, [&](int cur) {
+        const char* const bb = lora_b_base(e, cur, n0, n);
+#pragma unroll
+        for (int jx = 0; jx < NJ; ++jx) {
+            if (!__ballot(id[jx] == cur)) continue;
+#pragma unroll
+            for (int i0 = 0; i0 < NI; i0 += kPair) {
+                v16f x[kPair];
+#pragma unroll
+                for (int u = 0; u < kPair; ++u)
+                    if (i0 + u < NI) x[u] = acc[i0 + u][jx];
+                for (int s = 0; s < e.rp; s += 32) {      // two 16-rank steps
+                    bf16x8 bf[2][kPair];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int u = 0; u < kPair; ++u)
+                            if (i0 + u < NI)
+                                bf[h][u] = lora_load(bb, boff[i0 + u] + (s + 16 * h) * 2, s + 16 * h + q8 < e.rank);
+                    for (int p = 0; p < e.parts; ++p) {
+                        bf16x8 tf[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) tf[h] = lora_load(tb, toff[jx] + p * tpart + (s + 16 * h) * 2, true);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int u = 0; u < kPair; ++u)
+                                if (i0 + u < NI) x[u] = mfma32_bf16(bf[h][u], tf[h], x[u]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kPair; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (i0 + u < NI) acc[i0 + u][jx][r] = id[jx] == cur ? x[u][r] : acc[i0 + u][jx][r];
+            }
+        }
+    });
+}
+
 // The end of a ring kernel (all of its loads retired): split k stores this split's raw sums
 // to the partial buffer; f32 output goes straight from the accumulators; bf16 output is
 // scaled, staged through the ring as TM rows of 512 bytes and stored row by row.
-template <int TN, int TM>
+template <int TN, int TM, bool kLora>
 __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN / 64][TM / 128], int64_t m0,
                                               int64_t n0, int ks, uint8_t* smem, int t, int wn, int wm, int r32,
                                               int q) {
@@ -502,6 +583,21 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
         return;
     }
     const float sa = *g.a_scale;
+    if constexpr (kLora) {
+#pragma unroll
+        for (int i = 0; i < kNI; ++i)
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq) {
+                const int64_t nb = n0 + wn * (TN / 2) + i * 32 + gq * 8 + q * 4;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float sc = sa * g.w_scale[(nb + r < g.n ? nb + r : g.n - 1) * g.ws_step];
+#pragma unroll
+                    for (int jx = 0; jx < kJX; ++jx) acc[i][jx][4 * gq + r] *= sc;
+                }
+            }
+        lora_add32(acc, g.lora, m0 + wm * (TM / 4), g.m, n0 + wn * (TN / 2), g.n, t & 63);
+    }
     if (g.out_f32) {
         // f32 output: each lane stores its four consecutive n of one m row straight from the
         // accumulators (16 bytes per lane; the output is twice the bf16 size, no LDS staging)
@@ -512,7 +608,8 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
                 const int64_t nb = n0 + wn * (TN / 2) + i * 32 + gq * 8 + q * 4;
                 float sc[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sc[r] = sa * g.w_scale[(nb + r < g.n ? nb + r : g.n - 1) * g.ws_step];
+                for (int r = 0; r < 4; ++r)
+                    sc[r] = kLora ? 1.0f : sa * g.w_scale[(nb + r < g.n ? nb + r : g.n - 1) * g.ws_step];
 #pragma unroll
                 for (int jx = 0; jx < kJX; ++jx) {
                     const int64_t mm = m0 + wm * (TM / 4) + jx * 32 + r32;
@@ -531,7 +628,8 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
             const int64_t nb = n0 + nl + q * 4;
             float sc[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[r] = sa * g.w_scale[(nb + r < g.n ? nb + r : g.n - 1) * g.ws_step];
+            for (int r = 0; r < 4; ++r)
+                sc[r] = kLora ? 1.0f : sa * g.w_scale[(nb + r < g.n ? nb + r : g.n - 1) * g.ws_step];
 #pragma unroll
             for (int jx = 0; jx < kJX; ++jx) {
                 const int ml = wm * (TM / 4) + jx * 32 + r32;
@@ -568,7 +666,7 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
 }
 
 // Operands under 2^31 bytes (buffer offsets). Grid = number of TN x TM tiles, 512 threads.
-template <int TN, int TM, bool kExact>
+template <int TN, int TM, bool kExact, bool kLora>
 __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     using RS = RingShape<TN, TM>;
     constexpr int kStage = RS::kStage, kRing = RS::kRing, kNI = RS::kNI, kJX = RS::kJX, kLoads = RS::kLoads;
@@ -691,7 +789,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     }
     wait_vmcnt<0>();   // the ring's trailing loads (past k) before the ring is reused
 
-    ring_epilogue<TN, TM>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
+    ring_epilogue<TN, TM, kLora>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
 }
 
 
@@ -699,7 +797,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
 // TN + TM rows, so every DMA request is a whole 128-byte line (the 64-byte stages issue half
 // lines) and a CU's requests in flight carry twice the bytes. A DMA block is 8 rows (1 KB);
 // each stage runs two MFMA k-steps. 192 x 128 only: four 40 KB stages fit the LDS.
-template <int TN, int TM, bool kExact>
+template <int TN, int TM, bool kExact, bool kLora>
 __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
     constexpr int kK = 128;                              // k bytes per stage
     constexpr int kStage = (TN + TM) * kK;
@@ -800,7 +898,7 @@ __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     }
     wait_vmcnt<0>();   // the ring's trailing loads (past k) before the ring is reused
-    ring_epilogue<TN, TM>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
+    ring_epilogue<TN, TM, kLora>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
 }
 
 // Split-k epilogue: out[m, n] = (sum over s of part[s, m, n], in split order) * a_scale *
@@ -872,19 +970,19 @@ static int panel_rows(int64_t m, int64_t n, int BM, int BN) {
 // of four-step groups (at 512 x 2688 x 4096 23.6 -> 23.1 us, 128 x 2688 x 4096 19.5 -> 18.0;
 // where four-step padding was needed, as at k = 2688, it lost), else two; exact sums keep two,
 // as their conversions leave no registers for more.
-template <int BM, int WN, bool kExact>
+template <int BM, int WN, bool kExact, bool kLora>
 static void launch_panel(GemmArgs g, hipStream_t st) {
     g.panel_rows = panel_rows(g.m, g.n, BM, 4 * WN);
     const int64_t npan = (g.n + g.panel_rows - 1) / g.panel_rows, nmt = (g.m + BM - 1) / BM;
     const dim3 grid((unsigned)(8 * nmt * ((npan + 7) / 8)));
     if constexpr (!kExact) {
         if ((g.k + 127) / 128 % 4 == 0) {   // k-steps: a whole number of four-step groups
-            panel_kernel<BM, WN, false, 4><<<grid, dim3(256), 0, st>>>(g);
+            panel_kernel<BM, WN, false, 4, kLora><<<grid, dim3(256), 0, st>>>(g);
             count_launch(Kern::kPanel64x128, g.m);
             return;
         }
     }
-    panel_kernel<BM, WN, kExact, 2><<<grid, dim3(256), 0, st>>>(g);
+    panel_kernel<BM, WN, kExact, 2, kLora><<<grid, dim3(256), 0, st>>>(g);
     count_launch(kExact ? Kern::kPanel64x128Exact : Kern::kPanel64x128, g.m);
 }
 
@@ -934,7 +1032,7 @@ size_t gemm_part_bytes(int64_t m, int64_t n, int64_t k) {
     return S > 1 ? (size_t)S * (size_t)m * (size_t)n * sizeof(float) : 0;
 }
 
-template <bool kExact>
+template <bool kExact, bool kLora>
 static nhm_status dispatch_gemm(GemmArgs g, hipStream_t st, float* part, size_t part_bytes) {
     const int64_t m = g.m, n = g.n, k = g.k, lda = g.lda;
     // buffer descriptors address the operands with 32-bit offsets
@@ -948,40 +1046,42 @@ static nhm_status dispatch_gemm(GemmArgs g, hipStream_t st, float* part, size_t 
         const int64_t c256 = half_tiles >= 160 ? ((half_tiles + 255) / 256) * (256 + 128) : INT64_MAX;
         const int64_t c192 = t192 >= 160 ? ((t192 + 255) / 256) * (192 + 128) : INT64_MAX;
         if (c192 < c256) {
-            ring128_kernel<192, 128, kExact><<<dim3((unsigned)t192), dim3(512), 0, st>>>(g);
+            ring128_kernel<192, 128, kExact, kLora><<<dim3((unsigned)t192), dim3(512), 0, st>>>(g);
             count_launch(kExact ? Kern::kRing192x128Exact : Kern::kRing192x128, m);
             return check_launch("gemm (192 x 128)");
         }
-        tile256_kernel<256, 128, kExact><<<dim3((unsigned)half_tiles), dim3(512), 0, st>>>(g);
+        tile256_kernel<256, 128, kExact, kLora><<<dim3((unsigned)half_tiles), dim3(512), 0, st>>>(g);
         count_launch(kExact ? Kern::kRing256x128Exact : Kern::kRing256x128, m);
         return check_launch("gemm (256 x 128)");
     }
     if (m <= 640 && offsets_fit) {   // too few ring tiles to fill the chip
-        const int S = split_k(m, n, k);
-        if (S > 1 && part && part_bytes >= gemm_part_bytes(m, n, k) && (reinterpret_cast<uintptr_t>(part) & 15) == 0) {
-            g.ksplit = S;
-            g.part = part;
-            ring128_kernel<192, 128, kExact><<<dim3((unsigned)(t192 * S)), dim3(512), 0, st>>>(g);
-            count_launch(kExact ? Kern::kRing192x128Exact : Kern::kRing192x128, m);
-            nhm_status s = check_launch("gemm (192 x 128, split k)");
-            if (s != NHM_OK) return s;
-            splitk_reduce_kernel<<<dim3((unsigned)((m * n + 1023) / 1024)), dim3(256), 0, st>>>(g);
-            count_launch(Kern::kSplitkReduce, m);
-            return check_launch("gemm split-k reduce");
+        if constexpr (!kLora) {
+            const int S = split_k(m, n, k);
+            if (S > 1 && part && part_bytes >= gemm_part_bytes(m, n, k) && (reinterpret_cast<uintptr_t>(part) & 15) == 0) {
+                g.ksplit = S;
+                g.part = part;
+                ring128_kernel<192, 128, kExact, false><<<dim3((unsigned)(t192 * S)), dim3(512), 0, st>>>(g);
+                count_launch(kExact ? Kern::kRing192x128Exact : Kern::kRing192x128, m);
+                nhm_status s = check_launch("gemm (192 x 128, split k)");
+                if (s != NHM_OK) return s;
+                splitk_reduce_kernel<<<dim3((unsigned)((m * n + 1023) / 1024)), dim3(256), 0, st>>>(g);
+                count_launch(Kern::kSplitkReduce, m);
+                return check_launch("gemm split-k reduce");
+            }
         }
-        launch_panel<64, 32, kExact>(g, st);
+        launch_panel<64, 32, kExact, kLora>(g, st);
         return check_launch("gemm (panel)");
     }
     const int64_t wide_tiles = ((n + kWT - 1) / kWT) * ((m + kWT - 1) / kWT);
     if (offsets_fit && wide_tiles >= 160) {
-        tile256_kernel<256, 256, kExact><<<dim3((unsigned)wide_tiles), dim3(512), 0, st>>>(g);
+        tile256_kernel<256, 256, kExact, kLora><<<dim3((unsigned)wide_tiles), dim3(512), 0, st>>>(g);
         count_launch(kExact ? Kern::kRing256x256Exact : Kern::kRing256x256, m);
         return check_launch("gemm (256 x 256)");
     }
     if (!offsets_fit)   // refused by the callers' host checks before anything is enqueued
         return fail(NHM_ERR_UNSUPPORTED, "gemm: an operand of 2 GiB or more");
     const dim3 grid((unsigned)((n + kTile - 1) / kTile), (unsigned)((m + kTile - 1) / kTile));
-    gemm_kernel<kExact><<<grid, dim3(256), 0, st>>>(g);
+    gemm_kernel<kExact, kLora><<<grid, dim3(256), 0, st>>>(g);
     count_launch(kExact ? Kern::kTile128Exact : Kern::kTile128, m);
     return check_launch("gemm");
 }
@@ -994,7 +1094,19 @@ nhm_status launch_gemm(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* 
                        : ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0,
                out_f32};
     g.ws_step = ws_step;
-    return exact ? dispatch_gemm<true>(g, st, part, part_bytes) : dispatch_gemm<false>(g, st, part, part_bytes);
+    return exact ? dispatch_gemm<true, false>(g, st, part, part_bytes) : dispatch_gemm<false, false>(g, st, part, part_bytes);
+}
+
+nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* w, const float* w_scale,
+                            const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
+                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora) {
+    GemmArgs g{a, lda, m, w, w_scale, a_scale, n, k, out, ld_out,
+               out_f32 ? ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out_f32) % 16 == 0
+                       : ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0,
+               out_f32};
+    g.ws_step = ws_step;
+    g.lora = lora;
+    return exact ? dispatch_gemm<true, true>(g, st, nullptr, 0) : dispatch_gemm<false, true>(g, st, nullptr, 0);
 }
 
 }  // namespace nhm

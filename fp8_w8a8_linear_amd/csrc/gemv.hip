@@ -23,6 +23,7 @@
 // MFMA, so a wave keeps its whole share in flight. The per-wave partial tiles are
 // summed through LDS in wave order -- deterministic, and no communication between
 // workgroups (an agent-scope fence would write back the L2 of every XCD).
+#include "lora_device.h"
 #include "nhm_device.h"
 #include "nhm_internal.h"
 
@@ -44,16 +45,56 @@ struct GemvArgs {
     // workgroup b owns features [b base + min(b, extra), ...) -- base + 1 of them for b < extra,
     // base for the others (at most 16 x kTiles)
     int base, extra;
+    LoraEpi lora;      // the kernels with adapters only
 };
+
+// The adapters' part of the workgroup's kTiles row tiles, split over the waves: wave w takes the
+// w-th, (w + kWaves)-th, ... distinct adapter among the tokens. d[t] register r of lane l is
+// feature n0 + 16 t + 4 (l / 16) + r of token l % 16; lanes of other tokens stay as they are.
+template <int S, int kWaves, int kTiles>
+__device__ __forceinline__ void gemv_lora(v4f (&d)[kTiles], const GemvArgs& g, int64_t n0, int wave, int lane) {
+    const int r16 = lane & 15, q8 = 8 * (lane >> 4);
+    const int id[1] = {lora_row(g.lora, r16, g.m)};
+    const char* const tb = reinterpret_cast<const char*>(g.lora.t);
+    const uint32_t tpart = (uint32_t)g.lora.rp * 2;
+    const uint32_t toff = (uint32_t)(r16 < g.m ? r16 : g.m - 1) * g.lora.parts * tpart + q8 * 2;
+    int turn = 0;
+    lora_each(id, [&](int cur) {
+        if (turn++ % kWaves != wave) return;
+        const char* const bb = lora_b_base(g.lora, cur, n0, g.n);
+        bf16x8 bf[S][kTiles], tf[3][S];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                bf[s][t] = lora_load(bb, lora_b_off(g.lora, 16 * t + r16, n0, g.n) + q8 * 2 + 64 * s, 32 * s + q8 < g.lora.rank);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int s = 0; s < S; ++s) tf[p][s] = lora_load(tb, toff + (p < g.lora.parts ? p : 0) * tpart + 64 * s, true);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (p < g.lora.parts) x = mfma_bf16(bf[s][t], tf[p][s], x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[t][r] = id[0] == cur ? x[r] : d[t][r];
+        }
+    });
+}
 
 // Cache policy of the weight stream: the default. The non-temporal hint (nt) made the in_proj
 // GEMV at m = 8 slower, 9.24 against 8.37 us per launch (sc0 alone 8.39, sc1 9.76, nt with
 // either 9.23), although each weight row is read once per call.
 constexpr int kStreamAux = 0;
 
-template <int kWaves, int kSteps, int kTiles, bool kLines>
+template <int kWaves, int kSteps, int kTiles, bool kLines, bool kLora>
 __global__ __launch_bounds__(kWaves * 64) void gemv_kernel(const GemvArgs g) {
     __shared__ v4f s_red[kWaves][kTiles][64];   // every wave's partial of every row tile
+    __shared__ v4f s_lora[kLora ? kWaves : 1][kLora ? kTiles : 1][kLora ? 64 : 1];   // and of the adapters' part
     // kLines: this wave's transpose buffer, one k-step of the 16 kTiles rows
     __shared__ __attribute__((aligned(16))) uint8_t s_tr[kLines ? kWaves : 1][kLines ? 16 * kTiles * 128 : 16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -169,6 +210,16 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_kernel(const GemvArgs g) {
     // (deterministic) and stores it, so the row tiles' epilogues run side by side.
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) s_red[wave][t][lane] = acc[t];
+    if constexpr (kLora) {
+        v4f dl[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) dl[t] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (g.lora.rp == 32) gemv_lora<1, kWaves, kTiles>(dl, g, n0, wave, lane);
+        else if (g.lora.rp == 64) gemv_lora<2, kWaves, kTiles>(dl, g, n0, wave, lane);
+        else gemv_lora<4, kWaves, kTiles>(dl, g, n0, wave, lane);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) s_lora[wave][t][lane] = dl[t];
+    }
     __syncthreads();
     if (wave >= kTiles) return;
     v4f d = s_red[0][wave][lane];
@@ -180,6 +231,17 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_kernel(const GemvArgs g) {
     float sc[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) sc[r] = sa * __uint_as_float(g.ws_step != 0 ? sraw[r] : sraw[0]);
+    if constexpr (kLora) {   // the scaled projection plus the adapters' part (rows without one add nothing)
+        v4f a = s_lora[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) a += s_lora[w][wave][lane];
+        const bool has = lora_row(g.lora, col, g.m) >= 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            d[r] = has ? d[r] * sc[r] + a[r] : d[r] * sc[r];
+            sc[r] = 1.0f;
+        }
+    }
     {
         if (g.out_f32) {
             float* of = g.out_f32 + (int64_t)col * g.ld_out + nb;
@@ -214,28 +276,16 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_kernel(const GemvArgs g) {
     }
 }
 
-nhm_status launch_gemv(const uint8_t* a, int64_t lda, int m, const uint8_t* w, const float* w_scale,
-                       const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
-                       float* out_f32, uint8_t* out_q, int64_t ld_q, const float* q_scale, uint32_t* clear,
-                       int clear_n, int ws_step) {
-    GemvArgs g;
-    g.ws_step = ws_step;
-    g.clear = clear_n > 0 ? clear : nullptr;
-    g.clear_n = clear_n;
-    g.out_q = out_f32 ? nullptr : out_q;
-    g.ld_q = ld_q;
-    g.q_scale = q_scale;
-    g.vec_q = ld_q % 4 == 0 && reinterpret_cast<uintptr_t>(out_q) % 4 == 0;
-    g.a = a; g.lda = lda; g.m = m;
-    g.w = w; g.w_scale = w_scale; g.a_scale = a_scale; g.n = n; g.k = k;
-    g.out = out; g.ld_out = ld_out;
-    g.out_f32 = out_f32;
-    g.vec_out = out_f32 ? ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out_f32) % 16 == 0
-                        : ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0;
+template <bool kLora>
+static nhm_status dispatch_gemv(GemvArgs g, hipStream_t st) {
+    const int64_t m = g.m, lda = g.lda, n = g.n, k = g.k;
+    g.vec_q = g.ld_q % 4 == 0 && reinterpret_cast<uintptr_t>(g.out_q) % 4 == 0;
+    g.vec_out = g.out_f32 ? g.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(g.out_f32) % 16 == 0
+                          : g.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % 8 == 0;
     g.ksteps = (int)((k + 127) / 128);
     if (g.ksteps > 16 * kGemvMaxSteps)
         return fail(NHM_ERR_UNSUPPORTED, "gemv: k %lld exceeds %d", (long long)k, 16 * 128 * kGemvMaxSteps);
-    if (n * k >= (int64_t(1) << 31) || (int64_t)m * lda >= (int64_t(1) << 31))
+    if (n * k >= (int64_t(1) << 31) || m * lda >= (int64_t(1) << 31))
         return fail(NHM_ERR_UNSUPPORTED, "gemv: operands of 2 GiB or more");
     // 4 waves up to 23 k-steps (k < 2944), then 8, then 16; each wave holds its steps in
     // registers, their count rounded up to 2, 4, 6 or 8
@@ -257,7 +307,7 @@ nhm_status launch_gemv(const uint8_t* a, int64_t lda, int m, const uint8_t* w, c
     g.extra = (int)(n % wgs);
     const int tiles = (g.base + (g.extra ? 1 : 0) + 15) / 16;
     const dim3 grid((unsigned)wgs);
-#define NHM_GEMV_LAUNCH(W, S, T) gemv_kernel<W, S, T, (W == 8)><<<grid, dim3(W * 64), 0, st>>>(g)
+#define NHM_GEMV_LAUNCH(W, S, T) gemv_kernel<W, S, T, (W == 8), kLora><<<grid, dim3(W * 64), 0, st>>>(g)
 #define NHM_GEMV_STEPS(W, T)                         \
     do {                                             \
         if (steps == 2) NHM_GEMV_LAUNCH(W, 2, T);    \
@@ -278,6 +328,37 @@ nhm_status launch_gemv(const uint8_t* a, int64_t lda, int m, const uint8_t* w, c
 #undef NHM_GEMV_LAUNCH
     count_launch(Kern::kGemv, m);
     return check_launch("gemv");
+}
+
+nhm_status launch_gemv(const uint8_t* a, int64_t lda, int m, const uint8_t* w, const float* w_scale,
+                       const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
+                       float* out_f32, uint8_t* out_q, int64_t ld_q, const float* q_scale, uint32_t* clear,
+                       int clear_n, int ws_step) {
+    GemvArgs g{};
+    g.ws_step = ws_step;
+    g.clear = clear_n > 0 ? clear : nullptr;
+    g.clear_n = clear_n;
+    g.out_q = out_f32 ? nullptr : out_q;
+    g.ld_q = ld_q;
+    g.q_scale = q_scale;
+    g.a = a; g.lda = lda; g.m = m;
+    g.w = w; g.w_scale = w_scale; g.a_scale = a_scale; g.n = n; g.k = k;
+    g.out = out; g.ld_out = ld_out;
+    g.out_f32 = out_f32;
+    return dispatch_gemv<false>(g, st);
+}
+
+nhm_status launch_gemv_lora(const uint8_t* a, int64_t lda, int m, const uint8_t* w, const float* w_scale,
+                            const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
+                            float* out_f32, int ws_step, const LoraEpi& lora) {
+    GemvArgs g{};
+    g.ws_step = ws_step;
+    g.a = a; g.lda = lda; g.m = m;
+    g.w = w; g.w_scale = w_scale; g.a_scale = a_scale; g.n = n; g.k = k;
+    g.out = out; g.ld_out = ld_out;
+    g.out_f32 = out_f32;
+    g.lora = lora;
+    return dispatch_gemv<true>(g, st);
 }
 
 }  // namespace nhm

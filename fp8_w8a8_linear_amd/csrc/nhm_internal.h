@@ -28,7 +28,7 @@ enum class Kern : int {
     kQuantVec8, kQuantScalar, kDequantChannel, kGemv, kRing192x128, kRing192x128Exact, kRing256x128,
     kRing256x128Exact, kRing256x256, kRing256x256Exact, kPanel64x128, kPanel64x128Exact, kTile128,
     kTile128Exact, kSplitkReduce, kDecodeSsm, kGnormQuant, kClear, kConvFwd, kSsdState, kSsdPass, kSsdOut,
-    kLoraDown, kLoraUp, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan, kCount
+    kLoraDown, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan, kCount
 };
 void count_launch(Kern k, int64_t rows);
 
@@ -39,6 +39,11 @@ void fill_layout(const nhm_geometry* g, nhm_layout* l);
 nhm_status linear_check(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
                         const void* out, nhm_dtype out_type, int64_t ld_out, const void* ws, size_t ws_bytes,
                         size_t need);
+// The weight-streaming GEMV serves m <= 16 (k up to 16384, weights under 2 GiB: its buffer
+// descriptors take 32-bit offsets); the tiled GEMM the rest.
+inline bool use_gemv(int64_t m, int64_t n, int64_t k) { return m <= 16 && k <= 16384 && n * k < (int64_t(1) << 31); }
+// Index step of the weight scale: per channel (w_scale[n]) or one scale for every channel.
+inline int ws_step(const nhm_fp8_weight& w) { return w.w_scale_per_tensor ? 0 : 1; }
 // bytes of the e4m3 copy of a bf16 activation
 size_t linear_codes_ws(int64_t m, int64_t k, nhm_dtype t);
 // One projection on an e4m3 activation [m, lda]; out_f32 non-null: f32 output instead of out.
@@ -175,25 +180,43 @@ nhm_status launch_prefill_mid(const PrefillArgs& a, hipStream_t st);
 void launch_ssd_state(const PrefillArgs& a, hipStream_t st);
 void launch_ssd_out(const PrefillArgs& a, hipStream_t st);
 
-// ---- low-rank adapters (lora.hip)
-struct LoraArgs {
+// ---- low-rank adapters (lora.hip, and the projections' epilogues in gemv.hip and gemm.hip)
+
+// The low-rank product t = scale x A_e^T enters the second product as bf16 parts that add up to
+// it: parts 0, 1 (, 2) of row i at t[(i * parts + part) * rp], rp = 32, 64 or 128, the
+// first that holds the rank, zeros past it. Rows without an adapter hold nothing.
+constexpr int kLoraMaxRank = 128;
+inline int lora_rp(int rank) { return rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+// What a projection's epilogue needs to add t B_e^T to its f32 result before it is rounded.
+struct LoraEpi {
+    const uint16_t* t = nullptr;            // [m, parts, rp]
+    const uint16_t* b = nullptr;            // bf16 [n_adapters, n, rank]
+    const int32_t* row_adapter = nullptr;   // [m]
+    int32_t n_adapters = 0, rank = 0, rp = 0, parts = 0;
+};
+
+struct LoraDownArgs {
     const uint16_t* x;         // bf16 [m, ld_x], or nullptr with x_codes
     const uint8_t* x_codes;    // e4m3 [m, ld_x], worth code * *a_scale
-    int64_t ld_x, m, n, k;
+    int64_t ld_x, m, k;
     const float* a_scale;      // [1]
+    uint8_t* q;                // non-null (bf16 input): also the codes E4M3(x / *a_scale) [m, k]
     const uint16_t* a;         // bf16 [n_adapters, rank, k]
-    const uint16_t* b;         // bf16 [n_adapters, n, rank]
     const float* scale;        // [n_adapters] or nullptr
-    int32_t n_adapters, rank;
+    int32_t n_adapters, rank, rp, parts;
     const int32_t* row_adapter;   // [m]
-    float* t;                  // [m, rank]
-    float* base;               // f32 projection [m, n]
-    uint16_t* out;             // bf16 [m, ld_out], or nullptr with out_f32
-    float* out_f32;
-    int64_t ld_out;
+    uint16_t* t;               // [m, parts, rp]
 };
-nhm_status launch_lora_down(const LoraArgs& g, hipStream_t st);
-nhm_status launch_lora_up(const LoraArgs& g, hipStream_t st);
+nhm_status launch_lora_down(const LoraDownArgs& g, hipStream_t st);
+
+// The projections with the adapters' part (the same kernels and choices as without, no split over k).
+nhm_status launch_gemv_lora(const uint8_t* a, int64_t lda, int m, const uint8_t* w, const float* w_scale,
+                            const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
+                            float* out_f32, int ws_step, const LoraEpi& lora);
+nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* w, const float* w_scale,
+                            const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
+                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora);
 
 // ---- beam search (beam.hip)
 struct BeamArgs {

@@ -11,14 +11,12 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 
 bool rank_ok(int32_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
 
-// Regions of the adapter call's workspace: the activation codes, the f32 projection, the low-rank product.
-struct LoraWs { size_t codes, base, t, total; };
-LoraWs lora_ws(int64_t m, int64_t n, int64_t k, nhm_dtype a_type, int32_t rank) {
+// Regions of the adapter call's workspace: the activation codes of a bf16 input, the low-rank product.
+struct LoraWs { size_t t, total; };
+LoraWs lora_ws(int64_t m, int64_t k, nhm_dtype a_type, int32_t rank) {
     LoraWs w{};
-    w.codes = 0;
-    w.base = align_up(linear_codes_ws(m, k, a_type), 256);
-    w.t = w.base + align_up((size_t)m * (size_t)n * sizeof(float), 256);
-    w.total = w.t + align_up((size_t)m * (size_t)rank * sizeof(float), 256);
+    w.t = align_up(linear_codes_ws(m, k, a_type), 256);
+    w.total = w.t + align_up((size_t)m * 3 * lora_rp(rank) * sizeof(uint16_t), 256);
     return w;
 }
 
@@ -46,7 +44,7 @@ extern "C" {
 
 size_t nhm_fp8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, nhm_dtype a_type, int32_t rank) {
     if (m <= 0 || n <= 0 || k <= 0 || !rank_ok(rank)) return 0;
-    return lora_ws(m, n, k, a_type, rank).total;
+    return lora_ws(m, k, a_type, rank).total;
 }
 
 nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
@@ -55,42 +53,39 @@ nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64
     clear_error();
     nhm_status s = check_lora(lora);
     if (s != NHM_OK) return s;
-    const size_t need = w && m > 0 && w->n > 0 && w->k > 0 ? lora_ws(m, w->n, w->k, a_type, lora->rank).total : 0;
+    const size_t need = w && m > 0 && w->n > 0 && w->k > 0 ? lora_ws(m, w->k, a_type, lora->rank).total : 0;
     s = linear_check(a, a_type, m, ld_a, w, out, out_type, ld_out, ws, ws_bytes, need);
     if (s != NHM_OK || m == 0) return s;
     if (m > INT_MAX) return fail(NHM_ERR_SHAPE, "m %lld out of range", (long long)m);
     if (!row_adapter) return fail(NHM_ERR_NULL, "row_adapter is NULL");
     if (!aligned(row_adapter, 4)) return fail(NHM_ERR_ALIGN, "row_adapter must be 4-byte aligned");
     hipStream_t st = (hipStream_t)stream;
-    const LoraWs l = lora_ws(m, w->n, w->k, a_type, lora->rank);
+    const LoraWs l = lora_ws(m, w->k, a_type, lora->rank);
     char* wsb = static_cast<char*>(ws);
-    const uint8_t* q = static_cast<const uint8_t*>(a);
-    int64_t ld_q = ld_a;
-    if (a_type == NHM_BF16) {
-        uint8_t* qb = reinterpret_cast<uint8_t*>(wsb + l.codes);
-        launch_quantize(static_cast<const uint16_t*>(a), m, w->k, ld_a, w->a_scale, qb, w->k, st);
-        if ((s = check_launch("lora quant")) != NHM_OK) return s;
-        q = qb;
-        ld_q = w->k;
-    }
-    LoraArgs g{};
-    g.x = a_type == NHM_BF16 ? static_cast<const uint16_t*>(a) : nullptr;
-    g.x_codes = a_type == NHM_BF16 ? nullptr : q;
+    const bool bf16 = a_type == NHM_BF16;
+    const uint8_t* q = bf16 ? reinterpret_cast<uint8_t*>(wsb) : static_cast<const uint8_t*>(a);
+    const int64_t ld_q = bf16 ? w->k : ld_a;
+    LoraDownArgs g{};
+    g.x = bf16 ? static_cast<const uint16_t*>(a) : nullptr;
+    g.x_codes = bf16 ? nullptr : q;
     g.ld_x = ld_a;
-    g.m = m; g.n = w->n; g.k = w->k;
+    g.m = m; g.k = w->k;
     g.a_scale = w->a_scale;
-    g.a = lora->a; g.b = lora->b; g.scale = lora->scale;
+    g.q = bf16 ? reinterpret_cast<uint8_t*>(wsb) : nullptr;
+    g.a = lora->a; g.scale = lora->scale;
     g.n_adapters = lora->n_adapters; g.rank = lora->rank;
+    g.rp = lora_rp(lora->rank);
+    g.parts = out_type == NHM_F32 ? 3 : 2;
     g.row_adapter = row_adapter;
-    g.t = reinterpret_cast<float*>(wsb + l.t);
-    g.base = reinterpret_cast<float*>(wsb + l.base);
-    g.out = out_type == NHM_BF16 ? static_cast<uint16_t*>(out) : nullptr;
-    g.out_f32 = out_type == NHM_F32 ? static_cast<float*>(out) : nullptr;
-    g.ld_out = ld_out;
+    g.t = reinterpret_cast<uint16_t*>(wsb + l.t);
     if ((s = launch_lora_down(g, st)) != NHM_OK) return s;
-    if ((s = project(q, ld_q, m, *w, nullptr, w->n, st, reinterpret_cast<float*>(wsb + l.base), nullptr, 0, exact != 0)) != NHM_OK)
-        return s;
-    return launch_lora_up(g, st);
+    const LoraEpi epi{g.t, lora->b, row_adapter, g.n_adapters, g.rank, g.rp, g.parts};
+    uint16_t* ob = out_type == NHM_BF16 ? static_cast<uint16_t*>(out) : nullptr;
+    float* of = out_type == NHM_F32 ? static_cast<float*>(out) : nullptr;
+    if (use_gemv(m, w->n, w->k))
+        return launch_gemv_lora(q, ld_q, (int)m, w->w, w->w_scale, w->a_scale, w->n, w->k, ob, ld_out, st, of, ws_step(*w), epi);
+    return launch_gemm_lora(q, ld_q, m, w->w, w->w_scale, w->a_scale, w->n, w->k, ob, ld_out, st, of, exact != 0, ws_step(*w),
+                            epi);
 }
 
 size_t nhm_beam_select_workspace_bytes(int64_t n_groups, int32_t n_beams, int64_t vocab, int32_t n_cand) {

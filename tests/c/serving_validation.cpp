@@ -35,8 +35,15 @@ nhm_status launch_decode_ssm(const DecodeSsmArgs&, int, hipStream_t) { reached("
 void launch_clear(uint32_t*, int, hipStream_t) { reached("launch_clear"); }
 nhm_status launch_gnorm_quant(const GnormArgs&, hipStream_t) { reached("launch_gnorm_quant"); }
 nhm_status launch_prefill_mid(const PrefillArgs&, hipStream_t) { reached("launch_prefill_mid"); }
-nhm_status launch_lora_down(const LoraArgs&, hipStream_t) { reached("launch_lora_down"); }
-nhm_status launch_lora_up(const LoraArgs&, hipStream_t) { reached("launch_lora_up"); }
+nhm_status launch_lora_down(const LoraDownArgs&, hipStream_t) { reached("launch_lora_down"); }
+nhm_status launch_gemv_lora(const uint8_t*, int64_t, int, const uint8_t*, const float*, const float*, int64_t, int64_t,
+                            uint16_t*, int64_t, hipStream_t, float*, int, const LoraEpi&) {
+    reached("launch_gemv_lora");
+}
+nhm_status launch_gemm_lora(const uint8_t*, int64_t, int64_t, const uint8_t*, const float*, const float*, int64_t, int64_t,
+                            uint16_t*, int64_t, hipStream_t, float*, bool, int, const LoraEpi&) {
+    reached("launch_gemm_lora");
+}
 size_t beam_ws_bytes(int64_t rows, int64_t, int32_t) { return (size_t)rows * 16; }
 nhm_status launch_beam_select(BeamArgs, void*, hipStream_t) { reached("launch_beam_select"); }
 nhm_status launch_beam_reorder(const ReorderArgs&, int64_t, int32_t, hipStream_t) { reached("launch_beam_reorder"); }
