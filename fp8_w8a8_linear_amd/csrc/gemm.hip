@@ -112,13 +112,148 @@ __device__ __forceinline__ v4f mfma16_step(const v8i& a, const v8i& b, const v4f
     }
 }
 
+// ---------------------------------------------------------------- direct-to-LDS loads
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// Buffer descriptor over [base, base + bytes) (bytes clamped to 2^31 - 1) with range checking.
+__device__ __forceinline__ i32x4 buffer_desc(const void* base, int64_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    i32x4 r;
+    r[0] = (int)(uint32_t)b;
+    r[1] = (int)((uint32_t)(b >> 32) & 0xffffu);
+    r[2] = (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff);
+    r[3] = 0x00020000;
+    return r;
+}
+
+// 16 bytes per lane from byte offset voff of the buffer into LDS at lds + 16 * lane (an
+// offset past the range writes zeros). Issued as asm so that the compiler's wait insertion
+// does not hold every later LDS read behind it; the kernel waits for these loads itself.
+__device__ __forceinline__ void dma16(const i32x4& rs, const uint8_t* lds, uint32_t voff) {
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)lds;
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(rs)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+constexpr uint32_t kOutOfRange = 0x80000000u;   // past every buffer range used here (< 2^31 bytes)
+
+// ---------------------------------------------------------------- the adapters' part of a tile
+
+// After a tile's k loop: for each distinct adapter among the tile's TM rows, compute(cur, c0, tl, bl)
+// adds the products of 64 ranks from c0 on. tl: the rows' t, part p at tl + p TM 128, 128 bytes per row
+// under swz128; bl: the tile's TN features of B_cur likewise (zeros past the rank, the rows and the
+// features). t is loaded once per 64 ranks, B_cur of the next adapter while this one is worked on;
+// both go straight to LDS and are read there by every wave that needs them, where loads into
+// registers paid a round trip to L2 per step (15,360 x 10,304 x 2,688 at rank 64: 723 us against
+// 500 without adapters). Every wave of the workgroup calls this, with LDS that nobody reads any more.
+template <int TN, int TM, int NT>
+constexpr int lora_lds() { return 3 * TM * 128 + 2 * TN * 128; }
+
+template <int TN, int TM, int NT, typename F>
+__device__ __forceinline__ void lora_tile(const LoraEpi& e, int64_t m0, int64_t m, int64_t n0, int64_t n, uint8_t* smem,
+                                          int wave, int lane, F compute) {
+    constexpr int kIds = TM / 64, kWaves = NT / 64;
+    static_assert(TM % 64 == 0 && TN % 8 == 0, "tile shape");
+    uint64_t all[kIds], any = 0;
+    int id[kIds];
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+        id[j] = lora_row(e, m0 + 64 * j + lane, m);
+        all[j] = __ballot(id[j] >= 0);
+        any |= all[j];
+    }
+    if (any == 0) return;
+    uint8_t* const bl = smem + e.parts * TM * 128;
+    const int lr = lane >> 3;                                        // row of an 8-row block of 1 KB
+    // descriptors and the adapter at hand are the same in every lane; the compiler is told
+    auto uniform = [](i32x4 r) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
+        return r;
+    };
+    const i32x4 trs = uniform(buffer_desc(e.t + m0 * e.parts * e.rp, (m - m0) * e.parts * e.rp * 2));
+    auto next = [&](uint64_t (&todo)[kIds]) {
+        int cur = -1;
+#pragma unroll
+        for (int j = 0; j < kIds; ++j)
+            if (cur < 0 && todo[j]) cur = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(todo[j]));
+#pragma unroll
+        for (int j = 0; j < kIds; ++j) todo[j] &= ~__ballot(id[j] == cur);
+        return cur;
+    };
+    for (int c0 = 0; c0 < e.rp; c0 += 64) {
+        __syncthreads();             // the LDS is free: of the k loop, or of the previous ranks
+        for (int p = 0; p < e.parts; ++p)
+            for (int blk = wave; blk < TM / 8; blk += kWaves) {
+                const int row = blk * 8 + lr, rank = c0 + 8 * ((lane & 7) ^ (row & 7) ^ ((row >> 3) & 1));
+                dma16(trs, smem + p * TM * 128 + blk * 1024,
+                      rank < e.rp && m0 + row < m ? (uint32_t)(((row * e.parts + p) * e.rp + rank) * 2) : kOutOfRange);
+            }
+        auto stage_b = [&](int cur, int buf) {
+            const i32x4 brs = uniform(buffer_desc(e.b + ((int64_t)cur * n + n0) * e.rank, (n - n0) * e.rank * 2));
+            for (int blk = wave; blk < TN / 8; blk += kWaves) {
+                const int row = blk * 8 + lr, rank = c0 + 8 * ((lane & 7) ^ (row & 7) ^ ((row >> 3) & 1));
+                dma16(brs, bl + buf * TN * 128 + blk * 1024,
+                      rank < e.rank && n0 + row < n ? (uint32_t)((row * e.rank + rank) * 2) : kOutOfRange);
+            }
+        };
+        uint64_t todo[kIds];
+#pragma unroll
+        for (int j = 0; j < kIds; ++j) todo[j] = all[j];
+        int cur = next(todo), buf = 0;
+        stage_b(cur, 0);
+        while (cur >= 0) {
+            wait_vmcnt<0>();         // this wave's share of t and B_cur
+            __syncthreads();         // everyone's; and everyone is done with the other buffer
+            const int nxt = next(todo);
+            if (nxt >= 0) stage_b(nxt, buf ^ 1);
+            compute(cur, c0, smem, bl + buf * TN * 128);
+            cur = nxt;
+            buf ^= 1;
+        }
+    }
+    __syncthreads();                 // the LDS may be written again
+}
+
+// compute() of waves with 16 x 16 tiles: acc[i][j] register r of lane l is feature nw + 16 i +
+// 4 (l / 16) + r of row mw + 16 j + l % 16 of the workgroup's tile.
+template <int TM, int TNW, int TMW>
+__device__ __forceinline__ void lora_mma16(v4f (&acc)[TNW][TMW], const LoraEpi& e, const int (&id)[TMW], int cur, int c0,
+                                           const uint8_t* tl, const uint8_t* bl, int mw, int nw, int lane) {
+    const int r16 = lane & 15, q = lane >> 4;
+    const int steps = e.rp - c0 > 32 ? 2 : 1;      // 32 ranks each
+#pragma unroll
+    for (int j = 0; j < TMW; ++j) {
+        if (!__ballot(id[j] == cur)) continue;
+        v4f x[TNW];
+#pragma unroll
+        for (int i = 0; i < TNW; ++i) x[i] = acc[i][j];
+        for (int s = 0; s < steps; ++s) {
+            bf16x8 bf[TNW];
+#pragma unroll
+            for (int i = 0; i < TNW; ++i) bf[i] = __builtin_bit_cast(bf16x8, lds16(bl + swz128(nw + 16 * i + r16, 4 * s + q)));
+            for (int p = 0; p < e.parts; ++p) {
+                const bf16x8 tf = __builtin_bit_cast(bf16x8, lds16(tl + p * TM * 128 + swz128(mw + 16 * j + r16, 4 * s + q)));
+#pragma unroll
+                for (int i = 0; i < TNW; ++i) x[i] = mfma_bf16(bf[i], tf, x[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TNW; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = id[j] == cur ? x[i][r] : acc[i][j][r];
+    }
+}
+
 // ---------------------------------------------------------------- panel kernel
 
 __device__ __forceinline__ uint4 bload(const __amdgpu_buffer_rsrc_t& r, uint32_t off) {
     const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
-constexpr uint32_t kOutOfRange = 0x80000000u;   // past every buffer range used here (< 2^31 bytes)
 
 // D: weight k-steps in flight per wave (and activation tiles in registers).
 template <int BM, int WN, bool kExact, int D, bool kLora>
@@ -127,7 +262,9 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     constexpr int U = D % 2 == 0 ? D : 2 * D;   // loop unroll: step kt's registers are slot kt % D
     constexpr int LA = BM * 8 / 256;   // 16-byte chunks of the activation tile per thread
     static_assert(WN % 16 == 0 && BM % 32 == 0, "tile shape");
-    __shared__ __attribute__((aligned(16))) uint8_t sA[3][BM * 128];
+    // the activation tiles, and after the k loop the adapters' operands
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kLora ? lora_lds<BN, BM, 256>() : 3 * BM * 128];
+    uint8_t (&sA)[3][BM * 128] = *reinterpret_cast<uint8_t (*)[3][BM * 128]>(smem);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane >> 4, r16 = lane & 15;
     // Tile order: blocks are dealt to the 8 XCDs round robin (block b runs on XCD b % 8),
     // so consecutive blocks of one XCD walk the m-tiles of one weight panel.
@@ -245,7 +382,13 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
             for (int j = 0; j < TM; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[i][j][r] *= sa * wsc[i][r];
-        lora_add16(acc, g.lora, m0, g.m, nw0, g.n, lane);
+        int id[TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) id[j] = lora_row(g.lora, m0 + j * 16 + r16, g.m);
+        lora_tile<BN, BM, 256>(g.lora, m0, g.m, (int64_t)pan * PW, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+                               [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
+                                   lora_mma16<BM>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
+                               });
     }
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
@@ -292,8 +435,10 @@ __device__ __forceinline__ v8i lds_operand(const uint8_t* s, int row, int q) {
 
 template <bool kExact, bool kLora>
 __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
-    __shared__ __attribute__((aligned(16))) uint8_t sW[2][kTile * kTile];
-    __shared__ __attribute__((aligned(16))) uint8_t sA[2][kTile * kTile];
+    // two stages of both operands, and after the k loop the adapters' operands
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kLora ? lora_lds<kTile, kTile, 256>() : 4 * kTile * kTile];
+    uint8_t (&sW)[2][kTile * kTile] = *reinterpret_cast<uint8_t (*)[2][kTile * kTile]>(smem);
+    uint8_t (&sA)[2][kTile * kTile] = *reinterpret_cast<uint8_t (*)[2][kTile * kTile]>(smem + 2 * kTile * kTile);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wn = wave >> 1, wm = wave & 1;
     const int q = lane >> 4, r16 = lane & 15;
@@ -355,7 +500,13 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[i][j][r] *= sa * wsc[i][r];
-        lora_add16(acc, g.lora, m0 + wm * 64, g.m, n0 + wn * 64, g.n, lane);
+        int id[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) id[j] = lora_row(g.lora, m0 + wm * 64 + j * 16 + r16, g.m);
+        lora_tile<kTile, kTile, 256>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+                                     [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
+                                         lora_mma16<kTile>(acc, g.lora, id, cur, c0, tl, bl, wm * 64, wn * 64, lane);
+                                     });
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -376,7 +527,6 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
 // ---------------------------------------------------------------- 256 x 256 tile kernel
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -449,28 +599,6 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
 // cover all 16 slots of the 256-byte bank window, and 8 consecutive rows all 8 of 128 bytes.
 __device__ __forceinline__ int swz64(int row, int c) { return row * 64 + ((c ^ (((row >> 1) ^ (row >> 2)) & 3)) << 4); }
 
-// Buffer descriptor over [base, base + bytes) (bytes clamped to 2^31 - 1) with range checking.
-__device__ __forceinline__ i32x4 buffer_desc(const void* base, int64_t bytes) {
-    const uint64_t b = reinterpret_cast<uint64_t>(base);
-    i32x4 r;
-    r[0] = (int)(uint32_t)b;
-    r[1] = (int)((uint32_t)(b >> 32) & 0xffffu);
-    r[2] = (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff);
-    r[3] = 0x00020000;
-    return r;
-}
-
-// 16 bytes per lane from byte offset voff of the buffer into LDS at lds + 16 * lane (an
-// offset past the range writes zeros). Issued as asm so that the compiler's wait insertion
-// does not hold every later LDS read behind it; the kernel waits for these loads itself.
-__device__ __forceinline__ void dma16(const i32x4& rs, const uint8_t* lds, uint32_t voff) {
-    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)lds;
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(rs)
-                 : "memory", "m0");
-}
-
-__device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-
 // Block -> (tile origin m0, n0; k split ks) of a ring kernel. Blocks go to the 8 XCDs round
 // robin; each XCD takes a contiguous share of the tiles in an order that walks 8 m-tiles per
 // n-tile, so the ~32 tiles an XCD holds at once share 8 activation and 4 weight panels
@@ -488,67 +616,6 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& g, int64_t& m0, int64_
     const int gms = min(kGroupM, ntm - grp * kGroupM);
     m0 = (int64_t)(grp * kGroupM + within % gms) * TM;
     n0 = (int64_t)(within / gms) * TN;
-}
-
-// The adapters' part of a ring kernel's 32 x 32 tiles (already scaled): acc[i][jx] of a lane holds
-// row m0 + 32 jx + l % 32. Feature blocks in pairs, so that the copies that are selected from fit
-// beside the accumulators. Tiles past the weight or the rows stay as they are.
-template <int NI, int NJ>
-__device__ __forceinline__ void lora_add32(v16f (&acc)[NI][NJ], const LoraEpi& e, int64_t m0, int64_t m, int64_t n0,
-                                           int64_t n, int lane) {
-    if (n0 >= n || m0 >= m) return;
-    constexpr int kPair = NI > 1 ? 2 : 1;
-    const int r32 = lane & 31, q8 = 8 * (lane >> 5);
-    const char* const tb = reinterpret_cast<const char*>(e.t + m0 * e.parts * e.rp);
-    const uint32_t tpart = (uint32_t)e.rp * 2;
-    int id[NJ];
-    uint32_t toff[NJ], boff[NI];
-#pragma unroll
-    for (int jx = 0; jx < NJ; ++jx) {
-        const int64_t row = m0 + 32 * jx + r32;
-        id[jx] = lora_row(e, row, m);
-        toff[jx] = (uint32_t)((row < m ? row : m - 1) - m0) * e.parts * tpart + q8 * 2;
-    }
-#pragma unroll
-    for (int i = 0; i < NI; ++i) boff[i] = lora_b_off(e, 32 * i + r32, n0, n) + q8 * 2;
-    lora_each(id, [&](int cur) {
-        const char* const bb = lora_b_base(e, cur, n0, n);
-#pragma unroll
-        for (int jx = 0; jx < NJ; ++jx) {
-            if (!__ballot(id[jx] == cur)) continue;
-#pragma unroll
-            for (int i0 = 0; i0 < NI; i0 += kPair) {
-                v16f x[kPair];
-#pragma unroll
-                for (int u = 0; u < kPair; ++u)
-                    if (i0 + u < NI) x[u] = acc[i0 + u][jx];
-                for (int s = 0; s < e.rp; s += 32) {      // two 16-rank steps
-                    bf16x8 bf[2][kPair];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int u = 0; u < kPair; ++u)
-                            if (i0 + u < NI)
-                                bf[h][u] = lora_load(bb, boff[i0 + u] + (s + 16 * h) * 2, s + 16 * h + q8 < e.rank);
-                    for (int p = 0; p < e.parts; ++p) {
-                        bf16x8 tf[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) tf[h] = lora_load(tb, toff[jx] + p * tpart + (s + 16 * h) * 2, true);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int u = 0; u < kPair; ++u)
-                                if (i0 + u < NI) x[u] = mfma32_bf16(bf[h][u], tf[h], x[u]);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < kPair; ++u)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (i0 + u < NI) acc[i0 + u][jx][r] = id[jx] == cur ? x[u][r] : acc[i0 + u][jx][r];
-            }
-        }
-    });
 }
 
 // The end of a ring kernel (all of its loads retired): split k stores this split's raw sums
@@ -596,7 +663,36 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
                     for (int jx = 0; jx < kJX; ++jx) acc[i][jx][4 * gq + r] *= sc;
                 }
             }
-        lora_add32(acc, g.lora, m0 + wm * (TM / 4), g.m, n0 + wn * (TN / 2), g.n, t & 63);
+        int id[kJX];
+#pragma unroll
+        for (int jx = 0; jx < kJX; ++jx) id[jx] = lora_row(g.lora, m0 + wm * (TM / 4) + jx * 32 + r32, g.m);
+        lora_tile<TN, TM, 512>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(t >> 6), t & 63,
+                               [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
+            const int steps = g.lora.rp - c0 > 32 ? 4 : 2;      // 16 ranks each
+#pragma unroll
+            for (int jx = 0; jx < kJX; ++jx) {
+                if (!__ballot(id[jx] == cur)) continue;
+                v16f x[kNI];
+#pragma unroll
+                for (int i = 0; i < kNI; ++i) x[i] = acc[i][jx];
+                for (int h = 0; h < steps; ++h) {
+                    bf16x8 bf[kNI];
+#pragma unroll
+                    for (int i = 0; i < kNI; ++i)
+                        bf[i] = __builtin_bit_cast(bf16x8, lds16(bl + swz128(wn * (TN / 2) + 32 * i + r32, 2 * h + q)));
+                    for (int p = 0; p < g.lora.parts; ++p) {
+                        const bf16x8 tf = __builtin_bit_cast(
+                            bf16x8, lds16(tl + p * TM * 128 + swz128(wm * (TM / 4) + 32 * jx + r32, 2 * h + q)));
+#pragma unroll
+                        for (int i = 0; i < kNI; ++i) x[i] = mfma32_bf16(bf[i], tf, x[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kNI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][jx][r] = id[jx] == cur ? x[i][r] : acc[i][jx][r];
+            }
+        });
     }
     if (g.out_f32) {
         // f32 output: each lane stores its four consecutive n of one m row straight from the
@@ -676,6 +772,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[kRing * kStage];
     // the epilogue stages the bf16 tile in the ring as TM rows of 512 bytes (TN <= 256)
     static_assert(kRing * kStage >= TM * 512, "the epilogue stages the whole bf16 tile in the ring");
+    static_assert(kRing * kStage >= lora_lds<TN, TM, 512>(), "and the adapters' operands");
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wn = wave >> 2, wm = wave & 3;        // wave tile: n TN / 2 x m TM / 4
@@ -809,6 +906,7 @@ __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
     static_assert(kBlocks % 8 == 0 && kRing >= 4 && (kRing - 2) * kLoads < 64, "ring depth and the vmcnt field");
     __shared__ __attribute__((aligned(16))) uint8_t smem[kRing * kStage];
     static_assert(kRing * kStage >= TM * 512, "the epilogue stages the whole bf16 tile in the ring");
+    static_assert(kRing * kStage >= lora_lds<TN, TM, 512>(), "and the adapters' operands");
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wn = wave >> 2, wm = wave & 3;        // wave tile: n TN / 2 x m TM / 4

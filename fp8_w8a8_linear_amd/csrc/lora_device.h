@@ -54,53 +54,4 @@ __device__ __forceinline__ void lora_each(const int (&id)[N], F f) {
     }
 }
 
-// 16 x 16 tiles: acc[i][j] register r of lane l is feature n0 + 16 i + 4 (l / 16) + r of row
-// m0 + 16 j + l % 16. Nothing happens where the tiles lie past the weight or the rows.
-template <int TN, int TM>
-__device__ __forceinline__ void lora_add16(v4f (&acc)[TN][TM], const LoraEpi& e, int64_t m0, int64_t m, int64_t n0,
-                                           int64_t n, int lane) {
-    if (n0 >= n || m0 >= m) return;
-    const int r16 = lane & 15, q8 = 8 * (lane >> 4);
-    const char* const tb = reinterpret_cast<const char*>(e.t + m0 * e.parts * e.rp);
-    const uint32_t tpart = (uint32_t)e.rp * 2;
-    int id[TM];
-    uint32_t toff[TM], boff[TN];
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-        const int64_t row = m0 + 16 * j + r16;
-        id[j] = lora_row(e, row, m);
-        toff[j] = (uint32_t)((row < m ? row : m - 1) - m0) * e.parts * tpart + q8 * 2;
-    }
-#pragma unroll
-    for (int i = 0; i < TN; ++i) boff[i] = lora_b_off(e, 16 * i + r16, n0, n) + q8 * 2;
-    lora_each(id, [&](int cur) {
-        const char* const bb = lora_b_base(e, cur, n0, n);
-        v4f x[TN][TM];
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-            for (int j = 0; j < TM; ++j) x[i][j] = acc[i][j];
-        for (int s = 0; s < e.rp; s += 32) {
-            bf16x8 bf[TN];
-#pragma unroll
-            for (int i = 0; i < TN; ++i) bf[i] = lora_load(bb, boff[i] + s * 2, s + q8 < e.rank);
-            for (int p = 0; p < e.parts; ++p) {
-                bf16x8 tf[TM];
-#pragma unroll
-                for (int j = 0; j < TM; ++j) tf[j] = lora_load(tb, toff[j] + p * tpart + s * 2, true);
-#pragma unroll
-                for (int j = 0; j < TM; ++j)
-#pragma unroll
-                    for (int i = 0; i < TN; ++i) x[i][j] = mfma_bf16(bf[i], tf[j], x[i][j]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-            for (int j = 0; j < TM; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = id[j] == cur ? x[i][j][r] : acc[i][j][r];
-    });
-}
-
 }  // namespace nhm

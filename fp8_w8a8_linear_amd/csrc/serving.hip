@@ -59,6 +59,8 @@ nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64
     if (m > INT_MAX) return fail(NHM_ERR_SHAPE, "m %lld out of range", (long long)m);
     if (!row_adapter) return fail(NHM_ERR_NULL, "row_adapter is NULL");
     if (!aligned(row_adapter, 4)) return fail(NHM_ERR_ALIGN, "row_adapter must be 4-byte aligned");
+    if (w->n * lora->rank >= (int64_t(1) << 30))       // 32-bit byte offsets within one adapter's B
+        return fail(NHM_ERR_UNSUPPORTED, "lora: an adapter's b of 2 GiB or more");
     hipStream_t st = (hipStream_t)stream;
     const LoraWs l = lora_ws(m, w->k, a_type, lora->rank);
     char* wsb = static_cast<char*>(ws);
