@@ -2,13 +2,17 @@
 // same pass over x the e4m3 codes the projection reads. The projection's own kernels add
 // t B_e^T in their epilogues (lora_device.h).
 //
-// Matrix instructions with 16 ranks as the A operand and 16 rows of x as the B operand. A
-// workgroup owns 16 kRows rows and 16 kRanks ranks over all of k, kWaves / kRows waves to each 16
-// rows, which take the 32-wide k-steps round robin, several in flight; their sums meet in LDS
-// in wave order. Rows in a tile may have any adapters: the tile is taken once per distinct
-// adapter, and each time only its rows are stored, so another adapter's values reach nobody
-// else. What it must read is x and the used adapters' A; in decode both are small and latency
-// bounds it, in a long prefill x's bytes do.
+// Matrix instructions with 16 ranks as the A operand and 16 rows of x as the B operand. Rows in a
+// tile may have any adapters: the tile is taken once per distinct adapter, and each time only its rows
+// are stored, so another adapter's values reach nobody else. What it must read is x and the used
+// adapters' A, and with a bf16 x it writes the codes.
+//  * Few rows: latency bounds it. A workgroup owns 16 rows and 16 ranks over all of k, 16 waves
+//    that take the 32-wide k-steps round robin with all their loads in flight (at k = 2,688 one round), and
+//    a share of the tile's distinct adapters.
+//  * Many rows (8,192 or more fill half of the chip): x's bytes bound it. A workgroup owns 64 rows and up to 64 ranks,
+//    8 waves that each take whole 64 x 64 k-steps, so that x and A enter the CU once, the next
+//    step's operands on their way while one is multiplied.
+// The waves' sums meet in LDS and are added in wave order.
 #include "nhm_device.h"
 #include "nhm_internal.h"
 
@@ -31,131 +35,234 @@ __device__ __forceinline__ void store_codes(uint8_t* q, const bf16x8& v, float s
     *reinterpret_cast<uint2*>(q) = c;
 }
 
-constexpr int kUnroll = 4;   // k-steps whose loads are in flight together
+// Ranks r0 .. r0 + 3 of a row (d, unscaled) into its parts.
+__device__ __forceinline__ void store_parts(const LoraDownArgs& g, int64_t row, int r0, const v4f& d, float sc) {
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = r0 + r < g.rank ? d[r] * sc : 0.f;
+    for (int p = 0; p < g.parts; ++p) {
+        const uint32_t lo = f32x2_to_bf16x2(v[0], v[1]), hi = f32x2_to_bf16x2(v[2], v[3]);
+        *reinterpret_cast<uint2*>(g.t + (row * g.parts + p) * g.rp + r0) = make_uint2(lo, hi);
+        const uint32_t h[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)      // what this part leaves (nothing of an infinity or NaN)
+            v[r] = (h[r] & 0x7f80u) == 0x7f80u ? 0.f : v[r] - bf16_to_f32(h[r]);
+    }
+}
 
-// X: uint16_t (bf16) or uint8_t (codes). gridDim: (row tiles, rank groups, shares of the distinct
-// adapters of a tile).
-template <typename X, int kWaves, int kRows, int kRanks>
-__global__ __launch_bounds__(kWaves * 64) void lora_down_kernel(const LoraDownArgs g) {
-    constexpr int KW = kWaves / kRows;       // waves that share a row tile's k
-    __shared__ v4f s_part[kRows][KW][kRanks][64];
+// X: uint16_t (bf16) or uint8_t (codes).
+template <typename X>
+__device__ __forceinline__ const X* x_rows(const LoraDownArgs& g) {
+    if constexpr (sizeof(X) == 2) return g.x;
+    else return g.x_codes;
+}
+
+// ---------------------------------------------------------------- few rows
+
+constexpr int kFewWaves = 16, kFewSteps = 6;   // k-steps of a wave whose loads are in flight together
+
+// gridDim: (row tiles, rank groups, shares of the distinct adapters of a tile).
+template <typename X>
+__global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const LoraDownArgs g) {
+    __shared__ v4f s_part[kFewWaves][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rt = wave / KW, kw = wave % KW;
     const int r16 = lane & 15, q8 = 8 * (lane >> 4);
-    const int64_t row = ((int64_t)blockIdx.x * kRows + rt) * 16 + r16;
+    const int64_t row = (int64_t)blockIdx.x * 16 + r16;
     const int64_t src = row < g.m ? row : g.m - 1;
-    const X* const xr = (sizeof(X) == 2 ? reinterpret_cast<const X*>(g.x) : reinterpret_cast<const X*>(g.x_codes)) + src * g.ld_x;
-    const int rank0 = blockIdx.y * 16 * kRanks;
-    int id = row < g.m ? g.row_adapter[row] : -1;
-    if (id >= g.n_adapters) id = -1;
+    int id = g.row_adapter[src];
+    const X* const xr = x_rows<X>(g) + src * g.ld_x;
     const int steps = (int)((g.k + 31) / 32);
-    const bool quant = sizeof(X) == 2 && g.q && blockIdx.y == 0 && blockIdx.z == 0;
     const float s = *g.a_scale;
-    const bool fast = fast_scale(s);
-    const float rs = quant ? __fdiv_rn(1.0f, s) : 0.f;
+    bool codes = sizeof(X) == 2 && g.q && blockIdx.y == 0 && blockIdx.z == 0;
+    const int r = blockIdx.y * 16 + r16;                         // this lane's rank of A
+    const int64_t arow = r < g.rank ? r : g.rank - 1;
+    const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
 
     // One pass over this wave's steps: the codes if asked, and the products with adapter cur (>= 0).
-    v4f acc[kRanks];
-    auto pass = [&](int cur, bool codes) {
+    auto pass = [&](int cur, bool with_codes) {
+        v4f acc = {0.f, 0.f, 0.f, 0.f};
+        const uint16_t* const ar = g.a + ((int64_t)(cur < 0 ? 0 : cur) * g.rank + arow) * g.k;
+        const bool fast = fast_scale(s);
+        const float rs = with_codes ? __fdiv_rn(1.0f, s) : 0.f;
+        for (int s0 = wave; s0 < steps; s0 += kFewWaves * kFewSteps) {
+            bf16x8 xv[kFewSteps], av[kFewSteps];
 #pragma unroll
-        for (int j = 0; j < kRanks; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
-        const uint16_t* ar[kRanks];
+            for (int u = 0; u < kFewSteps; ++u) {
+                const int kk = (s0 + u * kFewWaves) * 32 + q8;
+                xv[u] = zero;
+                av[u] = zero;
+                if (kk < g.k) {
+                    xv[u] = x8(xr + kk);
+                    if (cur >= 0) av[u] = x8(ar + kk);
+                }
+            }
+            if (with_codes) {
 #pragma unroll
-        for (int j = 0; j < kRanks; ++j) {
+                for (int u = 0; u < kFewSteps; ++u) {
+                    const int kk = (s0 + u * kFewWaves) * 32 + q8;
+                    if (kk < g.k && row < g.m) store_codes(g.q + row * g.k + kk, xv[u], s, rs, fast);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kFewSteps; ++u) acc = mfma_bf16(av[u], xv[u], acc);
+        }
+        return acc;
+    };
+
+    if (row >= g.m || id >= g.n_adapters) id = -1;
+    uint64_t todo = __ballot(id >= 0) & 0xffffu;
+    for (unsigned turn = 0; todo; ++turn) {
+        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        todo &= ~__ballot(id == cur);
+        if (turn % gridDim.z != blockIdx.z) continue;
+        const float sc = (g.scale ? g.scale[cur] : 1.0f) * (sizeof(X) == 1 ? s : 1.0f);
+        s_part[wave][lane] = pass(cur, codes);
+        codes = false;
+        __syncthreads();
+        if (wave == 0) {
+            v4f d = s_part[0][lane];
+#pragma unroll
+            for (int w = 1; w < kFewWaves; ++w) d += s_part[w][lane];
+            if (id == cur) store_parts(g, row, blockIdx.y * 16 + 4 * (lane >> 4), d, sc);
+        }
+        __syncthreads();
+    }
+    if (codes) pass(-1, true);      // no row here has an adapter
+}
+
+// ---------------------------------------------------------------- many rows
+
+constexpr int kManyWaves = 8, kManyRows = 4;   // row tiles of 16 per workgroup
+
+// NR: 16-rank tiles per workgroup. gridDim: (64-row tiles, groups of 16 NR ranks).
+template <typename X, int NR>
+__global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const LoraDownArgs g) {
+    __shared__ v4f s_part[kManyWaves][kManyRows * NR][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, q8 = 8 * (lane >> 4);
+    const int64_t row0 = (int64_t)blockIdx.x * (16 * kManyRows);
+    const int rank0 = blockIdx.y * 16 * NR;
+    const float s = *g.a_scale;
+    const bool fast = fast_scale(s);
+    const float rs = __fdiv_rn(1.0f, s);
+    int id[kManyRows];
+    const X* xr[kManyRows];
+#pragma unroll
+    for (int i = 0; i < kManyRows; ++i) {
+        const int64_t row = row0 + 16 * i + r16;
+        id[i] = row < g.m ? g.row_adapter[row] : -1;
+        if (id[i] >= g.n_adapters) id[i] = -1;
+        xr[i] = x_rows<X>(g) + (row < g.m ? row : g.m - 1) * g.ld_x;
+    }
+    const int full = (int)(g.k / 32);              // whole 32-wide steps; one of 16 may follow
+    const int steps = (int)((g.k + 31) / 32);
+    const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
+    bool codes = sizeof(X) == 2 && g.q && blockIdx.y == 0;
+
+    struct Ops { bf16x8 x[kManyRows], a[NR]; };
+    v4f acc[kManyRows][NR];
+    auto pass = [&](int cur, bool with_codes) {
+        const uint16_t* ar[NR];
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
             const int r = rank0 + 16 * j + r16;
             ar[j] = g.a + ((int64_t)(cur < 0 ? 0 : cur) * g.rank + (r < g.rank ? r : g.rank - 1)) * g.k;
         }
-        for (int s0 = kw; s0 < steps; s0 += KW * kUnroll) {
-            bf16x8 xv[kUnroll], av[kUnroll][kRanks];
-            bool in[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t kk = (int64_t)(s0 + u * KW) * 32 + q8;
-                in[u] = kk < g.k;                               // steps past k read the row's start and count as zeros
-                xv[u] = x8(xr + (in[u] ? kk : 0));
-                if (cur >= 0) {
+        for (int i = 0; i < kManyRows; ++i)
 #pragma unroll
-                    for (int j = 0; j < kRanks; ++j) av[u][j] = x8(ar[j] + (in[u] ? kk : 0));
+            for (int j = 0; j < NR; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        auto load = [&](Ops& o, int step) {
+            const int kk = step * 32 + q8;
+            if (step < full) {
+#pragma unroll
+                for (int i = 0; i < kManyRows; ++i) o.x[i] = x8(xr[i] + kk);
+#pragma unroll
+                for (int j = 0; j < NR; ++j) o.a[j] = x8(ar[j] + kk);
+            } else {                               // the half step at the end, or a step past it: zeros
+#pragma unroll
+                for (int i = 0; i < kManyRows; ++i) o.x[i] = kk < g.k ? x8(xr[i] + kk) : zero;
+#pragma unroll
+                for (int j = 0; j < NR; ++j) o.a[j] = kk < g.k ? x8(ar[j] + kk) : zero;
+            }
+        };
+        auto use = [&](const Ops& o, int step) {
+            const int kk = step * 32 + q8;
+            if (with_codes) {
+#pragma unroll
+                for (int i = 0; i < kManyRows; ++i) {
+                    const int64_t row = row0 + 16 * i + r16;
+                    if (kk < g.k && row < g.m) store_codes(g.q + row * g.k + kk, o.x[i], s, rs, fast);
                 }
             }
+            if (cur >= 0) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                if (codes && in[u] && row < g.m) store_codes(g.q + row * g.k + (int64_t)(s0 + u * KW) * 32 + q8, xv[u], s, rs, fast);
-                if (cur >= 0) {
-                    const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
-                    const bf16x8 xz = in[u] ? xv[u] : zero;
+                for (int i = 0; i < kManyRows; ++i)
 #pragma unroll
-                    for (int j = 0; j < kRanks; ++j) acc[j] = mfma_bf16(in[u] ? av[u][j] : zero, xz, acc[j]);
-                }
+                    for (int j = 0; j < NR; ++j) acc[i][j] = mfma_bf16(o.a[j], o.x[i], acc[i][j]);
             }
+        };
+        Ops o0, o1, o2;
+        load(o0, wave);
+        load(o1, wave + kManyWaves);
+        for (int st = wave; st < steps; st += 3 * kManyWaves) {
+            load(o2, st + 2 * kManyWaves);
+            use(o0, st);
+            load(o0, st + 3 * kManyWaves);
+            use(o1, st + kManyWaves);
+            load(o1, st + 4 * kManyWaves);
+            use(o2, st + 2 * kManyWaves);
         }
     };
 
-    // The distinct adapters among the workgroup's rows: every wave of a row tile sees the same ones,
-    // waves of other row tiles go through empty turns so that the barriers match.
-    __shared__ int s_turns[kRows];
-    uint64_t todo = __ballot(id >= 0) & 0xffffu;
-    int turns = 0;
-    for (uint64_t left = todo; left; ++turns) {
-        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        left &= ~__ballot(id == cur);
-    }
-    int most = turns;
-    if constexpr (kRows > 1) {
-        if (lane == 0 && kw == 0) s_turns[rt] = turns;
-        __syncthreads();
+    uint64_t todo[kManyRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) most = max(most, s_turns[i]);
-    }
-    bool codes = quant;
-    for (int turn = 0; turn < most; ++turn) {
+    for (int i = 0; i < kManyRows; ++i) todo[i] = __ballot(id[i] >= 0) & 0xffffu;
+    for (;;) {
         int cur = -1;
-        if (todo) {
-            cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-            todo &= ~__ballot(id == cur);
-        }
-        if (turn % gridDim.z != blockIdx.z) continue;
-        if (cur >= 0 || codes) pass(cur, codes);
+#pragma unroll
+        for (int i = 0; i < kManyRows; ++i)
+            if (cur < 0 && todo[i]) cur = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo[i]));
+        if (cur < 0) break;
+#pragma unroll
+        for (int i = 0; i < kManyRows; ++i) todo[i] &= ~__ballot(id[i] == cur);
+        pass(cur, codes);
         codes = false;
+        const float sc = (g.scale ? g.scale[cur] : 1.0f) * (sizeof(X) == 1 ? s : 1.0f);
 #pragma unroll
-        for (int j = 0; j < kRanks; ++j) s_part[rt][kw][j][lane] = acc[j];
+        for (int i = 0; i < kManyRows; ++i)
+#pragma unroll
+            for (int j = 0; j < NR; ++j) s_part[wave][i * NR + j][lane] = acc[i][j];
         __syncthreads();
-        // this row tile's waves finish its rank tiles in turn
-        for (int j = kw; j < kRanks && cur >= 0; j += KW) {
-            v4f d = s_part[rt][0][j][lane];
+        for (int t = wave; t < kManyRows * NR; t += kManyWaves) {
+            v4f d = s_part[0][t][lane];
 #pragma unroll
-            for (int w = 1; w < KW; ++w) d += s_part[rt][w][j][lane];
-            const int r0 = rank0 + 16 * j + 4 * (lane >> 4);         // d[r] is rank r0 + r of the row
-            if (id != cur || r0 >= g.rp) continue;
-            const float sc = (g.scale ? g.scale[cur] : 1.0f) * (sizeof(X) == 1 ? s : 1.0f);
-            float v[4];
+            for (int w = 1; w < kManyWaves; ++w) d += s_part[w][t][lane];
+            const int64_t row = row0 + 16 * (t / NR) + r16;
+            const int r0 = rank0 + 16 * (t % NR) + 4 * (lane >> 4);
+            int mine = -1;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = r0 + r < g.rank ? d[r] * sc : 0.f;
-            for (int p = 0; p < g.parts; ++p) {
-                const uint32_t lo = f32x2_to_bf16x2(v[0], v[1]), hi = f32x2_to_bf16x2(v[2], v[3]);
-                *reinterpret_cast<uint2*>(g.t + (row * g.parts + p) * g.rp + r0) = make_uint2(lo, hi);
-                const uint32_t h[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
-#pragma unroll
-                for (int r = 0; r < 4; ++r)      // what this part leaves (nothing of an infinity or NaN)
-                    v[r] = (h[r] & 0x7f80u) == 0x7f80u ? 0.f : v[r] - bf16_to_f32(h[r]);
-            }
+            for (int i = 0; i < kManyRows; ++i) mine = i == t / NR ? id[i] : mine;
+            if (mine == cur && r0 < g.rp) store_parts(g, row, r0, d, sc);
         }
         __syncthreads();
     }
-    if (codes && (blockIdx.z == 0)) pass(-1, true);      // no row here has an adapter
+    if (codes) pass(-1, true);      // no row here has an adapter
 }
 
 template <typename X>
 static void launch_down(const LoraDownArgs& g, hipStream_t st) {
     const int64_t tiles = (g.m + 15) / 16;
-    const unsigned groups = (unsigned)(g.rp / 16);
     if (tiles >= 512) {
-        lora_down_kernel<X, 8, 4, 4><<<dim3((unsigned)((tiles + 3) / 4), (groups + 3) / 4), dim3(512), 0, st>>>(g);
+        const dim3 grid((unsigned)((tiles + kManyRows - 1) / kManyRows), (unsigned)((g.rp + 63) / 64));
+        if (g.rp == 32) lora_down_many_kernel<X, 2><<<grid, dim3(kManyWaves * 64), 0, st>>>(g);
+        else lora_down_many_kernel<X, 4><<<grid, dim3(kManyWaves * 64), 0, st>>>(g);
         return;
     }
+    const unsigned groups = (unsigned)(g.rp / 16);
     int64_t z = 1024 / (tiles * groups);
     z = z < 1 ? 1 : z > 16 ? 16 : z;
-    lora_down_kernel<X, 16, 1, 1><<<dim3((unsigned)tiles, groups, (unsigned)z), dim3(1024), 0, st>>>(g);
+    lora_down_few_kernel<X><<<dim3((unsigned)tiles, groups, (unsigned)z), dim3(kFewWaves * 64), 0, st>>>(g);
 }
 
 nhm_status launch_lora_down(const LoraDownArgs& g, hipStream_t st) {
