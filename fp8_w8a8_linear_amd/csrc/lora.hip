@@ -61,29 +61,51 @@ __device__ __forceinline__ const X* x_rows(const LoraDownArgs& g) {
 
 constexpr int kFewWaves = 16, kFewSteps = 6;   // k-steps of a wave whose loads are in flight together
 
-// gridDim: (row tiles, rank groups, shares of the distinct adapters of a tile).
+// gridDim: (row tiles, rank groups, shares + extra): blockIdx.z < shares takes every shares-th
+// distinct adapter of the tile; the workgroups past that form the tile's codes, one or a few vectors a
+// thread (in the same workgroups as the products they made the code long and the launch slow: 9.2 us
+// for 8 rows).
 template <typename X>
-__global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const LoraDownArgs g) {
+__global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const LoraDownArgs g, int shares) {
     __shared__ v4f s_part[kFewWaves][64];
+    const int64_t tile0 = (int64_t)blockIdx.x * 16;
+    if constexpr (sizeof(X) == 2) {
+        if ((int)blockIdx.z >= shares) {
+            const int per_row = (int)(g.k / 8);
+            const int total = (int)min((int64_t)16, g.m - tile0) * per_row;
+            const float s = *g.a_scale;
+            const float rs = __fdiv_rn(1.0f, s);
+            const bool fast = fast_scale(s);
+            const int stride = (int)(gridDim.z - shares) * gridDim.y * kFewWaves * 64;
+            for (int v = ((blockIdx.z - shares) * gridDim.y + blockIdx.y) * kFewWaves * 64 + threadIdx.x; v < total; v += stride) {
+                const int64_t row = tile0 + v / per_row, c = (int64_t)(v % per_row) * 8;
+                store_codes(g.q + row * g.k + c, x8(g.x + row * g.ld_x + c), s, rs, fast);
+            }
+            return;
+        }
+    }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q8 = 8 * (lane >> 4);
-    const int64_t row = (int64_t)blockIdx.x * 16 + r16;
+    const int64_t row = tile0 + r16;
     const int64_t src = row < g.m ? row : g.m - 1;
     int id = g.row_adapter[src];
     const X* const xr = x_rows<X>(g) + src * g.ld_x;
     const int steps = (int)((g.k + 31) / 32);
-    const float s = *g.a_scale;
-    bool codes = sizeof(X) == 2 && g.q && blockIdx.y == 0 && blockIdx.z == 0;
     const int r = blockIdx.y * 16 + r16;                         // this lane's rank of A
     const int64_t arow = r < g.rank ? r : g.rank - 1;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
-
-    // One pass over this wave's steps: the codes if asked, and the products with adapter cur (>= 0).
-    auto pass = [&](int cur, bool with_codes) {
+    if (row >= g.m || id >= g.n_adapters) id = -1;
+    uint64_t todo = __ballot(id >= 0) & 0xffffu;
+    for (int turn = 0; todo; ++turn) {
+        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        todo &= ~__ballot(id == cur);
+        if (turn % shares != (int)blockIdx.z) continue;
+        // the scales through the scalar cache, and no branch that would wait for them
+        typedef const __attribute__((address_space(4))) float* scalar_f32;
+        const float s = *reinterpret_cast<scalar_f32>(reinterpret_cast<uintptr_t>(g.a_scale));
+        const float se = *reinterpret_cast<scalar_f32>(reinterpret_cast<uintptr_t>(g.scale ? g.scale + cur : g.a_scale));
         v4f acc = {0.f, 0.f, 0.f, 0.f};
-        const uint16_t* const ar = g.a + ((int64_t)(cur < 0 ? 0 : cur) * g.rank + arow) * g.k;
-        const bool fast = fast_scale(s);
-        const float rs = with_codes ? __fdiv_rn(1.0f, s) : 0.f;
+        const uint16_t* const ar = g.a + ((int64_t)cur * g.rank + arow) * g.k;
         for (int s0 = wave; s0 < steps; s0 += kFewWaves * kFewSteps) {
             bf16x8 xv[kFewSteps], av[kFewSteps];
 #pragma unroll
@@ -92,42 +114,24 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
                 xv[u] = zero;
                 av[u] = zero;
                 if (kk < g.k) {
+                    av[u] = x8(ar + kk);
                     xv[u] = x8(xr + kk);
-                    if (cur >= 0) av[u] = x8(ar + kk);
-                }
-            }
-            if (with_codes) {
-#pragma unroll
-                for (int u = 0; u < kFewSteps; ++u) {
-                    const int kk = (s0 + u * kFewWaves) * 32 + q8;
-                    if (kk < g.k && row < g.m) store_codes(g.q + row * g.k + kk, xv[u], s, rs, fast);
                 }
             }
 #pragma unroll
             for (int u = 0; u < kFewSteps; ++u) acc = mfma_bf16(av[u], xv[u], acc);
         }
-        return acc;
-    };
-
-    if (row >= g.m || id >= g.n_adapters) id = -1;
-    uint64_t todo = __ballot(id >= 0) & 0xffffu;
-    for (unsigned turn = 0; todo; ++turn) {
-        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        todo &= ~__ballot(id == cur);
-        if (turn % gridDim.z != blockIdx.z) continue;
-        const float sc = (g.scale ? g.scale[cur] : 1.0f) * (sizeof(X) == 1 ? s : 1.0f);
-        s_part[wave][lane] = pass(cur, codes);
-        codes = false;
+        s_part[wave][lane] = acc;
         __syncthreads();
         if (wave == 0) {
             v4f d = s_part[0][lane];
 #pragma unroll
             for (int w = 1; w < kFewWaves; ++w) d += s_part[w][lane];
+            const float sc = (g.scale ? se : 1.0f) * (sizeof(X) == 1 ? s : 1.0f);
             if (id == cur) store_parts(g, row, blockIdx.y * 16 + 4 * (lane >> 4), d, sc);
         }
         __syncthreads();
     }
-    if (codes) pass(-1, true);      // no row here has an adapter
 }
 
 // ---------------------------------------------------------------- many rows
@@ -262,7 +266,11 @@ static void launch_down(const LoraDownArgs& g, hipStream_t st) {
     const unsigned groups = (unsigned)(g.rp / 16);
     int64_t z = 1024 / (tiles * groups);
     z = z < 1 ? 1 : z > 16 ? 16 : z;
-    lora_down_few_kernel<X><<<dim3((unsigned)tiles, groups, (unsigned)z), dim3(kFewWaves * 64), 0, st>>>(g);
+    // a vector of eight codes per thread, up to as many workgroups again
+    const int64_t vecs = sizeof(X) == 2 && g.q ? (g.k / 8 * 16 + kFewWaves * 64 - 1) / (kFewWaves * 64) : 0;
+    int64_t extra = (vecs + groups - 1) / groups;
+    extra = extra > z ? z : extra;
+    lora_down_few_kernel<X><<<dim3((unsigned)tiles, groups, (unsigned)(z + extra)), dim3(kFewWaves * 64), 0, st>>>(g, (int)z);
 }
 
 nhm_status launch_lora_down(const LoraDownArgs& g, hipStream_t st) {
