@@ -142,21 +142,32 @@ constexpr uint32_t kOutOfRange = 0x80000000u;   // past every buffer range used 
 
 // ---------------------------------------------------------------- the adapters' part of a tile
 
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// 32x32x16 bf16 MFMA, f32 accumulate: lane l supplies row (l % 32) of A and column (l % 32) of
+// B as 8 consecutive k of the 16-k step chosen by l / 32; the accumulator layout is that of
+// the 32x32x64 e4m3 MFMA.
+__device__ __forceinline__ v16f mfma32_bf16(const bf16x8& a, const bf16x8& b, const v16f& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+
 // After a tile's k loop: for each distinct adapter among the tile's TM rows, compute(cur, c0, tl, bl)
 // adds the products of 64 ranks from c0 on. tl: the rows' t, part p at tl + p TM 128, 128 bytes per row
 // under swz128; bl: the tile's TN features of B_cur likewise (zeros past the rank, the rows and the
-// features). t is loaded once per 64 ranks, B_cur of the next adapter while this one is worked on;
-// both go straight to LDS and are read there by every wave that needs them, where loads into
-// registers paid a round trip to L2 per step (15,360 x 10,304 x 2,688 at rank 64: 723 us against
-// 500 without adapters). Every wave of the workgroup calls this, with LDS that nobody reads any more.
-template <int TN, int TM, int NT>
-constexpr int lora_lds() { return 3 * TM * 128 + 2 * TN * 128; }
+// features). t is loaded once per 64 ranks; the next adapters' B are on their way, as many as the LDS
+// holds, while one is worked on. Both go straight to LDS and are read there by every wave that
+// needs them, where loads into registers paid a round trip to L2 per step. Every wave of the
+// workgroup calls this, with LDS that nobody reads any more.
+// B buffers beside three parts of t in LDS bytes: at least two.
+template <int TN, int TM>
+constexpr int lora_bufs(int lds) { return (lds - 3 * TM * 128) / (TN * 128); }
 
-template <int TN, int TM, int NT, typename F>
+template <int TN, int TM, int NT, int LDS, typename F>
 __device__ __forceinline__ void lora_tile(const LoraEpi& e, int64_t m0, int64_t m, int64_t n0, int64_t n, uint8_t* smem,
                                           int wave, int lane, F compute) {
-    constexpr int kIds = TM / 64, kWaves = NT / 64;
-    static_assert(TM % 64 == 0 && TN % 8 == 0, "tile shape");
+    constexpr int kIds = TM / 64, kWaves = NT / 64, kBufs = lora_bufs<TN, TM>(LDS), kB = TN / 8 / kWaves;
+    static_assert(TM % 64 == 0 && TN % (8 * kWaves) == 0 && kBufs >= 2 && (kBufs - 2) * kB < 64, "tile shape and the vmcnt field");
     uint64_t all[kIds], any = 0;
     int id[kIds];
 #pragma unroll
@@ -166,7 +177,7 @@ __device__ __forceinline__ void lora_tile(const LoraEpi& e, int64_t m0, int64_t 
         any |= all[j];
     }
     if (any == 0) return;
-    uint8_t* const bl = smem + e.parts * TM * 128;
+    uint8_t* const bl = smem + 3 * TM * 128;
     const int lr = lane >> 3;                                        // row of an 8-row block of 1 KB
     // descriptors and the adapter at hand are the same in every lane; the compiler is told
     auto uniform = [](i32x4 r) {
@@ -192,59 +203,135 @@ __device__ __forceinline__ void lora_tile(const LoraEpi& e, int64_t m0, int64_t 
                 dma16(trs, smem + p * TM * 128 + blk * 1024,
                       rank < e.rp && m0 + row < m ? (uint32_t)(((row * e.parts + p) * e.rp + rank) * 2) : kOutOfRange);
             }
-        auto stage_b = [&](int cur, int buf) {
-            const i32x4 brs = uniform(buffer_desc(e.b + ((int64_t)cur * n + n0) * e.rank, (n - n0) * e.rank * 2));
-            for (int blk = wave; blk < TN / 8; blk += kWaves) {
+        auto stage_b = [&](int cur, int buf) {      // cur < 0: zeros, so that every stage is kB loads
+            const i32x4 brs = uniform(buffer_desc(e.b + ((int64_t)max(cur, 0) * n + n0) * e.rank, (n - n0) * e.rank * 2));
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                const int blk = wave + u * kWaves;
                 const int row = blk * 8 + lr, rank = c0 + 8 * ((lane & 7) ^ (row & 7) ^ ((row >> 3) & 1));
                 dma16(brs, bl + buf * TN * 128 + blk * 1024,
-                      rank < e.rank && n0 + row < n ? (uint32_t)((row * e.rank + rank) * 2) : kOutOfRange);
+                      cur >= 0 && rank < e.rank && n0 + row < n ? (uint32_t)((row * e.rank + rank) * 2) : kOutOfRange);
             }
         };
-        uint64_t todo[kIds];
+        // two walks over the distinct adapters: the loads' and, kBufs - 1 behind it, the products'
+        uint64_t ahead[kIds], todo[kIds];
 #pragma unroll
-        for (int j = 0; j < kIds; ++j) todo[j] = all[j];
-        int cur = next(todo), buf = 0;
-        stage_b(cur, 0);
-        while (cur >= 0) {
-            wait_vmcnt<0>();         // this wave's share of t and B_cur
-            __syncthreads();         // everyone's; and everyone is done with the other buffer
-            const int nxt = next(todo);
-            if (nxt >= 0) stage_b(nxt, buf ^ 1);
+        for (int j = 0; j < kIds; ++j) ahead[j] = todo[j] = all[j];
+        for (int b = 0; b < kBufs - 1; ++b) stage_b(next(ahead), b);
+        int buf = 0;
+        for (int cur = next(todo); cur >= 0; cur = next(todo)) {
+            wait_vmcnt<(kBufs - 2) * kB>();      // this wave's share of t and B_cur
+            __syncthreads();                     // everyone's; and everyone is done with the buffer staged next
+            stage_b(next(ahead), buf == 0 ? kBufs - 1 : buf - 1);
             compute(cur, c0, smem, bl + buf * TN * 128);
-            cur = nxt;
-            buf ^= 1;
+            buf = buf + 1 == kBufs ? 0 : buf + 1;
         }
+        wait_vmcnt<0>();             // the stages past the last adapter
     }
     __syncthreads();                 // the LDS may be written again
 }
 
 // compute() of waves with 16 x 16 tiles: acc[i][j] register r of lane l is feature nw + 16 i +
-// 4 (l / 16) + r of row mw + 16 j + l % 16 of the workgroup's tile.
+// 4 (l / 16) + r of row mw + 16 j + l % 16 of the workgroup's tile. The parts are written out: as a
+// loop their sums were carried around in copies that a read overtook (wrong sums in one register).
 template <int TM, int TNW, int TMW>
 __device__ __forceinline__ void lora_mma16(v4f (&acc)[TNW][TMW], const LoraEpi& e, const int (&id)[TMW], int cur, int c0,
                                            const uint8_t* tl, const uint8_t* bl, int mw, int nw, int lane) {
+    asm volatile("" : "+v"(lane));                 // addresses formed here, not held over the whole kernel
     const int r16 = lane & 15, q = lane >> 4;
-    const int steps = e.rp - c0 > 32 ? 2 : 1;      // 32 ranks each
-#pragma unroll
-    for (int j = 0; j < TMW; ++j) {
-        if (!__ballot(id[j] == cur)) continue;
+    auto mma = [&](int j, int s) {                 // 32 ranks of row tile j
         v4f x[TNW];
+        bf16x8 bf[TNW];
+        const uint8_t* const ta = tl + swz128(mw + 16 * j + r16, 4 * s + q);
+        const bf16x8 t0 = __builtin_bit_cast(bf16x8, lds16(ta)), t1 = __builtin_bit_cast(bf16x8, lds16(ta + TM * 128));
 #pragma unroll
-        for (int i = 0; i < TNW; ++i) x[i] = acc[i][j];
-        for (int s = 0; s < steps; ++s) {
-            bf16x8 bf[TNW];
+        for (int i = 0; i < TNW; ++i) bf[i] = __builtin_bit_cast(bf16x8, lds16(bl + swz128(nw + 16 * i + r16, 4 * s + q)));
 #pragma unroll
-            for (int i = 0; i < TNW; ++i) bf[i] = __builtin_bit_cast(bf16x8, lds16(bl + swz128(nw + 16 * i + r16, 4 * s + q)));
-            for (int p = 0; p < e.parts; ++p) {
-                const bf16x8 tf = __builtin_bit_cast(bf16x8, lds16(tl + p * TM * 128 + swz128(mw + 16 * j + r16, 4 * s + q)));
+        for (int i = 0; i < TNW; ++i) x[i] = mfma_bf16(bf[i], t1, mfma_bf16(bf[i], t0, acc[i][j]));
+        if (e.parts > 2) {
+            const bf16x8 t2 = __builtin_bit_cast(bf16x8, lds16(ta + 2 * TM * 128));
 #pragma unroll
-                for (int i = 0; i < TNW; ++i) x[i] = mfma_bf16(bf[i], tf, x[i]);
-            }
+            for (int i = 0; i < TNW; ++i) x[i] = mfma_bf16(bf[i], t2, x[i]);
         }
 #pragma unroll
         for (int i = 0; i < TNW; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[i][j][r] = id[j] == cur ? x[i][r] : acc[i][j][r];
+    };
+#pragma unroll
+    for (int j = 0; j < TMW; ++j) {
+        if (!__ballot(id[j] == cur)) continue;
+        mma(j, 0);
+        if (e.rp - c0 > 32) mma(j, 1);
+    }
+}
+
+// The same of waves with 32 x 32 tiles: row mw + 32 jx + l % 32. Where every row of the wave has the
+// adapter (long runs), the products go straight into the accumulators; else feature tiles in pairs, into
+// copies that are selected from.
+template <int TM, int NI, int NJ>
+__device__ __forceinline__ void lora_mma32(v16f (&acc)[NI][NJ], const LoraEpi& e, const int (&id)[NJ], int cur, int c0,
+                                           const uint8_t* tl, const uint8_t* bl, int mw, int nw, int lane) {
+    asm volatile("" : "+v"(lane));                 // addresses formed here, not held over the whole kernel
+    const int r32 = lane & 31, q = lane >> 5;
+    const int steps = e.rp - c0 > 32 ? 4 : 2;      // 16 ranks each
+    auto tf = [&](int jx, int h, int p) {
+        return __builtin_bit_cast(bf16x8, lds16(tl + p * TM * 128 + swz128(mw + 32 * jx + r32, 2 * h + q)));
+    };
+    auto bf = [&](int i, int h) { return __builtin_bit_cast(bf16x8, lds16(bl + swz128(nw + 32 * i + r32, 2 * h + q))); };
+    bool mine = true;
+#pragma unroll
+    for (int jx = 0; jx < NJ; ++jx) mine = mine && id[jx] == cur;
+    if (__ballot(!mine) == 0) {
+        for (int h = 0; h < steps; ++h) {
+            bf16x8 b[NI], t[NJ];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) b[i] = bf(i, h);
+            auto part = [&](int p) {
+#pragma unroll
+                for (int jx = 0; jx < NJ; ++jx) t[jx] = tf(jx, h, p);
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+#pragma unroll
+                    for (int jx = 0; jx < NJ; ++jx) acc[i][jx] = mfma32_bf16(b[i], t[jx], acc[i][jx]);
+            };
+            part(0);
+            part(1);
+            if (e.parts > 2) part(2);
+        }
+        return;
+    }
+    constexpr int kPair = NI * NJ > 6 ? 1 : 2;     // what fits beside the accumulators
+#pragma unroll
+    for (int jx = 0; jx < NJ; ++jx) {
+        if (!__ballot(id[jx] == cur)) continue;
+#pragma unroll
+        for (int i0 = 0; i0 < NI; i0 += kPair) {
+            v16f x[kPair];
+#pragma unroll
+            for (int u = 0; u < kPair; ++u)
+                if (i0 + u < NI) x[u] = acc[i0 + u][jx];
+            for (int h = 0; h < steps; ++h) {
+                bf16x8 b[kPair];
+#pragma unroll
+                for (int u = 0; u < kPair; ++u)
+                    if (i0 + u < NI) b[u] = bf(i0 + u, h);
+                auto part = [&](int p) {
+                    const bf16x8 t = tf(jx, h, p);
+#pragma unroll
+                    for (int u = 0; u < kPair; ++u)
+                        if (i0 + u < NI) x[u] = mfma32_bf16(b[u], t, x[u]);
+                };
+                part(0);
+                part(1);
+                if (e.parts > 2) part(2);
+            }
+#pragma unroll
+            for (int u = 0; u < kPair; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (i0 + u < NI) acc[i0 + u][jx][r] = id[jx] == cur ? x[u][r] : acc[i0 + u][jx][r];
+        }
     }
 }
 
@@ -262,8 +349,10 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     constexpr int U = D % 2 == 0 ? D : 2 * D;   // loop unroll: step kt's registers are slot kt % D
     constexpr int LA = BM * 8 / 256;   // 16-byte chunks of the activation tile per thread
     static_assert(WN % 16 == 0 && BM % 32 == 0, "tile shape");
-    // the activation tiles, and after the k loop the adapters' operands
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kLora ? lora_lds<BN, BM, 256>() : 3 * BM * 128];
+    // the activation tiles, and after the k loop the adapters' operands (with adapters: room for B of
+    // eight at a time, whose round trips would follow one another in a batch of many adapters)
+    constexpr int kLds = kLora ? 3 * BM * 128 + 8 * BN * 128 : 3 * BM * 128;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
     uint8_t (&sA)[3][BM * 128] = *reinterpret_cast<uint8_t (*)[3][BM * 128]>(smem);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane >> 4, r16 = lane & 15;
     // Tile order: blocks are dealt to the 8 XCDs round robin (block b runs on XCD b % 8),
@@ -385,7 +474,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
         int id[TM];
 #pragma unroll
         for (int j = 0; j < TM; ++j) id[j] = lora_row(g.lora, m0 + j * 16 + r16, g.m);
-        lora_tile<BN, BM, 256>(g.lora, m0, g.m, (int64_t)pan * PW, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+        lora_tile<BN, BM, 256, kLds>(g.lora, m0, g.m, (int64_t)pan * PW, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
                                [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
                                    lora_mma16<BM>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
                                });
@@ -436,7 +525,8 @@ __device__ __forceinline__ v8i lds_operand(const uint8_t* s, int row, int q) {
 template <bool kExact, bool kLora>
 __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
     // two stages of both operands, and after the k loop the adapters' operands
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kLora ? lora_lds<kTile, kTile, 256>() : 4 * kTile * kTile];
+    constexpr int kLds = kLora ? 3 * kTile * 128 + 4 * kTile * 128 : 4 * kTile * kTile;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
     uint8_t (&sW)[2][kTile * kTile] = *reinterpret_cast<uint8_t (*)[2][kTile * kTile]>(smem);
     uint8_t (&sA)[2][kTile * kTile] = *reinterpret_cast<uint8_t (*)[2][kTile * kTile]>(smem + 2 * kTile * kTile);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -503,7 +593,7 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
         int id[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) id[j] = lora_row(g.lora, m0 + wm * 64 + j * 16 + r16, g.m);
-        lora_tile<kTile, kTile, 256>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+        lora_tile<kTile, kTile, 256, kLds>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
                                      [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
                                          lora_mma16<kTile>(acc, g.lora, id, cur, c0, tl, bl, wm * 64, wn * 64, lane);
                                      });
@@ -526,7 +616,6 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
 
 // ---------------------------------------------------------------- 256 x 256 tile kernel
 
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -550,13 +639,6 @@ struct RingShape {
 
 __device__ __forceinline__ v16f mfma32_e4m3(const v8i& a, const v8i& b, const v16f& c) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-
-// 32x32x16 bf16 MFMA, f32 accumulate: lane l supplies row (l % 32) of A and column (l % 32) of
-// B as 8 consecutive k of the 16-k step chosen by l / 32; the accumulator layout is that of
-// the 32x32x64 e4m3 MFMA.
-__device__ __forceinline__ v16f mfma32_bf16(const bf16x8& a, const bf16x8& b, const v16f& c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
 // One 64-deep k-step of a wave's NI x NJ grid of 32 x 32 tiles (weight fragments w, activation
@@ -621,7 +703,7 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& g, int64_t& m0, int64_
 // The end of a ring kernel (all of its loads retired): split k stores this split's raw sums
 // to the partial buffer; f32 output goes straight from the accumulators; bf16 output is
 // scaled, staged through the ring as TM rows of 512 bytes and stored row by row.
-template <int TN, int TM, bool kLora>
+template <int TN, int TM, bool kLora, int LDS>
 __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN / 64][TM / 128], int64_t m0,
                                               int64_t n0, int ks, uint8_t* smem, int t, int wn, int wm, int r32,
                                               int q) {
@@ -651,47 +733,33 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
     }
     const float sa = *g.a_scale;
     if constexpr (kLora) {
+        // scaled first; four consecutive features' scales in one load (zeros past n), a feature tile at a time
+        const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)g.w_scale, (short)0, g.ws_step != 0 ? (int)(g.n * 4) : 4, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < kNI; ++i)
+        for (int i = 0; i < kNI; ++i) {
+            v4u raw[4];
 #pragma unroll
             for (int gq = 0; gq < 4; ++gq) {
                 const int64_t nb = n0 + wn * (TN / 2) + i * 32 + gq * 8 + q * 4;
+                raw[gq] = __builtin_amdgcn_raw_buffer_load_b128(srs, g.ws_step != 0 ? (uint32_t)(nb * 4) : 0u, 0, 0);
+            }
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float sc = sa * g.w_scale[(nb + r < g.n ? nb + r : g.n - 1) * g.ws_step];
+                    const float sc = sa * __uint_as_float(g.ws_step != 0 ? raw[gq][r] : raw[gq][0]);
 #pragma unroll
                     for (int jx = 0; jx < kJX; ++jx) acc[i][jx][4 * gq + r] *= sc;
                 }
-            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
         int id[kJX];
 #pragma unroll
         for (int jx = 0; jx < kJX; ++jx) id[jx] = lora_row(g.lora, m0 + wm * (TM / 4) + jx * 32 + r32, g.m);
-        lora_tile<TN, TM, 512>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(t >> 6), t & 63,
+        lora_tile<TN, TM, 512, LDS>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(t >> 6), t & 63,
                                [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
-            const int steps = g.lora.rp - c0 > 32 ? 4 : 2;      // 16 ranks each
-#pragma unroll
-            for (int jx = 0; jx < kJX; ++jx) {
-                if (!__ballot(id[jx] == cur)) continue;
-                v16f x[kNI];
-#pragma unroll
-                for (int i = 0; i < kNI; ++i) x[i] = acc[i][jx];
-                for (int h = 0; h < steps; ++h) {
-                    bf16x8 bf[kNI];
-#pragma unroll
-                    for (int i = 0; i < kNI; ++i)
-                        bf[i] = __builtin_bit_cast(bf16x8, lds16(bl + swz128(wn * (TN / 2) + 32 * i + r32, 2 * h + q)));
-                    for (int p = 0; p < g.lora.parts; ++p) {
-                        const bf16x8 tf = __builtin_bit_cast(
-                            bf16x8, lds16(tl + p * TM * 128 + swz128(wm * (TM / 4) + 32 * jx + r32, 2 * h + q)));
-#pragma unroll
-                        for (int i = 0; i < kNI; ++i) x[i] = mfma32_bf16(bf[i], tf, x[i]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kNI; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][jx][r] = id[jx] == cur ? x[i][r] : acc[i][jx][r];
-            }
+            lora_mma32<TM>(acc, g.lora, id, cur, c0, tl, bl, wm * (TM / 4), wn * (TN / 2), t & 63);
         });
     }
     if (g.out_f32) {
@@ -772,7 +840,6 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[kRing * kStage];
     // the epilogue stages the bf16 tile in the ring as TM rows of 512 bytes (TN <= 256)
     static_assert(kRing * kStage >= TM * 512, "the epilogue stages the whole bf16 tile in the ring");
-    static_assert(kRing * kStage >= lora_lds<TN, TM, 512>(), "and the adapters' operands");
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wn = wave >> 2, wm = wave & 3;        // wave tile: n TN / 2 x m TM / 4
@@ -886,7 +953,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     }
     wait_vmcnt<0>();   // the ring's trailing loads (past k) before the ring is reused
 
-    ring_epilogue<TN, TM, kLora>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
+    ring_epilogue<TN, TM, kLora, kRing * kStage>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
 }
 
 
@@ -906,7 +973,6 @@ __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
     static_assert(kBlocks % 8 == 0 && kRing >= 4 && (kRing - 2) * kLoads < 64, "ring depth and the vmcnt field");
     __shared__ __attribute__((aligned(16))) uint8_t smem[kRing * kStage];
     static_assert(kRing * kStage >= TM * 512, "the epilogue stages the whole bf16 tile in the ring");
-    static_assert(kRing * kStage >= lora_lds<TN, TM, 512>(), "and the adapters' operands");
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wn = wave >> 2, wm = wave & 3;        // wave tile: n TN / 2 x m TM / 4
@@ -996,7 +1062,7 @@ __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     }
     wait_vmcnt<0>();   // the ring's trailing loads (past k) before the ring is reused
-    ring_epilogue<TN, TM, kLora>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
+    ring_epilogue<TN, TM, kLora, kRing * kStage>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
 }
 
 // Split-k epilogue: out[m, n] = (sum over s of part[s, m, n], in split order) * a_scale *
