@@ -50,7 +50,7 @@ struct GemmArgs {
     float* part = nullptr;
     int ws_step = 1;    // weight scale index step: 1 per channel, 0 per tensor
     int panel_rows = 0; // panel kernel: weight rows per panel (0: all of its waves' rows)
-    LoraEpi lora;       // the kernels with adapters (kLora) only
+    LoraEpi lora;       // the kernels with adapters only: kLora 1 (bf16 output, t in two parts) or 2 (f32, three)
 };
 
 // Row r of a 128-byte-wide LDS tile holds its 16-byte chunk c at slot c ^ (r & 7):
@@ -163,16 +163,25 @@ __device__ __forceinline__ v16f mfma32_bf16(const bf16x8& a, const bf16x8& b, co
 template <int TN, int TM>
 constexpr int lora_bufs(int lds) { return (lds - 3 * TM * 128) / (TN * 128); }
 
+// rows: the tile's rows' adapters (LoraRows, read ahead of the k loop); features at or past nend are zeros.
+template <int TM>
+struct LoraRows {
+    int id[TM / 64];             // of row 64 j + lane
+    __device__ __forceinline__ void load(const LoraEpi& e, int64_t m0, int64_t m, int lane) {
+#pragma unroll
+        for (int j = 0; j < TM / 64; ++j) id[j] = lora_row(e, m0 + 64 * j + lane, m);
+    }
+};
+
 template <int TN, int TM, int NT, int LDS, typename F>
-__device__ __forceinline__ void lora_tile(const LoraEpi& e, int64_t m0, int64_t m, int64_t n0, int64_t n, uint8_t* smem,
-                                          int wave, int lane, F compute) {
+__device__ __forceinline__ void lora_tile(const LoraEpi& e, const LoraRows<TM>& rows, int64_t m0, int64_t m, int64_t n0,
+                                          int64_t n, int64_t nend, uint8_t* smem, int wave, int lane, F compute) {
     constexpr int kIds = TM / 64, kWaves = NT / 64, kBufs = lora_bufs<TN, TM>(LDS), kB = TN / 8 / kWaves;
     static_assert(TM % 64 == 0 && TN % (8 * kWaves) == 0 && kBufs >= 2 && (kBufs - 2) * kB < 64, "tile shape and the vmcnt field");
     uint64_t all[kIds], any = 0;
-    int id[kIds];
+    const int (&id)[kIds] = rows.id;
 #pragma unroll
     for (int j = 0; j < kIds; ++j) {
-        id[j] = lora_row(e, m0 + 64 * j + lane, m);
         all[j] = __ballot(id[j] >= 0);
         any |= all[j];
     }
@@ -210,7 +219,7 @@ __device__ __forceinline__ void lora_tile(const LoraEpi& e, int64_t m0, int64_t 
                 const int blk = wave + u * kWaves;
                 const int row = blk * 8 + lr, rank = c0 + 8 * ((lane & 7) ^ (row & 7) ^ ((row >> 3) & 1));
                 dma16(brs, bl + buf * TN * 128 + blk * 1024,
-                      cur >= 0 && rank < e.rank && n0 + row < n ? (uint32_t)((row * e.rank + rank) * 2) : kOutOfRange);
+                      cur >= 0 && rank < e.rank && n0 + row < nend ? (uint32_t)((row * e.rank + rank) * 2) : kOutOfRange);
             }
         };
         // two walks over the distinct adapters: the loads' and, kBufs - 1 behind it, the products'
@@ -232,31 +241,32 @@ __device__ __forceinline__ void lora_tile(const LoraEpi& e, int64_t m0, int64_t 
 }
 
 // compute() of waves with 16 x 16 tiles: acc[i][j] register r of lane l is feature nw + 16 i +
-// 4 (l / 16) + r of row mw + 16 j + l % 16 of the workgroup's tile. The parts are written out: as a
-// loop their sums were carried around in copies that a read overtook (wrong sums in one register).
-template <int TM, int TNW, int TMW>
+// 4 (l / 16) + r of row mw + 16 j + l % 16 of the workgroup's tile. The products are formed apart and
+// added in the lanes they belong to; kParts matrix instructions per 32 ranks, written out (as a loop over the
+// parts their sums were carried around in copies that a read overtook: wrong sums in one register).
+template <int TM, int kParts, int TNW, int TMW>
 __device__ __forceinline__ void lora_mma16(v4f (&acc)[TNW][TMW], const LoraEpi& e, const int (&id)[TMW], int cur, int c0,
                                            const uint8_t* tl, const uint8_t* bl, int mw, int nw, int lane) {
     asm volatile("" : "+v"(lane));                 // addresses formed here, not held over the whole kernel
     const int r16 = lane & 15, q = lane >> 4;
     auto mma = [&](int j, int s) {                 // 32 ranks of row tile j
         v4f x[TNW];
-        bf16x8 bf[TNW];
-        const uint8_t* const ta = tl + swz128(mw + 16 * j + r16, 4 * s + q);
-        const bf16x8 t0 = __builtin_bit_cast(bf16x8, lds16(ta)), t1 = __builtin_bit_cast(bf16x8, lds16(ta + TM * 128));
+        bf16x8 bf[TNW], t[kParts];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+            t[p] = __builtin_bit_cast(bf16x8, lds16(tl + p * TM * 128 + swz128(mw + 16 * j + r16, 4 * s + q)));
 #pragma unroll
         for (int i = 0; i < TNW; ++i) bf[i] = __builtin_bit_cast(bf16x8, lds16(bl + swz128(nw + 16 * i + r16, 4 * s + q)));
 #pragma unroll
-        for (int i = 0; i < TNW; ++i) x[i] = mfma_bf16(bf[i], t1, mfma_bf16(bf[i], t0, acc[i][j]));
-        if (e.parts > 2) {
-            const bf16x8 t2 = __builtin_bit_cast(bf16x8, lds16(ta + 2 * TM * 128));
+        for (int i = 0; i < TNW; ++i) {
+            x[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < TNW; ++i) x[i] = mfma_bf16(bf[i], t2, x[i]);
+            for (int p = 0; p < kParts; ++p) x[i] = mfma_bf16(bf[i], t[p], x[i]);
         }
 #pragma unroll
         for (int i = 0; i < TNW; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] = id[j] == cur ? x[i][r] : acc[i][j][r];
+            for (int r = 0; r < 4; ++r) acc[i][j][r] += id[j] == cur ? x[i][r] : 0.f;
     };
 #pragma unroll
     for (int j = 0; j < TMW; ++j) {
@@ -266,73 +276,37 @@ __device__ __forceinline__ void lora_mma16(v4f (&acc)[TNW][TMW], const LoraEpi& 
     }
 }
 
-// The same of waves with 32 x 32 tiles: row mw + 32 jx + l % 32. Where every row of the wave has the
-// adapter (long runs), the products go straight into the accumulators; else feature tiles in pairs, into
-// copies that are selected from.
-template <int TM, int NI, int NJ>
+// The same of waves with 32 x 32 tiles: row mw + 32 jx + l % 32. A tile at a time: left to
+// itself the compiler keeps every tile's products to the end, beside the accumulators, and spills
+// (256 x 256 tiles: 540 us with the code in place and no adapter in use, against 470).
+template <int TM, int kParts, int NI, int NJ>
 __device__ __forceinline__ void lora_mma32(v16f (&acc)[NI][NJ], const LoraEpi& e, const int (&id)[NJ], int cur, int c0,
                                            const uint8_t* tl, const uint8_t* bl, int mw, int nw, int lane) {
     asm volatile("" : "+v"(lane));                 // addresses formed here, not held over the whole kernel
     const int r32 = lane & 31, q = lane >> 5;
     const int steps = e.rp - c0 > 32 ? 4 : 2;      // 16 ranks each
-    auto tf = [&](int jx, int h, int p) {
-        return __builtin_bit_cast(bf16x8, lds16(tl + p * TM * 128 + swz128(mw + 32 * jx + r32, 2 * h + q)));
-    };
-    auto bf = [&](int i, int h) { return __builtin_bit_cast(bf16x8, lds16(bl + swz128(nw + 32 * i + r32, 2 * h + q))); };
-    bool mine = true;
+    bool mine = false;
 #pragma unroll
-    for (int jx = 0; jx < NJ; ++jx) mine = mine && id[jx] == cur;
-    if (__ballot(!mine) == 0) {
-        for (int h = 0; h < steps; ++h) {
-            bf16x8 b[NI], t[NJ];
+    for (int jx = 0; jx < NJ; ++jx) mine = mine || id[jx] == cur;
+    if (!__ballot(mine)) return;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) b[i] = bf(i, h);
-            auto part = [&](int p) {
+    for (int jx = 0; jx < NJ; ++jx)
 #pragma unroll
-                for (int jx = 0; jx < NJ; ++jx) t[jx] = tf(jx, h, p);
+        for (int i = 0; i < NI; ++i) {
+            v16f x;
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-#pragma unroll
-                    for (int jx = 0; jx < NJ; ++jx) acc[i][jx] = mfma32_bf16(b[i], t[jx], acc[i][jx]);
-            };
-            part(0);
-            part(1);
-            if (e.parts > 2) part(2);
-        }
-        return;
-    }
-    constexpr int kPair = NI * NJ > 6 ? 1 : 2;     // what fits beside the accumulators
-#pragma unroll
-    for (int jx = 0; jx < NJ; ++jx) {
-        if (!__ballot(id[jx] == cur)) continue;
-#pragma unroll
-        for (int i0 = 0; i0 < NI; i0 += kPair) {
-            v16f x[kPair];
-#pragma unroll
-            for (int u = 0; u < kPair; ++u)
-                if (i0 + u < NI) x[u] = acc[i0 + u][jx];
+            for (int r = 0; r < 16; ++r) x[r] = 0.f;
+#pragma unroll 1
             for (int h = 0; h < steps; ++h) {
-                bf16x8 b[kPair];
+                const bf16x8 b = __builtin_bit_cast(bf16x8, lds16(bl + swz128(nw + 32 * i + r32, 2 * h + q)));
 #pragma unroll
-                for (int u = 0; u < kPair; ++u)
-                    if (i0 + u < NI) b[u] = bf(i0 + u, h);
-                auto part = [&](int p) {
-                    const bf16x8 t = tf(jx, h, p);
-#pragma unroll
-                    for (int u = 0; u < kPair; ++u)
-                        if (i0 + u < NI) x[u] = mfma32_bf16(b[u], t, x[u]);
-                };
-                part(0);
-                part(1);
-                if (e.parts > 2) part(2);
+                for (int p = 0; p < kParts; ++p)
+                    x = mfma32_bf16(b, __builtin_bit_cast(bf16x8, lds16(tl + p * TM * 128 + swz128(mw + 32 * jx + r32, 2 * h + q))), x);
             }
 #pragma unroll
-            for (int u = 0; u < kPair; ++u)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (i0 + u < NI) acc[i0 + u][jx][r] = id[jx] == cur ? x[u][r] : acc[i0 + u][jx][r];
+            for (int r = 0; r < 16; ++r) acc[i][jx][r] += id[jx] == cur ? x[r] : 0.f;
+            asm volatile("" : "+v"(acc[i][jx]));   // added here, not after the last tile's products
         }
-    }
 }
 
 // ---------------------------------------------------------------- panel kernel
@@ -343,7 +317,7 @@ __device__ __forceinline__ uint4 bload(const __amdgpu_buffer_rsrc_t& r, uint32_t
 }
 
 // D: weight k-steps in flight per wave (and activation tiles in registers).
-template <int BM, int WN, bool kExact, int D, bool kLora>
+template <int BM, int WN, bool kExact, int D, int kLora>
 __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     constexpr int BN = 4 * WN, TN = WN / 16, TM = BM / 16;
     constexpr int U = D % 2 == 0 ? D : 2 * D;   // loop unroll: step kt's registers are slot kt % D
@@ -366,6 +340,8 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     if (pan >= npan) return;
     const int64_t pend = min((int64_t)(pan + 1) * PW, g.n);
     const int64_t m0 = (int64_t)mt * BM, nw0 = (int64_t)pan * PW + wave * WN;
+    LoraRows<BM> lrows;
+    if constexpr (kLora != 0) lrows.load(g.lora, m0, g.m, lane);
     const int nk = (int)((g.k + 127) / 128);
     const int ns = (nk + U - 1) / U * U;   // steps, padded to the unroll (padding steps read zeros)
 
@@ -464,7 +440,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     }
 
     const float sa = *g.a_scale;
-    if constexpr (kLora) {   // scale first, then add the adapters' part (feature rows past the panel are not stored)
+    if constexpr (kLora != 0) {   // scale first, then add the adapters' part (feature rows past the panel are not stored)
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -474,9 +450,9 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
         int id[TM];
 #pragma unroll
         for (int j = 0; j < TM; ++j) id[j] = lora_row(g.lora, m0 + j * 16 + r16, g.m);
-        lora_tile<BN, BM, 256, kLds>(g.lora, m0, g.m, (int64_t)pan * PW, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+        lora_tile<BN, BM, 256, kLds>(g.lora, lrows, m0, g.m, (int64_t)pan * PW, g.n, pend, smem, __builtin_amdgcn_readfirstlane(wave), lane,
                                [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
-                                   lora_mma16<BM>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
+                                   lora_mma16<BM, kLora + 1>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
                                });
     }
 #pragma unroll
@@ -487,7 +463,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
         for (int r = 0; r < 4; ++r) sc[r] = kLora ? 1.0f : sa * wsc[i][r];
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-            if (g.out_f32)
+            if (kLora ? kLora == 2 : g.out_f32 != nullptr)
                 store_tile_f32(g.out_f32, g.ld_out, m0 + j * 16 + r16, nw0 + i * 16 + 4 * q, g.m, pend, acc[i][j], sc, full);
             else
                 store_tile(g.out, g.ld_out, m0 + j * 16 + r16, nw0 + i * 16 + 4 * q, g.m, pend, acc[i][j], sc, full);
@@ -522,7 +498,7 @@ __device__ __forceinline__ v8i lds_operand(const uint8_t* s, int row, int q) {
     return cat8(*reinterpret_cast<const uint4*>(s + swz(row, 2 * q)), *reinterpret_cast<const uint4*>(s + swz(row, 2 * q + 1)));
 }
 
-template <bool kExact, bool kLora>
+template <bool kExact, int kLora>
 __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
     // two stages of both operands, and after the k loop the adapters' operands
     constexpr int kLds = kLora ? 3 * kTile * 128 + 4 * kTile * 128 : 4 * kTile * kTile;
@@ -534,6 +510,8 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
     const int q = lane >> 4, r16 = lane & 15;
     const int64_t n0 = (int64_t)blockIdx.x * kTile, m0 = (int64_t)blockIdx.y * kTile;
     const int nk = (int)((g.k + kTile - 1) / kTile);
+    LoraRows<kTile> lrows;
+    if constexpr (kLora != 0) lrows.load(g.lora, m0, g.m, lane);
 
     float wsc[4][4];
 #pragma unroll
@@ -583,7 +561,7 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
 
     const float sa = *g.a_scale;
     const bool full = g.vec_out && m0 + wm * 64 + 64 <= g.m && n0 + wn * 64 + 64 <= g.n;
-    if constexpr (kLora) {
+    if constexpr (kLora != 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -593,9 +571,9 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
         int id[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) id[j] = lora_row(g.lora, m0 + wm * 64 + j * 16 + r16, g.m);
-        lora_tile<kTile, kTile, 256, kLds>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+        lora_tile<kTile, kTile, 256, kLds>(g.lora, lrows, m0, g.m, n0, g.n, g.n, smem, __builtin_amdgcn_readfirstlane(wave), lane,
                                      [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
-                                         lora_mma16<kTile>(acc, g.lora, id, cur, c0, tl, bl, wm * 64, wn * 64, lane);
+                                         lora_mma16<kTile, kLora + 1>(acc, g.lora, id, cur, c0, tl, bl, wm * 64, wn * 64, lane);
                                      });
     }
 #pragma unroll
@@ -605,7 +583,7 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
         for (int r = 0; r < 4; ++r) sc[r] = kLora ? 1.0f : sa * wsc[i][r];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (g.out_f32)
+            if (kLora ? kLora == 2 : g.out_f32 != nullptr)
                 store_tile_f32(g.out_f32, g.ld_out, m0 + wm * 64 + j * 16 + r16, n0 + wn * 64 + i * 16 + 4 * q, g.m, g.n,
                                acc[i][j], sc, full);
             else
@@ -703,17 +681,17 @@ __device__ __forceinline__ void ring_tile(const GemmArgs& g, int64_t& m0, int64_
 // The end of a ring kernel (all of its loads retired): split k stores this split's raw sums
 // to the partial buffer; f32 output goes straight from the accumulators; bf16 output is
 // scaled, staged through the ring as TM rows of 512 bytes and stored row by row.
-template <int TN, int TM, bool kLora, int LDS>
+template <int TN, int TM, int kLora, int LDS>
 __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN / 64][TM / 128], int64_t m0,
                                               int64_t n0, int ks, uint8_t* smem, int t, int wn, int wm, int r32,
-                                              int q) {
+                                              int q, const LoraRows<TM>& lrows) {
     constexpr int kNI = TN / 64, kJX = TM / 128;
     // acc[i][jx] register r: n = 32 i + 8 (r / 4) + 4 q + r % 4, m = 32 jx + lane % 32 (wave
     // tile relative). The scaled bf16 tile is staged in LDS as [m][n] with 512-byte rows, the
     // 16-byte chunk cn of row ml at slot cn ^ (ml & 15) with its two 8-byte halves swapped when
     // bit 3 xor bit 4 of ml is set: the 8-byte writes of 32 rows at one n land in 32 distinct
     // slots of the 256-byte bank window. Each half-wave then stores one whole 512-byte row.
-    if (g.part) {
+    if (!kLora && g.part) {
         // split k: this split's raw sums, f32 [m, n] slice ks of the partial buffer
         float* pt = g.part + (int64_t)ks * g.m * g.n;
         const float one[4] = {1.f, 1.f, 1.f, 1.f};
@@ -732,7 +710,7 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
         return;
     }
     const float sa = *g.a_scale;
-    if constexpr (kLora) {
+    if constexpr (kLora != 0) {
         // scaled first; four consecutive features' scales in one load (zeros past n), a feature tile at a time
         const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
             (void*)g.w_scale, (short)0, g.ws_step != 0 ? (int)(g.n * 4) : 4, 0x00020000);
@@ -752,17 +730,18 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
 #pragma unroll
                     for (int jx = 0; jx < kJX; ++jx) acc[i][jx][4 * gq + r] *= sc;
                 }
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int jx = 0; jx < kJX; ++jx) asm volatile("" : "+v"(acc[i][jx]));
         }
         int id[kJX];
 #pragma unroll
         for (int jx = 0; jx < kJX; ++jx) id[jx] = lora_row(g.lora, m0 + wm * (TM / 4) + jx * 32 + r32, g.m);
-        lora_tile<TN, TM, 512, LDS>(g.lora, m0, g.m, n0, g.n, smem, __builtin_amdgcn_readfirstlane(t >> 6), t & 63,
+        lora_tile<TN, TM, 512, LDS>(g.lora, lrows, m0, g.m, n0, g.n, g.n, smem, __builtin_amdgcn_readfirstlane(t >> 6), t & 63,
                                [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
-            lora_mma32<TM>(acc, g.lora, id, cur, c0, tl, bl, wm * (TM / 4), wn * (TN / 2), t & 63);
+            lora_mma32<TM, kLora + 1>(acc, g.lora, id, cur, c0, tl, bl, wm * (TM / 4), wn * (TN / 2), t & 63);
         });
     }
-    if (g.out_f32) {
+    if (kLora ? kLora == 2 : g.out_f32 != nullptr) {
         // f32 output: each lane stores its four consecutive n of one m row straight from the
         // accumulators (16 bytes per lane; the output is twice the bf16 size, no LDS staging)
 #pragma unroll
@@ -830,7 +809,7 @@ __device__ __forceinline__ void ring_epilogue(const GemmArgs& g, v16f (&acc)[TN 
 }
 
 // Operands under 2^31 bytes (buffer offsets). Grid = number of TN x TM tiles, 512 threads.
-template <int TN, int TM, bool kExact, bool kLora>
+template <int TN, int TM, bool kExact, int kLora>
 __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     using RS = RingShape<TN, TM>;
     constexpr int kStage = RS::kStage, kRing = RS::kRing, kNI = RS::kNI, kJX = RS::kJX, kLoads = RS::kLoads;
@@ -878,6 +857,8 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     const int kper = (nk_all + g.ksplit - 1) / g.ksplit;
     const int s_beg = ks * kper;
     const int nk = min(kper, nk_all - s_beg);   // >= 1: the launcher leaves no split empty
+    LoraRows<TM> lrows;
+    if constexpr (kLora != 0) lrows.load(g.lora, m0, g.m, lane);
     auto issue = [&](int s) {   // stage s (past k its loads are out of range, zeros; past this
                                 // split's range they are loaded and never read)
         const uint32_t k0 = (uint32_t)(s_beg + s) * kWK;
@@ -953,7 +934,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
     }
     wait_vmcnt<0>();   // the ring's trailing loads (past k) before the ring is reused
 
-    ring_epilogue<TN, TM, kLora, kRing * kStage>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
+    ring_epilogue<TN, TM, kLora, kRing * kStage>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q, lrows);
 }
 
 
@@ -961,7 +942,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(const GemmArgs g) {
 // TN + TM rows, so every DMA request is a whole 128-byte line (the 64-byte stages issue half
 // lines) and a CU's requests in flight carry twice the bytes. A DMA block is 8 rows (1 KB);
 // each stage runs two MFMA k-steps. 192 x 128 only: four 40 KB stages fit the LDS.
-template <int TN, int TM, bool kExact, bool kLora>
+template <int TN, int TM, bool kExact, int kLora>
 __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
     constexpr int kK = 128;                              // k bytes per stage
     constexpr int kStage = (TN + TM) * kK;
@@ -1006,6 +987,8 @@ __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
     const int kper = (nk_all + g.ksplit - 1) / g.ksplit;
     const int s_beg = ks * kper;
     const int nk = min(kper, nk_all - s_beg);   // >= 1: the launcher leaves no split empty
+    LoraRows<TM> lrows;
+    if constexpr (kLora != 0) lrows.load(g.lora, m0, g.m, lane);
     auto issue = [&](int s) {   // stage s (past k: zeros; past this split's range: loaded, never read)
         const uint32_t k0 = (uint32_t)(s_beg + s) * kK;
         uint8_t* sb = smem + (s % kRing) * kStage;
@@ -1062,7 +1045,7 @@ __global__ __launch_bounds__(512) void ring128_kernel(const GemmArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     }
     wait_vmcnt<0>();   // the ring's trailing loads (past k) before the ring is reused
-    ring_epilogue<TN, TM, kLora, kRing * kStage>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q);
+    ring_epilogue<TN, TM, kLora, kRing * kStage>(g, acc, m0, n0, ks, smem, t, wn, wm, r32, q, lrows);
 }
 
 // Split-k epilogue: out[m, n] = (sum over s of part[s, m, n], in split order) * a_scale *
@@ -1134,7 +1117,7 @@ static int panel_rows(int64_t m, int64_t n, int BM, int BN) {
 // of four-step groups (at 512 x 2688 x 4096 23.6 -> 23.1 us, 128 x 2688 x 4096 19.5 -> 18.0;
 // where four-step padding was needed, as at k = 2688, it lost), else two; exact sums keep two,
 // as their conversions leave no registers for more.
-template <int BM, int WN, bool kExact, bool kLora>
+template <int BM, int WN, bool kExact, int kLora>
 static void launch_panel(GemmArgs g, hipStream_t st) {
     g.panel_rows = panel_rows(g.m, g.n, BM, 4 * WN);
     const int64_t npan = (g.n + g.panel_rows - 1) / g.panel_rows, nmt = (g.m + BM - 1) / BM;
@@ -1196,7 +1179,7 @@ size_t gemm_part_bytes(int64_t m, int64_t n, int64_t k) {
     return S > 1 ? (size_t)S * (size_t)m * (size_t)n * sizeof(float) : 0;
 }
 
-template <bool kExact, bool kLora>
+template <bool kExact, int kLora>
 static nhm_status dispatch_gemm(GemmArgs g, hipStream_t st, float* part, size_t part_bytes) {
     const int64_t m = g.m, n = g.n, k = g.k, lda = g.lda;
     // buffer descriptors address the operands with 32-bit offsets
@@ -1219,12 +1202,12 @@ static nhm_status dispatch_gemm(GemmArgs g, hipStream_t st, float* part, size_t 
         return check_launch("gemm (256 x 128)");
     }
     if (m <= 640 && offsets_fit) {   // too few ring tiles to fill the chip
-        if constexpr (!kLora) {
+        if constexpr (kLora == 0) {
             const int S = split_k(m, n, k);
             if (S > 1 && part && part_bytes >= gemm_part_bytes(m, n, k) && (reinterpret_cast<uintptr_t>(part) & 15) == 0) {
                 g.ksplit = S;
                 g.part = part;
-                ring128_kernel<192, 128, kExact, false><<<dim3((unsigned)(t192 * S)), dim3(512), 0, st>>>(g);
+                ring128_kernel<192, 128, kExact, 0><<<dim3((unsigned)(t192 * S)), dim3(512), 0, st>>>(g);
                 count_launch(kExact ? Kern::kRing192x128Exact : Kern::kRing192x128, m);
                 nhm_status s = check_launch("gemm (192 x 128, split k)");
                 if (s != NHM_OK) return s;
@@ -1258,7 +1241,7 @@ nhm_status launch_gemm(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* 
                        : ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0,
                out_f32};
     g.ws_step = ws_step;
-    return exact ? dispatch_gemm<true, false>(g, st, part, part_bytes) : dispatch_gemm<false, false>(g, st, part, part_bytes);
+    return exact ? dispatch_gemm<true, 0>(g, st, part, part_bytes) : dispatch_gemm<false, 0>(g, st, part, part_bytes);
 }
 
 nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* w, const float* w_scale,
@@ -1270,7 +1253,8 @@ nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint
                out_f32};
     g.ws_step = ws_step;
     g.lora = lora;
-    return exact ? dispatch_gemm<true, true>(g, st, nullptr, 0) : dispatch_gemm<false, true>(g, st, nullptr, 0);
+    if (out_f32) return exact ? dispatch_gemm<true, 2>(g, st, nullptr, 0) : dispatch_gemm<false, 2>(g, st, nullptr, 0);
+    return exact ? dispatch_gemm<true, 1>(g, st, nullptr, 0) : dispatch_gemm<false, 1>(g, st, nullptr, 0);
 }
 
 }  // namespace nhm

@@ -7,12 +7,15 @@
 // are stored, so another adapter's values reach nobody else. What it must read is x and the used
 // adapters' A, and with a bf16 x it writes the codes.
 //  * Few rows: latency bounds it. A workgroup owns 16 rows and 16 ranks over all of k, 16 waves
-//    that take the 32-wide k-steps round robin with all their loads in flight (at k = 2,688 one round), and
+//    that take the 32-wide k-steps round robin with all their loads in flight (up to k = 4,096 one round), and
 //    a share of the tile's distinct adapters.
 //  * Many rows (8,192 or more fill half of the chip): x's bytes bound it. A workgroup owns 64 rows and up to 64 ranks,
-//    8 waves that each take whole 64 x 64 k-steps, so that x and A enter the CU once, the next
+//    4 waves that each take whole 64 x 64 k-steps, so that x and A enter the CU once, the next
 //    step's operands on their way while one is multiplied.
-// The waves' sums meet in LDS and are added in wave order.
+// The waves' sums meet in LDS and are added in wave order. A lane's share of a 64-wide k-step is 16
+// consecutive values (two matrix instructions' worth; any deal of k to lanes will do that is the same for
+// both operands), so that the first of its two loads asks for whole 128-byte lines: with 32-wide steps
+// the halves of a line were fetched apart (15,360 rows from HBM: 62 us).
 #include "nhm_device.h"
 #include "nhm_internal.h"
 
@@ -26,13 +29,11 @@ __device__ __forceinline__ bf16x8 x8(const uint8_t* p) {
 }
 
 // The codes of eight bf16 values, as nhm_fp8_quantize_static forms them.
-__device__ __forceinline__ void store_codes(uint8_t* q, const bf16x8& v, float s, float rs, bool fast) {
+__device__ __forceinline__ uint2 codes8(const bf16x8& v, float s, float rs, bool fast) {
     const v4u u = __builtin_bit_cast(v4u, v);
     const uint4 in = make_uint4(u[0], u[1], u[2], u[3]);
-    uint2 c;
-    if (fast && __builtin_amdgcn_ballot_w64(bf16x8_special(in) != 0u) == 0) c = quant_bf16x8_fast(in, s, rs);
-    else c = quant_bf16x8(in, s);
-    *reinterpret_cast<uint2*>(q) = c;
+    if (fast && __builtin_amdgcn_ballot_w64(bf16x8_special(in) != 0u) == 0) return quant_bf16x8_fast(in, s, rs);
+    return quant_bf16x8(in, s);
 }
 
 // Ranks r0 .. r0 + 3 of a row (d, unscaled) into its parts.
@@ -59,7 +60,7 @@ __device__ __forceinline__ const X* x_rows(const LoraDownArgs& g) {
 
 // ---------------------------------------------------------------- few rows
 
-constexpr int kFewWaves = 16, kFewSteps = 6;   // k-steps of a wave whose loads are in flight together
+constexpr int kFewWaves = 16, kFewSteps = 4;   // k-steps of a wave whose loads are in flight together
 
 // gridDim: (row tiles, rank groups, shares + extra): blockIdx.z < shares takes every shares-th
 // distinct adapter of the tile; the workgroups past that form the tile's codes, one or a few vectors a
@@ -79,18 +80,18 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
             const int stride = (int)(gridDim.z - shares) * gridDim.y * kFewWaves * 64;
             for (int v = ((blockIdx.z - shares) * gridDim.y + blockIdx.y) * kFewWaves * 64 + threadIdx.x; v < total; v += stride) {
                 const int64_t row = tile0 + v / per_row, c = (int64_t)(v % per_row) * 8;
-                store_codes(g.q + row * g.k + c, x8(g.x + row * g.ld_x + c), s, rs, fast);
+                *reinterpret_cast<uint2*>(g.q + row * g.k + c) = codes8(x8(g.x + row * g.ld_x + c), s, rs, fast);
             }
             return;
         }
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r16 = lane & 15, q8 = 8 * (lane >> 4);
+    const int r16 = lane & 15, q16 = 16 * (lane >> 4);
     const int64_t row = tile0 + r16;
     const int64_t src = row < g.m ? row : g.m - 1;
     int id = g.row_adapter[src];
     const X* const xr = x_rows<X>(g) + src * g.ld_x;
-    const int steps = (int)((g.k + 31) / 32);
+    const int steps = (int)((g.k + 63) / 64);
     const int r = blockIdx.y * 16 + r16;                         // this lane's rank of A
     const int64_t arow = r < g.rank ? r : g.rank - 1;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
@@ -107,19 +108,24 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
         v4f acc = {0.f, 0.f, 0.f, 0.f};
         const uint16_t* const ar = g.a + ((int64_t)cur * g.rank + arow) * g.k;
         for (int s0 = wave; s0 < steps; s0 += kFewWaves * kFewSteps) {
-            bf16x8 xv[kFewSteps], av[kFewSteps];
+            bf16x8 xv[kFewSteps][2], av[kFewSteps][2];
 #pragma unroll
             for (int u = 0; u < kFewSteps; ++u) {
-                const int kk = (s0 + u * kFewWaves) * 32 + q8;
-                xv[u] = zero;
-                av[u] = zero;
+                const int kk = (s0 + u * kFewWaves) * 64 + q16;      // 16 divides k: all of a lane's 16 or none
+#pragma unroll
+                for (int h = 0; h < 2; ++h) xv[u][h] = av[u][h] = zero;
                 if (kk < g.k) {
-                    av[u] = x8(ar + kk);
-                    xv[u] = x8(xr + kk);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        av[u][h] = x8(ar + kk + 8 * h);
+                        xv[u][h] = x8(xr + kk + 8 * h);
+                    }
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kFewSteps; ++u) acc = mfma_bf16(av[u], xv[u], acc);
+            for (int u = 0; u < kFewSteps; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) acc = mfma_bf16(av[u][h], xv[u][h], acc);
         }
         s_part[wave][lane] = acc;
         __syncthreads();
@@ -136,14 +142,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
 
 // ---------------------------------------------------------------- many rows
 
-constexpr int kManyWaves = 8, kManyRows = 4;   // row tiles of 16 per workgroup
+constexpr int kManyWaves = 4, kManyRows = 4;   // row tiles of 16 per workgroup
 
 // NR: 16-rank tiles per workgroup. gridDim: (64-row tiles, groups of 16 NR ranks).
 template <typename X, int NR>
 __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const LoraDownArgs g) {
     __shared__ v4f s_part[kManyWaves][kManyRows * NR][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r16 = lane & 15, q8 = 8 * (lane >> 4);
+    const int r16 = lane & 15, q16 = 16 * (lane >> 4);
     const int64_t row0 = (int64_t)blockIdx.x * (16 * kManyRows);
     const int rank0 = blockIdx.y * 16 * NR;
     const float s = *g.a_scale;
@@ -158,12 +164,12 @@ __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const L
         if (id[i] >= g.n_adapters) id[i] = -1;
         xr[i] = x_rows<X>(g) + (row < g.m ? row : g.m - 1) * g.ld_x;
     }
-    const int full = (int)(g.k / 32);              // whole 32-wide steps; one of 16 may follow
-    const int steps = (int)((g.k + 31) / 32);
+    const int full = (int)(g.k / 64);              // whole 64-wide steps; a part of one may follow
+    const int steps = (int)((g.k + 63) / 64);
     const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
     bool codes = sizeof(X) == 2 && g.q && blockIdx.y == 0;
 
-    struct Ops { bf16x8 x[kManyRows], a[NR]; };
+    struct Ops { bf16x8 x[kManyRows][2], a[NR][2]; };
     v4f acc[kManyRows][NR];
     auto pass = [&](int cur, bool with_codes) {
         const uint16_t* ar[NR];
@@ -176,46 +182,57 @@ __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const L
         for (int i = 0; i < kManyRows; ++i)
 #pragma unroll
             for (int j = 0; j < NR; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        // a step past the last whole one reads that again and is not used: loads under a branch would
+        // all be waited for at the next use of any
         auto load = [&](Ops& o, int step) {
-            const int kk = step * 32 + q8;
-            if (step < full) {
+            const int kk = min(step, full - 1) * 64 + q16;
 #pragma unroll
-                for (int i = 0; i < kManyRows; ++i) o.x[i] = x8(xr[i] + kk);
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int j = 0; j < NR; ++j) o.a[j] = x8(ar[j] + kk);
-            } else {                               // the half step at the end, or a step past it: zeros
+                for (int i = 0; i < kManyRows; ++i) o.x[i][h] = x8(xr[i] + kk + 8 * h);
 #pragma unroll
-                for (int i = 0; i < kManyRows; ++i) o.x[i] = kk < g.k ? x8(xr[i] + kk) : zero;
-#pragma unroll
-                for (int j = 0; j < NR; ++j) o.a[j] = kk < g.k ? x8(ar[j] + kk) : zero;
+                for (int j = 0; j < NR; ++j) o.a[j][h] = x8(ar[j] + kk + 8 * h);
             }
         };
         auto use = [&](const Ops& o, int step) {
-            const int kk = step * 32 + q8;
+            const int kk = step * 64 + q16;
             if (with_codes) {
 #pragma unroll
                 for (int i = 0; i < kManyRows; ++i) {
                     const int64_t row = row0 + 16 * i + r16;
-                    if (kk < g.k && row < g.m) store_codes(g.q + row * g.k + kk, o.x[i], s, rs, fast);
+                    const uint2 c0 = codes8(o.x[i][0], s, rs, fast), c1 = codes8(o.x[i][1], s, rs, fast);
+                    if (kk < g.k && row < g.m) *reinterpret_cast<v4u*>(g.q + row * g.k + kk) = v4u{c0.x, c0.y, c1.x, c1.y};
                 }
             }
             if (cur >= 0) {
 #pragma unroll
-                for (int i = 0; i < kManyRows; ++i)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < NR; ++j) acc[i][j] = mfma_bf16(o.a[j], o.x[i], acc[i][j]);
+                    for (int i = 0; i < kManyRows; ++i)
+#pragma unroll
+                        for (int j = 0; j < NR; ++j) acc[i][j] = mfma_bf16(o.a[j][h], o.x[i][h], acc[i][j]);
             }
         };
-        Ops o0, o1, o2;
-        load(o0, wave);
-        load(o1, wave + kManyWaves);
-        for (int st = wave; st < steps; st += 3 * kManyWaves) {
-            load(o2, st + 2 * kManyWaves);
-            use(o0, st);
-            load(o0, st + 3 * kManyWaves);
-            use(o1, st + kManyWaves);
-            load(o1, st + 4 * kManyWaves);
-            use(o2, st + 2 * kManyWaves);
+        Ops o0, o1;
+        if (full > 0) {
+            load(o0, wave);
+            for (int st = wave; st < full; st += 2 * kManyWaves) {
+                load(o1, st + kManyWaves);
+                use(o0, st);
+                load(o0, st + 2 * kManyWaves);
+                if (st + kManyWaves < full) use(o1, st + kManyWaves);
+            }
+        }
+        if (full < steps && wave == full % kManyWaves) {     // the rest of a k that 64 does not divide
+            const int kk = full * 64 + q16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < kManyRows; ++i) o0.x[i][h] = kk < g.k ? x8(xr[i] + kk + 8 * h) : zero;
+#pragma unroll
+                for (int j = 0; j < NR; ++j) o0.a[j][h] = kk < g.k ? x8(ar[j] + kk + 8 * h) : zero;
+            }
+            use(o0, full);
         }
     };
 
