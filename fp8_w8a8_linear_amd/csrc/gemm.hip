@@ -281,7 +281,10 @@ __device__ __forceinline__ void lora_mma16(v4f (&acc)[TNW][TMW], const LoraEpi& 
     for (int j = 0; j < TMW; ++j) {
         if (!__ballot(id[j] == cur)) continue;
         mma(j, 0);
-        if (e.rp - c0 > 32) mma(j, 1);
+        if (e.rp - c0 > 32) {
+            asm volatile("" ::: "memory");         // a branch, not both halves and a choice
+            mma(j, 1);
+        }
     }
 }
 
