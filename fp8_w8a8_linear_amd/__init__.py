@@ -15,7 +15,8 @@ __all__ = ["lib", "LIB_PATH", "NhmError", "Geometry", "Layout", "WsLayout", "Fp8
            "decode_ws_layout", "prefill_ws_layout", "mixer_decode", "mixer_prefill", "NHM_BF16", "NHM_E4M3",
            "NHM_F32", "fp8_dequant_channel_bf16", "mixer_decode_noalloc", "mixer_decode_q",
            "dispatch_counters", "Lora", "fp8_linear_lora", "fp8_linear_lora_workspace_bytes", "beam_select",
-           "beam_select_workspace_bytes", "beam_reorder", "BatchPlan", "batch_plan"]
+           "beam_select_workspace_bytes", "beam_reorder", "BatchPlan", "batch_plan", "mixer_decode_lora",
+           "mixer_prefill_lora", "decode_lora_ws_layout", "prefill_lora_ws_layout"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnhm.so")
 if not os.path.exists(LIB_PATH):
@@ -102,6 +103,12 @@ _SIGS = {
     "nhm_fp8_linear_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, C.c_int, _i32]),
     "nhm_fp8_linear_lora": (C.c_int, [_p, C.c_int, _i64, _i64, C.POINTER(_Fp8Weight), C.POINTER(_Lora), _p, _p, C.c_int,
                                       _i64, _i32, _p, _sz, _p]),
+    "nhm_mixer_decode_lora_ws_layout": (C.c_int, [C.POINTER(Geometry), _i32, _i32, C.POINTER(WsLayout)]),
+    "nhm_mixer_prefill_lora_ws_layout": (C.c_int, [C.POINTER(Geometry), _i64, _i32, _i32, _i32, C.POINTER(WsLayout)]),
+    "nhm_mixer_decode_lora": (C.c_int, [C.POINTER(_MixerParams), C.POINTER(_Lora), C.POINTER(_Lora), _p, _p, _i32, _p, _p,
+                                        C.c_int, _p, _i32, _p, _p, _sz, _p]),
+    "nhm_mixer_prefill_lora": (C.c_int, [C.POINTER(_MixerParams), C.POINTER(_Lora), C.POINTER(_Lora), _p, _p, _i64, _p,
+                                         _i32, _p, _p, _i32, _p, C.c_int, _p, _i32, _p, _p, _sz, _p]),
     "nhm_beam_select_workspace_bytes": (_sz, [_i64, _i32, _i64, _i32]),
     "nhm_beam_select": (C.c_int, [_p, C.c_int, _i64, _i64, _i32, _i64, _p, _p, _i32, _i32, _p, _p, _p, _p, _sz, _p]),
     "nhm_beam_reorder": (C.c_int, [C.POINTER(Geometry), _p, _p, _i64, _i32, C.POINTER(_StatePool), _i32, C.c_int, _i32,
@@ -411,6 +418,56 @@ def fp8_linear_lora(a, weight: Fp8Weight, lora: Lora, row_adapter, out=None, ws=
                     dev)
     _call(dev, stream, lib.nhm_fp8_linear_lora, a.data_ptr(), a_type, m, weight.k, C.byref(weight.struct),
           C.byref(lora.struct), row_adapter.data_ptr(), out.data_ptr(), out_type, weight.n, 1 if exact else 0,
+          ws.data_ptr(), ws.numel())
+    return out
+
+
+def decode_lora_ws_layout(batch, rank, g=GEOMETRY):
+    out = WsLayout()
+    _check(lib.nhm_mixer_decode_lora_ws_layout(C.byref(_geom(g)), batch, rank, C.byref(out)))
+    return {n: int(getattr(out, n)) for n, _ in WsLayout._fields_}
+
+
+def prefill_lora_ws_layout(n_tokens, n_seqs, rank, chunk=128, g=GEOMETRY):
+    out = WsLayout()
+    _check(lib.nhm_mixer_prefill_lora_ws_layout(C.byref(_geom(g)), n_tokens, n_seqs, chunk, rank, C.byref(out)))
+    return {n: int(getattr(out, n)) for n, _ in WsLayout._fields_}
+
+
+def _mixer_lora(params, lora_in, lora_out, row_adapter, rows, dev):
+    """The C arguments of the two adapter sets and the row map, checked against the block's projections."""
+    import torch
+    for lo, w, name in ((lora_in, params.in_proj, "lora_in"), (lora_out, params.out_proj, "lora_out")):
+        if lo is not None and (lo.n, lo.k) != (w.n, w.k):
+            raise ValueError(f"{name} is for a [{lo.n}, {lo.k}] projection, the block's is [{w.n}, {w.k}]")
+        if lo is not None and lo.a.device != dev:
+            raise ValueError(f"{name} is on {lo.a.device}, not on {dev}")
+    _on(dev, [(row_adapter, "row_adapter", (torch.int32,), (rows,))])
+    ref = lambda lo: None if lo is None else C.byref(lo.struct)  # noqa: E731
+    return ref(lora_in), ref(lora_out), None if row_adapter is None else row_adapter.data_ptr()
+
+
+def mixer_decode_lora(params: MixerParams, lora_in, lora_out, row_adapter, hidden, slot_idx, ssm_pool, conv_pool, out, ws,
+                      stream=None):
+    """mixer_decode with adapters beside in_proj and out_proj (Lora or None each); row_adapter int32 [batch].
+    ws: uint8 device tensor of the decode_lora_ws_layout size (for the larger rank)."""
+    dev = hidden.device
+    args = _mixer_lora(params, lora_in, lora_out, row_adapter, int(hidden.shape[0]), dev)
+    _call(dev, stream, lib.nhm_mixer_decode_lora, C.byref(params.struct), *args, hidden.data_ptr(), int(hidden.shape[0]),
+          slot_idx.data_ptr(), ssm_pool.data_ptr(), _ssm_type(ssm_pool), conv_pool.data_ptr(), int(ssm_pool.shape[0]),
+          out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def mixer_prefill_lora(params: MixerParams, lora_in, lora_out, row_adapter, hidden, cu_seqlens, slot_idx, has_initial,
+                       ssm_pool, conv_pool, out, ws, chunk=128, stream=None):
+    """mixer_prefill with adapters beside in_proj and out_proj (Lora or None each); row_adapter int32 [n_tokens]
+    (BatchPlan.token_adapter). ws: uint8 device tensor of the prefill_lora_ws_layout size (for the larger rank)."""
+    dev = hidden.device
+    args = _mixer_lora(params, lora_in, lora_out, row_adapter, int(hidden.shape[0]), dev)
+    _call(dev, stream, lib.nhm_mixer_prefill_lora, C.byref(params.struct), *args, hidden.data_ptr(), int(hidden.shape[0]),
+          cu_seqlens.data_ptr(), int(slot_idx.shape[0]), slot_idx.data_ptr(), has_initial.data_ptr(), chunk,
+          ssm_pool.data_ptr(), _ssm_type(ssm_pool), conv_pool.data_ptr(), int(ssm_pool.shape[0]), out.data_ptr(),
           ws.data_ptr(), ws.numel())
     return out
 

@@ -444,10 +444,10 @@ static nhm_status device_scratch(hipStream_t st, void** out) {
 // hidden_q (optional): the block input's e4m3 codes under in_proj's activation scale, used
 // instead of quantizing hidden (which may then be NULL). out_q (optional): the codes of the
 // bf16 block output under *out_q_scale.
-static nhm_status decode_call(const nhm_mixer_params* p, const uint16_t* hidden, const uint8_t* hidden_q,
-                              int32_t batch, const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type,
-                              uint16_t* conv_pool, int32_t n_slots, uint16_t* out, uint8_t* out_q,
-                              const float* out_q_scale, void* ws, size_t ws_bytes, void* stream, bool noalloc) {
+nhm_status mixer_decode_call(const nhm_mixer_params* p, const uint16_t* hidden, const uint8_t* hidden_q, int32_t batch,
+                             const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type, uint16_t* conv_pool,
+                             int32_t n_slots, uint16_t* out, uint8_t* out_q, const float* out_q_scale, void* ws,
+                             size_t ws_bytes, void* stream, bool noalloc, const ProjectionHooks* hooks) {
     g_err[0] = 0;
     if (ssm_type != NHM_F32 && ssm_type != NHM_BF16)
         return fail(NHM_ERR_UNSUPPORTED, "SSM state dtype %d: f32 or bf16", (int)ssm_type);
@@ -468,8 +468,9 @@ static nhm_status decode_call(const nhm_mixer_params* p, const uint16_t* hidden,
     if (noalloc && w.pub.total > kNoAllocScratchBytes)
         return fail(NHM_ERR_WORKSPACE, "batch %d needs %zu bytes of scratch; the library's per-device scratch holds %zu",
                     batch, w.pub.total, kNoAllocScratchBytes);
-    if (!noalloc && ws_bytes < w.pub.total)
-        return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", w.pub.total, ws_bytes);
+    const size_t total = w.pub.total + (hooks ? hooks->extra : 0);
+    if (!noalloc && ws_bytes < total)
+        return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", total, ws_bytes);
     if ((s = check_offsets(batch, p->g.hidden, l.d_in_proj, p->g.hidden, "decode in_proj")) != NHM_OK ||
         (s = check_offsets(batch, l.d_inner, p->g.hidden, l.d_inner, "decode out_proj")) != NHM_OK)
         return s;
@@ -482,9 +483,10 @@ static nhm_status decode_call(const nhm_mixer_params* p, const uint16_t* hidden,
     uint16_t* xc = reinterpret_cast<uint16_t*>(wsb + w.pub.xbc_conv);
     uint8_t* q_out = reinterpret_cast<uint8_t*>(wsb + w.pub.q_out);
 
+    const bool hook_in = hooks && hooks->in_proj;
     if (hidden_q) {
         q_in = hidden_q;   // pre-quantized by the caller (e.g. the previous block's out_q)
-    } else {
+    } else if (!hook_in) {
         launch_quantize(hidden, batch, H, H, p->in_proj.a_scale, const_cast<uint8_t*>(q_in), H, st);
         if ((s = check_launch("decode quant")) != NHM_OK) return s;
     }
@@ -497,13 +499,17 @@ static nhm_status decode_call(const nhm_mixer_params* p, const uint16_t* hidden,
     uint32_t* cnt = reinterpret_cast<uint32_t*>(wsb + w.cnt);
     if (!use_gemv(16, l.d_in_proj, H))
         return fail(NHM_ERR_UNSUPPORTED, "decode in_proj %d x %lld outside the GEMV", l.d_in_proj, (long long)H);
-    if (batch > 32) {
+    if (hook_in) {
+        s = hooks->in_proj(*hooks, hidden, batch, const_cast<uint8_t*>(q_in), zx, fused ? cnt : nullptr,
+                           fused ? batch * p->g.n_groups : 0, wsb + w.pub.total, st);
+        if (s != NHM_OK) return s;
+    } else if (batch > 32) {
         if (fused) launch_clear(cnt, batch * p->g.n_groups, st);
         if ((s = project(q_in, H, batch, p->in_proj, zx, l.d_in_proj, st, nullptr,
                          reinterpret_cast<float*>(wsb + w.part), w.part_bytes, true)) != NHM_OK)
             return s;
     }
-    for (int32_t r0 = 0; batch <= 32 && r0 < batch; r0 += 16) {
+    for (int32_t r0 = 0; !hook_in && batch <= 32 && r0 < batch; r0 += 16) {
         const int mg = batch - r0 < 16 ? batch - r0 : 16;
         s = launch_gemv(q_in + (int64_t)r0 * H, H, mg, p->in_proj.w, p->in_proj.w_scale, p->in_proj.a_scale,
                         l.d_in_proj, H, zx + (int64_t)r0 * l.d_in_proj, l.d_in_proj, st, nullptr, nullptr, 0, nullptr,
@@ -553,6 +559,8 @@ static nhm_status decode_call(const nhm_mixer_params* p, const uint16_t* hidden,
     ga.c_off = l.c_off;
     ga.d_state = p->g.d_state;
     if (!fused && (s = launch_gnorm_quant(ga, st)) != NHM_OK) return s;
+    if (hooks && hooks->out_proj)
+        return hooks->out_proj(*hooks, reinterpret_cast<uint16_t*>(wsb + w.pub.norm), q_out, batch, out, wsb + w.pub.total, st);
     // out_proj above 32 rows in one GEMM call (which splits k for these narrow shapes), reading
     // the weight once instead of once per 16 rows: one block at B = 64 104.9 -> 98.0 us; at
     // B = 32 two GEMV launches stay ahead (60.0 against 61.6 us). in_proj stays on the GEMV per
@@ -585,7 +593,7 @@ extern "C" {
 nhm_status nhm_mixer_decode_ex(const nhm_mixer_params* p, const uint16_t* hidden, int32_t batch,
                                const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type, uint16_t* conv_pool,
                                int32_t n_slots, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
-    return decode_call(p, hidden, nullptr, batch, slot_idx, ssm_pool, ssm_type, conv_pool, n_slots, out, nullptr,
+    return mixer_decode_call(p, hidden, nullptr, batch, slot_idx, ssm_pool, ssm_type, conv_pool, n_slots, out, nullptr,
                        nullptr, ws, ws_bytes, stream, false);
 }
 
@@ -593,14 +601,14 @@ nhm_status nhm_mixer_decode_q(const nhm_mixer_params* p, const uint16_t* hidden,
                               const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type, uint16_t* conv_pool,
                               int32_t n_slots, uint16_t* out, uint8_t* out_q, const float* out_q_scale, void* ws,
                               size_t ws_bytes, void* stream) {
-    return decode_call(p, hidden, hidden_q, batch, slot_idx, ssm_pool, ssm_type, conv_pool, n_slots, out, out_q,
+    return mixer_decode_call(p, hidden, hidden_q, batch, slot_idx, ssm_pool, ssm_type, conv_pool, n_slots, out, out_q,
                        out_q_scale, ws, ws_bytes, stream, false);
 }
 
 nhm_status nhm_mixer_decode_noalloc(const nhm_mixer_params* p, const uint16_t* hidden, int32_t batch,
                                     const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type, uint16_t* conv_pool,
                                     int32_t n_slots, uint16_t* out, void* stream) {
-    return decode_call(p, hidden, nullptr, batch, slot_idx, ssm_pool, ssm_type, conv_pool, n_slots, out, nullptr,
+    return mixer_decode_call(p, hidden, nullptr, batch, slot_idx, ssm_pool, ssm_type, conv_pool, n_slots, out, nullptr,
                        nullptr, nullptr, 0, stream, true);
 }
 
@@ -617,6 +625,17 @@ nhm_status nhm_mixer_prefill_ex(const nhm_mixer_params* p, const uint16_t* hidde
                                 const int32_t* has_initial, int32_t chunk, void* ssm_pool, nhm_dtype ssm_type,
                                 uint16_t* conv_pool, int32_t n_slots, uint16_t* out, void* ws, size_t ws_bytes,
                                 void* stream) {
+    return mixer_prefill_call(p, hidden, n_tokens, cu_seqlens, n_seqs, slot_idx, has_initial, chunk, ssm_pool, ssm_type,
+                              conv_pool, n_slots, out, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+nhm_status nhm::mixer_prefill_call(const nhm_mixer_params* p, const uint16_t* hidden, int64_t n_tokens,
+                                   const int32_t* cu_seqlens, int32_t n_seqs, const int32_t* slot_idx,
+                                   const int32_t* has_initial, int32_t chunk, void* ssm_pool, nhm_dtype ssm_type,
+                                   uint16_t* conv_pool, int32_t n_slots, uint16_t* out, void* ws, size_t ws_bytes,
+                                   void* stream, const ProjectionHooks* hooks) {
     g_err[0] = 0;
     if (ssm_type != NHM_F32 && ssm_type != NHM_BF16)
         return fail(NHM_ERR_UNSUPPORTED, "SSM state dtype %d: f32 or bf16", (int)ssm_type);
@@ -639,8 +658,8 @@ nhm_status nhm_mixer_prefill_ex(const nhm_mixer_params* p, const uint16_t* hidde
         !aligned(ws, 256))
         return fail(NHM_ERR_ALIGN, "hidden, out and pools must be 16-byte aligned, ws 256-byte aligned");
     const MixerWs w = prefill_ws(&p->g, n_tokens, n_seqs, chunk);
-    if (ws_bytes < w.pub.total)
-        return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", w.pub.total, ws_bytes);
+    const size_t total = w.pub.total + (hooks ? hooks->extra : 0);
+    if (ws_bytes < total) return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", total, ws_bytes);
     if ((int64_t)w.max_chunks * p->g.n_heads > INT32_MAX)   // one scan block per (chunk, head)
         return fail(NHM_ERR_UNSUPPORTED, "%d chunks x %d heads exceed the scan's grid", w.max_chunks, p->g.n_heads);
     if ((s = check_offsets(n_tokens, p->g.hidden, l.d_in_proj, p->g.hidden, "prefill in_proj")) != NHM_OK ||
@@ -651,7 +670,9 @@ nhm_status nhm_mixer_prefill_ex(const nhm_mixer_params* p, const uint16_t* hidde
     const int64_t H = p->g.hidden;
     uint8_t* q_in = reinterpret_cast<uint8_t*>(wsb + w.pub.q_in);
     uint16_t* zx = reinterpret_cast<uint16_t*>(wsb + w.pub.zxbcdt);
-    if (n_tokens > 0) {
+    if (n_tokens > 0 && hooks && hooks->in_proj) {
+        if ((s = hooks->in_proj(*hooks, hidden, n_tokens, q_in, zx, nullptr, 0, wsb + w.pub.total, st)) != NHM_OK) return s;
+    } else if (n_tokens > 0) {
         launch_quantize(hidden, n_tokens, H, H, p->in_proj.a_scale, q_in, H, st);
         if ((s = check_launch("prefill quant")) != NHM_OK) return s;
         // every product summed in f32: the e4m3 MFMA's coarser 128-product sums move about 1 %
@@ -701,10 +722,10 @@ nhm_status nhm_mixer_prefill_ex(const nhm_mixer_params* p, const uint16_t* hidde
     a.norm = reinterpret_cast<uint16_t*>(wsb + w.pub.norm);
     a.q_out = reinterpret_cast<uint8_t*>(wsb + w.pub.q_out);
     if ((s = launch_prefill_mid(a, st)) != NHM_OK) return s;
+    if (n_tokens > 0 && hooks && hooks->out_proj)
+        return hooks->out_proj(*hooks, a.norm, a.q_out, n_tokens, out, wsb + w.pub.total, st);
     if (n_tokens > 0)
         return project(a.q_out, l.d_inner, n_tokens, p->out_proj, out, H, st, nullptr,
                        reinterpret_cast<float*>(wsb + w.part), w.part_bytes);
     return NHM_OK;
 }
-
-}  // extern "C"

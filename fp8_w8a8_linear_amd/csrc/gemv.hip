@@ -350,9 +350,11 @@ nhm_status launch_gemv(const uint8_t* a, int64_t lda, int m, const uint8_t* w, c
 
 nhm_status launch_gemv_lora(const uint8_t* a, int64_t lda, int m, const uint8_t* w, const float* w_scale,
                             const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
-                            float* out_f32, int ws_step, const LoraEpi& lora) {
+                            float* out_f32, int ws_step, const LoraEpi& lora, uint32_t* clear, int clear_n) {
     GemvArgs g{};
     g.ws_step = ws_step;
+    g.clear = clear_n > 0 ? clear : nullptr;
+    g.clear_n = clear_n;
     g.a = a; g.lda = lda; g.m = m;
     g.w = w; g.w_scale = w_scale; g.a_scale = a_scale; g.n = n; g.k = k;
     g.out = out; g.ld_out = ld_out;

@@ -55,6 +55,33 @@ nhm_status project(const uint8_t* a, int64_t lda, int64_t m, const nhm_fp8_weigh
                    hipStream_t st, float* out_f32 = nullptr, float* part = nullptr, size_t part_bytes = 0,
                    bool exact = false, uint8_t* out_q = nullptr, int64_t ld_q = 0, const float* q_scale = nullptr);
 
+// The mixer's projections done by the caller: nhm_mixer_decode and nhm_mixer_prefill with a hook in place
+// of a projection call it where they would quantize and project themselves. extra: workspace bytes
+// past the call's own, which the hooks get as `ws`.
+struct ProjectionHooks {
+    // block input [m, hidden] bf16 -> its codes q and the in_proj output zx; clear_n words at clear (if any) zeroed
+    nhm_status (*in_proj)(const ProjectionHooks& h, const uint16_t* hidden, int64_t m, uint8_t* q, uint16_t* zx,
+                          uint32_t* clear, int clear_n, char* ws, hipStream_t st) = nullptr;
+    // norm output [m, d_inner] bf16 and its codes q -> block output
+    nhm_status (*out_proj)(const ProjectionHooks& h, const uint16_t* norm, const uint8_t* q, int64_t m, uint16_t* out,
+                           char* ws, hipStream_t st) = nullptr;
+    size_t extra = 0;
+    const nhm_mixer_params* p = nullptr;
+    const nhm_lora* lora_in = nullptr;
+    const nhm_lora* lora_out = nullptr;
+    const int32_t* row_adapter = nullptr;
+    bool decode = false;
+};
+nhm_status mixer_decode_call(const nhm_mixer_params* p, const uint16_t* hidden, const uint8_t* hidden_q, int32_t batch,
+                             const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type, uint16_t* conv_pool,
+                             int32_t n_slots, uint16_t* out, uint8_t* out_q, const float* out_q_scale, void* ws,
+                             size_t ws_bytes, void* stream, bool noalloc, const ProjectionHooks* hooks = nullptr);
+nhm_status mixer_prefill_call(const nhm_mixer_params* p, const uint16_t* hidden, int64_t n_tokens,
+                              const int32_t* cu_seqlens, int32_t n_seqs, const int32_t* slot_idx,
+                              const int32_t* has_initial, int32_t chunk, void* ssm_pool, nhm_dtype ssm_type,
+                              uint16_t* conv_pool, int32_t n_slots, uint16_t* out, void* ws, size_t ws_bytes,
+                              void* stream, const ProjectionHooks* hooks = nullptr);
+
 // ---- activation quant (quant.hip)
 void launch_quantize(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, const float* scale,
                      uint8_t* q, int64_t ld_q, hipStream_t st);
@@ -213,7 +240,8 @@ nhm_status launch_lora_down(const LoraDownArgs& g, hipStream_t st);
 // The projections with the adapters' part (the same kernels and choices as without, no split over k).
 nhm_status launch_gemv_lora(const uint8_t* a, int64_t lda, int m, const uint8_t* w, const float* w_scale,
                             const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
-                            float* out_f32, int ws_step, const LoraEpi& lora);
+                            float* out_f32, int ws_step, const LoraEpi& lora, uint32_t* clear = nullptr,
+                            int clear_n = 0);
 nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* w, const float* w_scale,
                             const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
                             float* out_f32, bool exact, int ws_step, const LoraEpi& lora);

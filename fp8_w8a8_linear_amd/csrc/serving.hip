@@ -30,6 +30,93 @@ nhm_status check_lora(const nhm_lora* l) {
     return NHM_OK;
 }
 
+// ---- the mixer's projections with adapters
+
+// The low-rank product's workspace of m rows, bf16 outputs.
+size_t mixer_t_bytes(int64_t m, int32_t rank) { return align_up((size_t)m * 2 * lora_rp(rank) * sizeof(uint16_t), 256); }
+
+LoraDownArgs down_args(const ProjectionHooks& h, const nhm_lora* l, const uint16_t* x, int64_t m, const nhm_fp8_weight& w,
+                       uint8_t* q, char* ws) {
+    LoraDownArgs g{};
+    g.x = x;
+    g.ld_x = w.k;
+    g.m = m; g.k = w.k;
+    g.a_scale = w.a_scale;
+    g.q = q;
+    g.a = l->a; g.scale = l->scale;
+    g.n_adapters = l->n_adapters; g.rank = l->rank;
+    g.rp = lora_rp(l->rank);
+    g.parts = 2;
+    g.row_adapter = h.row_adapter;
+    g.t = reinterpret_cast<uint16_t*>(ws);
+    return g;
+}
+
+// One projection of m rows: up to 32 decode rows 16 at a time on the GEMV, as the mixer's own, else one call.
+nhm_status project_rows(const LoraDownArgs& d, const nhm_lora* l, const nhm_fp8_weight& w, const uint8_t* q, uint16_t* out,
+                        bool decode, bool exact, uint32_t* clear, int clear_n, hipStream_t st) {
+    const LoraEpi e{d.t, l->b, d.row_adapter, d.n_adapters, d.rank, d.rp, d.parts};
+    const int64_t m = d.m;
+    if (decode ? m <= 32 && use_gemv(16, w.n, w.k) : use_gemv(m, w.n, w.k)) {
+        for (int64_t r0 = 0; r0 < m; r0 += 16) {
+            LoraEpi er = e;
+            er.t += r0 * e.parts * e.rp;
+            er.row_adapter += r0;
+            const nhm_status s = launch_gemv_lora(q + r0 * w.k, w.k, (int)(m - r0 < 16 ? m - r0 : 16), w.w, w.w_scale,
+                                                  w.a_scale, w.n, w.k, out + r0 * w.n, w.n, st, nullptr, ws_step(w), er,
+                                                  r0 == 0 ? clear : nullptr, r0 == 0 ? clear_n : 0);
+            if (s != NHM_OK) return s;
+        }
+        return NHM_OK;
+    }
+    if (clear && clear_n > 0) launch_clear(clear, clear_n, st);
+    return launch_gemm_lora(q, w.k, m, w.w, w.w_scale, w.a_scale, w.n, w.k, out, w.n, st, nullptr, exact, ws_step(w), e);
+}
+
+nhm_status hook_in(const ProjectionHooks& h, const uint16_t* hidden, int64_t m, uint8_t* q, uint16_t* zx, uint32_t* clear,
+                   int clear_n, char* ws, hipStream_t st) {
+    const LoraDownArgs d = down_args(h, h.lora_in, hidden, m, h.p->in_proj, q, ws);
+    const nhm_status s = launch_lora_down(d, st);
+    // every product summed in f32, as the mixer's own in_proj
+    return s != NHM_OK ? s : project_rows(d, h.lora_in, h.p->in_proj, q, zx, h.decode, true, clear, clear_n, st);
+}
+
+nhm_status hook_out(const ProjectionHooks& h, const uint16_t* norm, const uint8_t* q, int64_t m, uint16_t* out, char* ws,
+                    hipStream_t st) {
+    const LoraDownArgs d = down_args(h, h.lora_out, norm, m, h.p->out_proj, nullptr, ws);
+    const nhm_status s = launch_lora_down(d, st);
+    return s != NHM_OK ? s : project_rows(d, h.lora_out, h.p->out_proj, q, out, h.decode, false, nullptr, 0, st);
+}
+
+// Checks the adapters of a mixer call and fills in its hooks (either set of adapters may be NULL).
+nhm_status mixer_hooks(ProjectionHooks& h, const nhm_mixer_params* p, const nhm_lora* in, const nhm_lora* out,
+                       const int32_t* row_adapter, int64_t m, bool decode) {
+    if (!p) return fail(NHM_ERR_NULL, "params is NULL");
+    h.p = p;
+    h.row_adapter = row_adapter;
+    h.decode = decode;
+    for (int i = 0; i < 2; ++i) {
+        const nhm_lora* l = i == 0 ? in : out;
+        if (!l) continue;
+        const int64_t n = i == 0 ? p->in_proj.n : p->out_proj.n;
+        const nhm_status s = check_lora(l);
+        if (s != NHM_OK) return s;
+        if (n >= (int64_t(1) << 30) / l->rank)
+            return fail(NHM_ERR_UNSUPPORTED, "lora: an adapter's b of 2 GiB or more");
+        const size_t t = mixer_t_bytes(m, l->rank);
+        h.extra = h.extra > t ? h.extra : t;
+    }
+    if ((in || out) && m > 0) {
+        if (!row_adapter) return fail(NHM_ERR_NULL, "row_adapter is NULL");
+        if (!aligned(row_adapter, 4)) return fail(NHM_ERR_ALIGN, "row_adapter must be 4-byte aligned");
+    }
+    h.lora_in = in;
+    h.lora_out = out;
+    h.in_proj = in ? hook_in : nullptr;
+    h.out_proj = out ? hook_out : nullptr;
+    return NHM_OK;
+}
+
 constexpr int kMaxBeams = 32, kMaxCand = 64;
 constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxRows = int64_t(1) << 24;
 
@@ -59,7 +146,7 @@ nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64
     if (m > INT_MAX) return fail(NHM_ERR_SHAPE, "m %lld out of range", (long long)m);
     if (!row_adapter) return fail(NHM_ERR_NULL, "row_adapter is NULL");
     if (!aligned(row_adapter, 4)) return fail(NHM_ERR_ALIGN, "row_adapter must be 4-byte aligned");
-    if (w->n * lora->rank >= (int64_t(1) << 30))       // 32-bit byte offsets within one adapter's B
+    if (w->n >= (int64_t(1) << 30) / lora->rank)       // 32-bit byte offsets within one adapter's B
         return fail(NHM_ERR_UNSUPPORTED, "lora: an adapter's b of 2 GiB or more");
     hipStream_t st = (hipStream_t)stream;
     const LoraWs l = lora_ws(m, w->k, a_type, lora->rank);
@@ -88,6 +175,50 @@ nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64
         return launch_gemv_lora(q, ld_q, (int)m, w->w, w->w_scale, w->a_scale, w->n, w->k, ob, ld_out, st, of, ws_step(*w), epi);
     return launch_gemm_lora(q, ld_q, m, w->w, w->w_scale, w->a_scale, w->n, w->k, ob, ld_out, st, of, exact != 0, ws_step(*w),
                             epi);
+}
+
+nhm_status nhm_mixer_decode_lora_ws_layout(const nhm_geometry* g, int32_t batch, int32_t rank, nhm_ws_layout* out) {
+    const nhm_status s = nhm_mixer_decode_ws_layout(g, batch, out);
+    if (s != NHM_OK) return s;
+    if (!rank_ok(rank)) return fail(NHM_ERR_UNSUPPORTED, "lora: rank %d: a multiple of 8 in 8 .. 128", rank);
+    out->total += mixer_t_bytes(batch, rank);
+    return NHM_OK;
+}
+
+nhm_status nhm_mixer_prefill_lora_ws_layout(const nhm_geometry* g, int64_t n_tokens, int32_t n_seqs, int32_t chunk,
+                                            int32_t rank, nhm_ws_layout* out) {
+    const nhm_status s = nhm_mixer_prefill_ws_layout(g, n_tokens, n_seqs, chunk, out);
+    if (s != NHM_OK) return s;
+    if (!rank_ok(rank)) return fail(NHM_ERR_UNSUPPORTED, "lora: rank %d: a multiple of 8 in 8 .. 128", rank);
+    out->total += mixer_t_bytes(n_tokens, rank);
+    return NHM_OK;
+}
+
+nhm_status nhm_mixer_decode_lora(const nhm_mixer_params* p, const nhm_lora* lora_in, const nhm_lora* lora_out,
+                                 const int32_t* row_adapter, const uint16_t* hidden, int32_t batch,
+                                 const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type, uint16_t* conv_pool,
+                                 int32_t n_slots, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+    clear_error();
+    ProjectionHooks h;
+    const nhm_status s = mixer_hooks(h, p, lora_in, lora_out, row_adapter, batch < 0 ? 0 : batch, true);
+    if (s != NHM_OK) return s;
+    return mixer_decode_call(p, hidden, nullptr, batch, slot_idx, ssm_pool, ssm_type, conv_pool, n_slots, out, nullptr,
+                             nullptr, ws, ws_bytes, stream, false, &h);
+}
+
+nhm_status nhm_mixer_prefill_lora(const nhm_mixer_params* p, const nhm_lora* lora_in, const nhm_lora* lora_out,
+                                  const int32_t* row_adapter, const uint16_t* hidden, int64_t n_tokens,
+                                  const int32_t* cu_seqlens, int32_t n_seqs, const int32_t* slot_idx,
+                                  const int32_t* has_initial, int32_t chunk, void* ssm_pool, nhm_dtype ssm_type,
+                                  uint16_t* conv_pool, int32_t n_slots, uint16_t* out, void* ws, size_t ws_bytes,
+                                  void* stream) {
+    clear_error();
+    if (n_tokens > INT_MAX) return fail(NHM_ERR_SHAPE, "n_tokens %lld out of range", (long long)n_tokens);
+    ProjectionHooks h;
+    const nhm_status s = mixer_hooks(h, p, lora_in, lora_out, row_adapter, n_tokens < 0 ? 0 : n_tokens, false);
+    if (s != NHM_OK) return s;
+    return mixer_prefill_call(p, hidden, n_tokens, cu_seqlens, n_seqs, slot_idx, has_initial, chunk, ssm_pool, ssm_type,
+                              conv_pool, n_slots, out, ws, ws_bytes, stream, &h);
 }
 
 size_t nhm_beam_select_workspace_bytes(int64_t n_groups, int32_t n_beams, int64_t vocab, int32_t n_cand) {

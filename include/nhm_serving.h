@@ -57,6 +57,31 @@ NHM_API nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t 
                                        void* out, nhm_dtype out_type, int64_t ld_out, int32_t exact, void* ws,
                                        size_t ws_bytes, void* stream);
 
+/* nhm_mixer_decode_ex and nhm_mixer_prefill_ex with adapters beside the projections: lora_in of in_proj
+ * (n = d_in_proj, k = hidden) on the block input, lora_out of out_proj (n = hidden, k = d_inner) on the
+ * bf16 gated norm output. Either may be NULL: that projection runs as without. row_adapter (device) int32
+ * [batch] or [n_tokens] as for nhm_fp8_linear_lora (nhm_batch_plan's token_adapter is one), the same
+ * for both sets, which may differ in rank and number. in_proj sums every product in f32, out_proj as in
+ * the calls without adapters; where those split out_proj over k, these do not.
+ * A padded decode row (negative slot) has a zero norm output, so its output stays zero with any
+ * finite adapter. ws: the layout calls below, with the larger rank of the two sets.
+ * Errors: those of the calls without adapters and of nhm_fp8_linear_lora. */
+NHM_API nhm_status nhm_mixer_decode_lora_ws_layout(const nhm_geometry* g, int32_t batch, int32_t rank,
+                                                   nhm_ws_layout* out);
+NHM_API nhm_status nhm_mixer_decode_lora(const nhm_mixer_params* p, const nhm_lora* lora_in, const nhm_lora* lora_out,
+                                         const int32_t* row_adapter, const uint16_t* hidden, int32_t batch,
+                                         const int32_t* slot_idx, void* ssm_pool, nhm_dtype ssm_type,
+                                         uint16_t* conv_pool, int32_t n_slots, uint16_t* out, void* ws, size_t ws_bytes,
+                                         void* stream);
+NHM_API nhm_status nhm_mixer_prefill_lora_ws_layout(const nhm_geometry* g, int64_t n_tokens, int32_t n_seqs,
+                                                    int32_t chunk, int32_t rank, nhm_ws_layout* out);
+NHM_API nhm_status nhm_mixer_prefill_lora(const nhm_mixer_params* p, const nhm_lora* lora_in, const nhm_lora* lora_out,
+                                          const int32_t* row_adapter, const uint16_t* hidden, int64_t n_tokens,
+                                          const int32_t* cu_seqlens, int32_t n_seqs, const int32_t* slot_idx,
+                                          const int32_t* has_initial, int32_t chunk, void* ssm_pool,
+                                          nhm_dtype ssm_type, uint16_t* conv_pool, int32_t n_slots, uint16_t* out,
+                                          void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- beam search */
 
 /* Workspace bytes of nhm_beam_select (0 for arguments outside its limits). */

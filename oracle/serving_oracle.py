@@ -7,9 +7,10 @@ from __future__ import annotations
 
 import numpy as np
 
-from .nhm_oracle import bf16_to_f64, e4m3_decode, fp8_linear, quantize_static
+from .nhm_oracle import (GEOMETRY, bf16_from_f64, bf16_to_f64, causal_conv1d_silu, dt_and_decay, e4m3_decode, fp8_linear,
+                         gated_group_rmsnorm, layout, quantize_static, ssm_scan_sequential)
 
-__all__ = ["fp8_linear_lora", "lora_bound", "beam_select", "beam_reorder", "batch_plan"]
+__all__ = ["fp8_linear_lora", "lora_bound", "mixer_sequence_lora", "beam_select", "beam_reorder", "batch_plan"]
 
 
 def _lora_input(a, a_scale, codes):
@@ -59,6 +60,33 @@ def lora_bound(a, w_codes, w_scale, a_scale, lora_a, lora_b, lora_scale, row_ada
         tol[rows] += ((2.0 ** -25 if f32 else 2.0 ** -17) + (rank + 8) * 2.0 ** -24) * (t_abs @ B.T)
         tol[rows] += 2.0 ** -22 * (t_abs @ B.T)
     return tol
+
+
+def mixer_sequence_lora(p, lora_in, lora_out, adapter, hidden, window, state, g=GEOMETRY):
+    """One mixer block over one sequence, from a carried window and state, with adapters beside both
+    projections (lora_*: (a, b, scale) or None; adapter int [T]): the stages of mixer_sequence with the adapters'
+    part added to a projection before its one rounding to bf16. Without adapters it is mixer_sequence."""
+    lay = layout(g)
+    H, P, N, G = g["n_heads"], g["head_dim"], g["d_state"], g["n_groups"]
+    T = hidden.shape[0]
+
+    def project(x, w, ws, sa, lora):
+        if lora is None:
+            return fp8_linear(quantize_static(x, sa), w, ws, sa)
+        return fp8_linear_lora(x, w, ws, sa, *lora, adapter)
+
+    zx = bf16_from_f64(project(hidden, p["in_w"], p["in_w_scale"], p["in_a_scale"], lora_in))
+    z = zx[:, lay["z_off"]:lay["z_off"] + lay["z_width"]]
+    xbc = zx[:, lay["xbc_off"]:lay["xbc_off"] + lay["xbc_width"]]
+    _, conv, new_window = causal_conv1d_silu(xbc, window, p["conv_w"], p["conv_b"])
+    part = lambda o, n: bf16_to_f64(conv[:, lay[o]:lay[o] + lay[n]])  # noqa: E731
+    dt, dA = dt_and_decay(zx[:, lay["dt_off"]:lay["dt_off"] + lay["dt_width"]], p["dt_bias"], p["A_log"])
+    y, h = ssm_scan_sequential(part("x_off", "x_width").reshape(T, H, P), part("b_off", "b_width").reshape(T, G, N),
+                               part("c_off", "c_width").reshape(T, G, N), dt, dA, p["D"],
+                               np.asarray(state, np.float32).astype(np.float64))
+    _, norm = gated_group_rmsnorm(bf16_from_f64(y.reshape(T, H * P)), z, p["norm_w"], G, g["rms_eps"])
+    out = project(norm, p["out_w"], p["out_w_scale"], p["out_a_scale"], lora_out)
+    return out, new_window, h.astype(np.float32)
 
 
 def beam_select(logits, cum, n_cand, finished=None, eos=0):

@@ -37,7 +37,7 @@ nhm_status launch_gnorm_quant(const GnormArgs&, hipStream_t) { reached("launch_g
 nhm_status launch_prefill_mid(const PrefillArgs&, hipStream_t) { reached("launch_prefill_mid"); }
 nhm_status launch_lora_down(const LoraDownArgs&, hipStream_t) { reached("launch_lora_down"); }
 nhm_status launch_gemv_lora(const uint8_t*, int64_t, int, const uint8_t*, const float*, const float*, int64_t, int64_t,
-                            uint16_t*, int64_t, hipStream_t, float*, int, const LoraEpi&) {
+                            uint16_t*, int64_t, hipStream_t, float*, int, const LoraEpi&, uint32_t*, int) {
     reached("launch_gemv_lora");
 }
 nhm_status launch_gemm_lora(const uint8_t*, int64_t, int64_t, const uint8_t*, const float*, const float*, int64_t, int64_t,

@@ -60,3 +60,19 @@ def test_batch_plan_by_hand():
     assert p["token_seq"].tolist() == [0, 0, 2, 2, 2, -1, -1]
     assert p["token_pos"].tolist() == [0, 1, 9, 10, 11, -1, -1]
     assert p["token_adapter"].tolist() == [5, 5, -1, -1, -1, -1, -1]
+
+
+def test_mixer_without_adapters_is_the_mixer():
+    from oracle import mixer_sequence
+    g = dict(hidden=256, n_heads=8, head_dim=64, d_state=128, n_groups=2, conv_width=4, rms_eps=1e-5)
+    import workloads.synthetic as w
+    p = w.block_params(3, 0, g)
+    h, win, st = w.hidden(3, 4, g), w.conv_pool(3, 0, 1, g=g)[0], w.ssm_pool(3, 0, 1, g=g)[0]
+    ref = mixer_sequence(p, h, win, st, g)
+    lay_n, inner = p["in_w"].shape[0], p["out_w"].shape[1]
+    zero_in = (np.zeros((1, 8, 256), np.uint16), np.zeros((1, lay_n, 8), np.uint16), None)
+    zero_out = (np.zeros((1, 8, inner), np.uint16), np.zeros((1, 256, 8), np.uint16), None)
+    for li, lo in ((None, None), (zero_in, zero_out)):
+        out, window, state = so.mixer_sequence_lora(p, li, lo, np.zeros(4, np.int32), h, win, st, g)
+        assert np.array_equal(out, ref["out"]) and np.array_equal(window, ref["window"])
+        assert np.array_equal(state, ref["state"])

@@ -56,6 +56,53 @@ def test_lora_refusals(nhm):
     assert nhm.lib.nhm_fp8_linear_lora(A, 0, 8, 4096, C.byref(big), C.byref(lo), ID, O, 0, 1 << 19, 0, WS, 1 << 62, None) == 4
 
 
+def _mixer_args(nhm):
+    g = nhm.Geometry(**nhm.GEOMETRY)
+    w = lambda n, k: nhm._Fp8Weight(0x1000, 0x2000, 0x3000, n, k, 0)  # noqa: E731
+    return nhm._MixerParams(g, w(10304, 2688), w(2688, 4096), 0x5000, 0x6000, 0x7000, 0x8000, 0x9000, 0xA000)
+
+
+def test_mixer_lora_refusals(nhm):
+    """The mixer calls with adapters: their checks of the adapter sets, then those of the calls without."""
+    H, SL, SP, CP, O, WS, ID, CU, HI = [0x100000 * i for i in range(1, 10)]
+    p = _mixer_args(nhm)
+    ok = nhm._Lora(0x10000, 0x20000, 0x30000, 4, 16)
+    big = nhm._Lora(0x10000, 0x20000, None, 4, 64)
+
+    def dec(li=ok, lo=big, ids=ID, hidden=H, batch=8, wsb=None, ws=WS, pp=p):
+        ref = lambda l: None if l is None else C.byref(l)  # noqa: E731
+        wsb = nhm.decode_lora_ws_layout(8, 64)["total"] if wsb is None else wsb
+        return nhm.lib.nhm_mixer_decode_lora(None if pp is None else C.byref(pp), ref(li), ref(lo), ids, hidden, batch, SL, SP,
+                                             nhm.NHM_F32, CP, 64, O, ws, wsb, None)
+
+    def pre(li=ok, lo=big, ids=ID, hidden=H, T=40, n=2, wsb=None):
+        ref = lambda l: None if l is None else C.byref(l)  # noqa: E731
+        wsb = nhm.prefill_lora_ws_layout(40, 2, 64)["total"] if wsb is None else wsb
+        return nhm.lib.nhm_mixer_prefill_lora(C.byref(p), ref(li), ref(lo), ids, hidden, T, CU, n, SL, HI, 128, SP, nhm.NHM_F32,
+                                              CP, 64, O, WS, wsb, None)
+
+    assert dec(batch=0) == 0 and dec(batch=0, ids=None) == 0 and pre(T=0, n=0) == 0
+    assert dec(pp=None) == 1
+    for call, need in ((dec, nhm.decode_lora_ws_layout(8, 64)["total"]), (pre, nhm.prefill_lora_ws_layout(40, 2, 64)["total"])):
+        for over, status in [(dict(ids=None), 1), (dict(ids=ID + 2), 3), (dict(hidden=None), 1), (dict(hidden=H + 8), 3),
+                             (dict(wsb=need - 1), 5), (dict(li=nhm._Lora(0, 0x20000, None, 4, 16)), 1),
+                             (dict(lo=nhm._Lora(0x10000, 0x20008, None, 4, 16)), 3),
+                             (dict(li=nhm._Lora(0x10000, 0x20000, None, 0, 16)), 2),
+                             (dict(lo=nhm._Lora(0x10000, 0x20000, None, 4, 20)), 4)]:
+            st = call(**over)
+            assert st == status, (call, over, st, nhm.lib.nhm_last_error())
+    assert pre(T=-1) == 2 and pre(T=1 << 31) == 2 and dec(batch=-1) == 2
+    base = nhm.decode_ws_layout(8)
+    lay = nhm.decode_lora_ws_layout(8, 64)
+    assert lay["total"] > base["total"] and all(lay[k] == base[k] for k in base if k != "total")
+    assert nhm.prefill_lora_ws_layout(512, 2, 8)["total"] > nhm.prefill_ws_layout(512, 2)["total"]
+    for bad in (0, 4, 12, 136):
+        with pytest.raises(nhm.NhmError):
+            nhm.decode_lora_ws_layout(8, bad)
+        with pytest.raises(nhm.NhmError):
+            nhm.prefill_lora_ws_layout(512, 2, bad)
+
+
 def test_beam_select_refusals(nhm):
     X, CU, FI, SC, PA, TO, WS = [0x10000 * i for i in range(1, 8)]
     need = nhm.beam_select_workspace_bytes(2, 4, 1000, 8)
