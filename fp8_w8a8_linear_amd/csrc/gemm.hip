@@ -51,6 +51,7 @@ struct GemmArgs {
     int ws_step = 1;    // weight scale index step: 1 per channel, 0 per tensor
     int panel_rows = 0; // panel kernel: weight rows per panel (0: all of its waves' rows)
     LoraEpi lora;       // the kernels with adapters only: kLora 1 (bf16 output, t in two parts) or 2 (f32, three)
+    const float* delta = nullptr;   // kLora 3: the adapters' part [m, lora_ld(n)], formed ahead of the GEMM
 };
 
 // Row r of a 128-byte-wide LDS tile holds its 16-byte chunk c at slot c ^ (r & 7):
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     static_assert(WN % 16 == 0 && BM % 32 == 0, "tile shape");
     // the activation tiles, and after the k loop the adapters' operands (with adapters: room for B of
     // eight at a time, whose round trips would follow one another in a batch of many adapters)
-    constexpr int kLds = kLora ? 3 * BM * 128 + 8 * BN * 128 : 3 * BM * 128;
+    constexpr int kLds = kLora == 1 || kLora == 2 ? 3 * BM * 128 + 8 * BN * 128 : 3 * BM * 128;
     __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
     uint8_t (&sA)[3][BM * 128] = *reinterpret_cast<uint8_t (*)[3][BM * 128]>(smem);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane >> 4, r16 = lane & 15;
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     const int64_t pend = min((int64_t)(pan + 1) * PW, g.n);
     const int64_t m0 = (int64_t)mt * BM, nw0 = (int64_t)pan * PW + wave * WN;
     LoraRows<BM> lrows;
-    if constexpr (kLora != 0) lrows.load(g.lora, m0, g.m, lane);
+    if constexpr (kLora == 1 || kLora == 2) lrows.load(g.lora, m0, g.m, lane);
     const int nk = (int)((g.k + 127) / 128);
     const int ns = (nk + U - 1) / U * U;   // steps, padded to the unroll (padding steps read zeros)
 
@@ -462,10 +463,21 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
         int id[TM];
 #pragma unroll
         for (int j = 0; j < TM; ++j) id[j] = lora_row(g.lora, m0 + j * 16 + r16, g.m);
-        lora_tile<BN, BM, 256, kLds, true>(g.lora, lrows, m0, g.m, (int64_t)pan * PW, g.n, pend, smem, __builtin_amdgcn_readfirstlane(wave), lane,
-                               [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
-                                   lora_mma16<BM, kLora + 1>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
-                               });
+        if constexpr (kLora == 3) {     // rows without an adapter keep their sums' bits
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+#pragma unroll
+                for (int i = 0; i < TN; ++i) {
+                    const int64_t nb = nw0 + i * 16 + 4 * q, ld = lora_ld(g.n);
+                    if (id[j] < 0 || nb >= ld) continue;
+                    acc[i][j] += *reinterpret_cast<const v4f*>(g.delta + (m0 + j * 16 + r16) * ld + nb);
+                }
+        } else {
+            lora_tile<BN, BM, 256, kLds, true>(g.lora, lrows, m0, g.m, (int64_t)pan * PW, g.n, pend, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+                                   [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
+                                       lora_mma16<BM, kLora + 1>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
+                                   });
+        }
     }
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
@@ -475,7 +487,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
         for (int r = 0; r < 4; ++r) sc[r] = kLora ? 1.0f : sa * wsc[i][r];
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-            if (kLora ? kLora == 2 : g.out_f32 != nullptr)
+            if (kLora == 1 || kLora == 2 ? kLora == 2 : g.out_f32 != nullptr)
                 store_tile_f32(g.out_f32, g.ld_out, m0 + j * 16 + r16, nw0 + i * 16 + 4 * q, g.m, pend, acc[i][j], sc, full);
             else
                 store_tile(g.out, g.ld_out, m0 + j * 16 + r16, nw0 + i * 16 + 4 * q, g.m, pend, acc[i][j], sc, full);
@@ -1258,13 +1270,21 @@ nhm_status launch_gemm(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* 
 
 nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* w, const float* w_scale,
                             const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
-                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora) {
+                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora, float* delta) {
     GemmArgs g{a, lda, m, w, w_scale, a_scale, n, k, out, ld_out,
                out_f32 ? ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out_f32) % 16 == 0
                        : ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0,
                out_f32};
     g.ws_step = ws_step;
     g.lora = lora;
+    if (lora_apart(m, n, k) && m * lda < (int64_t(1) << 31)) {
+        const nhm_status s = launch_lora_up(lora, m, n, delta, st);
+        if (s != NHM_OK) return s;
+        g.delta = delta;
+        if (exact) launch_panel<64, 32, true, 3>(g, st);
+        else launch_panel<64, 32, false, 3>(g, st);
+        return check_launch("gemm (panel, adapters)");
+    }
     if (out_f32) return exact ? dispatch_gemm<true, 2>(g, st, nullptr, 0) : dispatch_gemm<false, 2>(g, st, nullptr, 0);
     return exact ? dispatch_gemm<true, 1>(g, st, nullptr, 0) : dispatch_gemm<false, 1>(g, st, nullptr, 0);
 }
