@@ -329,15 +329,16 @@ def mixer_prefill(params: MixerParams, hidden, cu_seqlens, slot_idx, has_initial
 def _on(dev, shapes):
     """Checks (tensor, name, dtypes, shape) entries: contiguous, on `dev`, of one of the dtypes and of the shape
     (None: not checked). Optional tensors may be None."""
+    index = dev.index
     for t, name, dtypes, shape in shapes:
         if t is None:
             continue
         _dev_tensor(t, name)
-        if t.device != dev:
+        if t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
         if t.dtype not in dtypes:
             raise TypeError(f"{name} of dtype {t.dtype}: expected {' or '.join(str(d) for d in dtypes)}")
-        if shape is not None and tuple(t.shape) != shape:
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name} of shape {tuple(t.shape)}: expected {shape}")
 
 
@@ -434,15 +435,19 @@ def prefill_lora_ws_layout(n_tokens, n_seqs, rank, chunk=128, g=GEOMETRY):
     return {n: int(getattr(out, n)) for n, _ in WsLayout._fields_}
 
 
-def _mixer_lora(params, lora_in, lora_out, row_adapter, rows, dev):
-    """The C arguments of the two adapter sets and the row map, checked against the block's projections."""
+def _mixer_lora(params, lora_in, lora_out, row_adapter, hidden, slot_idx, ssm_pool, conv_pool, out, ws):
+    """Checks a mixer call with adapters; the C arguments of the two sets and the row map."""
     import torch
+    dev, shape = hidden.device, (hidden.shape[0], params.geometry["hidden"])
     for lo, w, name in ((lora_in, params.in_proj, "lora_in"), (lora_out, params.out_proj, "lora_out")):
         if lo is not None and (lo.n, lo.k) != (w.n, w.k):
             raise ValueError(f"{name} is for a [{lo.n}, {lo.k}] projection, the block's is [{w.n}, {w.k}]")
         if lo is not None and lo.a.device != dev:
             raise ValueError(f"{name} is on {lo.a.device}, not on {dev}")
-    _on(dev, [(row_adapter, "row_adapter", (torch.int32,), (rows,))])
+    _on(dev, [(hidden, "hidden", _bf16_types(), shape), (out, "out", _bf16_types(), shape),
+              (row_adapter, "row_adapter", (torch.int32,), (shape[0],)), (slot_idx, "slot_idx", (torch.int32,), None),
+              (ssm_pool, "ssm_pool", _bf16_types() + (torch.float32,), None), (conv_pool, "conv_pool", _bf16_types(), None),
+              (ws, "ws", (torch.uint8,), None)])
     ref = lambda lo: None if lo is None else C.byref(lo.struct)  # noqa: E731
     return ref(lora_in), ref(lora_out), None if row_adapter is None else row_adapter.data_ptr()
 
@@ -452,7 +457,9 @@ def mixer_decode_lora(params: MixerParams, lora_in, lora_out, row_adapter, hidde
     """mixer_decode with adapters beside in_proj and out_proj (Lora or None each); row_adapter int32 [batch].
     ws: uint8 device tensor of the decode_lora_ws_layout size (for the larger rank)."""
     dev = hidden.device
-    args = _mixer_lora(params, lora_in, lora_out, row_adapter, int(hidden.shape[0]), dev)
+    args = _mixer_lora(params, lora_in, lora_out, row_adapter, hidden, slot_idx, ssm_pool, conv_pool, out, ws)
+    if slot_idx.shape != (hidden.shape[0],):
+        raise ValueError(f"slot_idx of shape {tuple(slot_idx.shape)}: expected one slot per row")
     _call(dev, stream, lib.nhm_mixer_decode_lora, C.byref(params.struct), *args, hidden.data_ptr(), int(hidden.shape[0]),
           slot_idx.data_ptr(), ssm_pool.data_ptr(), _ssm_type(ssm_pool), conv_pool.data_ptr(), int(ssm_pool.shape[0]),
           out.data_ptr(), ws.data_ptr(), ws.numel())
@@ -464,7 +471,10 @@ def mixer_prefill_lora(params: MixerParams, lora_in, lora_out, row_adapter, hidd
     """mixer_prefill with adapters beside in_proj and out_proj (Lora or None each); row_adapter int32 [n_tokens]
     (BatchPlan.token_adapter). ws: uint8 device tensor of the prefill_lora_ws_layout size (for the larger rank)."""
     dev = hidden.device
-    args = _mixer_lora(params, lora_in, lora_out, row_adapter, int(hidden.shape[0]), dev)
+    args = _mixer_lora(params, lora_in, lora_out, row_adapter, hidden, slot_idx, ssm_pool, conv_pool, out, ws)
+    import torch
+    n = int(slot_idx.shape[0])
+    _on(dev, [(cu_seqlens, "cu_seqlens", (torch.int32,), (n + 1,)), (has_initial, "has_initial", (torch.int32,), (n,))])
     _call(dev, stream, lib.nhm_mixer_prefill_lora, C.byref(params.struct), *args, hidden.data_ptr(), int(hidden.shape[0]),
           cu_seqlens.data_ptr(), int(slot_idx.shape[0]), slot_idx.data_ptr(), has_initial.data_ptr(), chunk,
           ssm_pool.data_ptr(), _ssm_type(ssm_pool), conv_pool.data_ptr(), int(ssm_pool.shape[0]), out.data_ptr(),

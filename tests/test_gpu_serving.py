@@ -78,6 +78,12 @@ LORA_CASES = [
     (700, 10304, 336, 64, 3, "runs", True, False, False),
     (3000, 4100, 144, 48, 6, "runs", False, False, True),
     (3000, 4101, 144, 128, 200, "mixed", False, True, True),
+    (5, 70, 16400, 16, 4, "mixed", False, True, True),           # k past the GEMV's: a tile of five rows
+    (9, 130, 16448, 24, 9, "mixed", True, False, False),
+    (9000, 300, 272, 40, 7, "runs", False, False, True),         # many rows: their low-rank kernel
+    (8193, 77, 176, 128, 300, "mixed", True, True, True),
+    (8200, 260, 48, 8, 12, "mixed", False, False, True),
+    (15000, 64, 16, 64, 5, "runs", False, True, True),
 ]
 
 
@@ -145,6 +151,23 @@ def test_lora_rows_keep_to_their_adapter(nhm, m, n, k):
     keep = torch.from_numpy((ids != 3) & (np.arange(m) != 1)).cuda()
     assert torch.equal(got[keep], clean[keep])
     assert bool(torch.isnan(got.view(torch.bfloat16)[1].float()).any())
+
+
+@pytest.mark.parametrize("m,n,k", [(7, 2690, 4096), (61, 2688, 4096), (257, 10304, 272), (700, 10304, 336), (641, 1000, 1040)])
+def test_lora_per_tensor_weight_scale(nhm, m, n, k):
+    """One weight scale for the whole projection gives what the same value in every channel gives, bit for bit."""
+    from tests.gpu_util import dev
+    from workloads import linear_case
+    inp = list(lora_inputs(m, n, k, 16, 3, seed=31))
+    _, w, ws, _ = linear_case(m, n, k, extra=77, per_tensor=True)
+    inp[1], inp[2] = w, ws
+    x, W, L, ids = lora_device(nhm, inp)
+    W1 = nhm.Fp8Weight(dev(w), dev(ws[:1].copy()), dev(inp[3]))
+    assert W1.per_tensor
+    a = nhm.fp8_linear_lora(x, W, L, ids)
+    b = nhm.fp8_linear_lora(x, W1, L, ids)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
 
 
 def test_lora_strides_through_the_abi(nhm):
