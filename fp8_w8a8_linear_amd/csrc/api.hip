@@ -26,7 +26,7 @@ static const char* const kKernNames[(int)Kern::kCount] = {
     "quant_vec8", "quant_scalar", "dequant_channel", "gemv", "gemm_ring192x128", "gemm_ring192x128_exact",
     "gemm_ring256x128", "gemm_ring256x128_exact", "gemm_ring256x256", "gemm_ring256x256_exact", "gemm_panel64x128",
     "gemm_panel64x128_exact", "gemm_tile128", "gemm_tile128_exact", "gemm_splitk_reduce", "decode_ssm",
-    "gnorm_quant", "clear", "conv_fwd", "ssd_state", "ssd_pass", "ssd_out", "lora_down", "lora_up", "beam_rows",
+    "gnorm_quant", "clear", "conv_fwd", "ssd_state", "ssd_pass", "ssd_out", "lora_down", "lora_rows", "lora_rows_exact", "beam_rows",
     "beam_pick", "beam_reorder", "batch_plan"};
 static std::atomic<uint64_t> g_launches[(int)Kern::kCount];
 static std::atomic<uint64_t> g_rows[(int)Kern::kCount];

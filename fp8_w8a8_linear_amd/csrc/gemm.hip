@@ -51,7 +51,6 @@ struct GemmArgs {
     int ws_step = 1;    // weight scale index step: 1 per channel, 0 per tensor
     int panel_rows = 0; // panel kernel: weight rows per panel (0: all of its waves' rows)
     LoraEpi lora;       // the kernels with adapters only: kLora 1 (bf16 output, t in two parts) or 2 (f32, three)
-    const float* delta = nullptr;   // kLora 3: the adapters' part [m, lora_ld(n)], formed ahead of the GEMM
 };
 
 // Row r of a 128-byte-wide LDS tile holds its 16-byte chunk c at slot c ^ (r & 7):
@@ -338,7 +337,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     static_assert(WN % 16 == 0 && BM % 32 == 0, "tile shape");
     // the activation tiles, and after the k loop the adapters' operands (with adapters: room for B of
     // eight at a time, whose round trips would follow one another in a batch of many adapters)
-    constexpr int kLds = kLora == 1 || kLora == 2 ? 3 * BM * 128 + 8 * BN * 128 : 3 * BM * 128;
+    constexpr int kLds = kLora ? 3 * BM * 128 + 8 * BN * 128 : 3 * BM * 128;
     __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
     uint8_t (&sA)[3][BM * 128] = *reinterpret_cast<uint8_t (*)[3][BM * 128]>(smem);
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane >> 4, r16 = lane & 15;
@@ -354,7 +353,7 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
     const int64_t pend = min((int64_t)(pan + 1) * PW, g.n);
     const int64_t m0 = (int64_t)mt * BM, nw0 = (int64_t)pan * PW + wave * WN;
     LoraRows<BM> lrows;
-    if constexpr (kLora == 1 || kLora == 2) lrows.load(g.lora, m0, g.m, lane);
+    if constexpr (kLora != 0) lrows.load(g.lora, m0, g.m, lane);
     const int nk = (int)((g.k + 127) / 128);
     const int ns = (nk + U - 1) / U * U;   // steps, padded to the unroll (padding steps read zeros)
 
@@ -463,21 +462,10 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
         int id[TM];
 #pragma unroll
         for (int j = 0; j < TM; ++j) id[j] = lora_row(g.lora, m0 + j * 16 + r16, g.m);
-        if constexpr (kLora == 3) {     // rows without an adapter keep their sums' bits
-#pragma unroll
-            for (int j = 0; j < TM; ++j)
-#pragma unroll
-                for (int i = 0; i < TN; ++i) {
-                    const int64_t nb = nw0 + i * 16 + 4 * q, ld = lora_ld(g.n);
-                    if (id[j] < 0 || nb >= ld) continue;
-                    acc[i][j] += *reinterpret_cast<const v4f*>(g.delta + (m0 + j * 16 + r16) * ld + nb);
-                }
-        } else {
-            lora_tile<BN, BM, 256, kLds, true>(g.lora, lrows, m0, g.m, (int64_t)pan * PW, g.n, pend, smem, __builtin_amdgcn_readfirstlane(wave), lane,
-                                   [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
-                                       lora_mma16<BM, kLora + 1>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
-                                   });
-        }
+        lora_tile<BN, BM, 256, kLds, true>(g.lora, lrows, m0, g.m, (int64_t)pan * PW, g.n, pend, smem, __builtin_amdgcn_readfirstlane(wave), lane,
+                               [&](int cur, int c0, const uint8_t* tl, const uint8_t* bl) {
+                                   lora_mma16<BM, kLora + 1>(acc, g.lora, id, cur, c0, tl, bl, 0, wave * WN, lane);
+                               });
     }
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
@@ -487,10 +475,162 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
         for (int r = 0; r < 4; ++r) sc[r] = kLora ? 1.0f : sa * wsc[i][r];
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-            if (kLora == 1 || kLora == 2 ? kLora == 2 : g.out_f32 != nullptr)
+            if (kLora ? kLora == 2 : g.out_f32 != nullptr)
                 store_tile_f32(g.out_f32, g.ld_out, m0 + j * 16 + r16, nw0 + i * 16 + 4 * q, g.m, pend, acc[i][j], sc, full);
             else
                 store_tile(g.out, g.ld_out, m0 + j * 16 + r16, nw0 + i * 16 + 4 * q, g.m, pend, acc[i][j], sc, full);
+    }
+}
+
+// ---------------------------------------------------------------- decode batch with adapters
+//
+// Few rows with an adapter per row, at a weight too narrow for the wide tiles. The panel kernel's few
+// workgroups take the adapters one after another in their epilogues (61 rows, 32 adapters, 2,688 x 4,096: 0.65 us
+// each). Here a workgroup owns 64 rows and 16 TN features, so that there are enough of them to fill the chip, and
+// its waves have two trades: two multiply 32 rows each, straight from memory, and kLoraSide others form
+// t B_e^T at the same time, the adapters shared out among them. A lane of those keeps the product of its own
+// row's adapter only, so all but one of the side waves hold zeros for an output, and their sum, taken in LDS
+// in wave order, is exact. Bound by the operand bytes a CU is handed, TN 16 features once per multiplying
+// wave and the 64 rows: four multiplying waves of 16 rows 29.5 us with the low-rank product, two 27.3, one
+// of 64 rows 29.2, the panel kernel 51 (21 without adapters); four steps in flight, six took 31.2 for 29.5.
+constexpr int kLoraMain = 2, kLoraSide = 8;
+
+template <int TN, bool kExact, int P>     // P: t's parts
+__global__ __launch_bounds__((kLoraMain + kLoraSide) * 64) void lora_rows_kernel(const GemmArgs g) {
+    constexpr int TM = 4 / kLoraMain;         // row tiles of a multiplying wave
+    constexpr int D = TN == 1 ? 4 : 2;    // k-steps in flight per wave
+    __shared__ v4f s_sum[kLoraSide][TN][4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, r16 = lane & 15;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * TN), m0 = (int64_t)blockIdx.y * 64;
+    if (wave >= kLoraMain) {
+        const LoraEpi& e = g.lora;
+        const int id[1] = {lora_row(e, m0 + lane, g.m)};
+        int mine[4];                      // of this lane's row of each row tile
+        uint32_t toff[4];
+        const uint32_t tpart = (uint32_t)e.rp * 2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            mine[j] = __shfl(id[0], 16 * j + r16);
+            toff[j] = (uint32_t)(min(m0 + 16 * j + r16, g.m - 1) - m0) * P * tpart + 16 * q;
+        }
+        const char* const tb = reinterpret_cast<const char*>(e.t) + m0 * P * tpart;
+        const int steps = e.rp / 32;
+        v4f d[TN][4];
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        int turn = 0;
+        lora_each(id, [&](int cur) {
+            if (turn++ % kLoraSide != wave - kLoraMain) return;
+            const char* const bb = lora_b_base(e, cur, n0, g.n);
+            const uint64_t rows = __ballot(id[0] == cur);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (((rows >> (16 * j)) & 0xffffu) == 0) continue;
+                v4f x[TN];
+#pragma unroll
+                for (int i = 0; i < TN; ++i) x[i] = v4f{0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < steps; ++s) {
+                    bf16x8 bf[TN], tf[P];
+#pragma unroll
+                    for (int i = 0; i < TN; ++i)
+                        bf[i] = lora_load(bb, lora_b_off(e, 16 * i + r16, n0, g.n) + 16 * q + 64 * s, 32 * s + 8 * q < e.rank);
+#pragma unroll
+                    for (int p = 0; p < P; ++p) tf[p] = lora_load(tb, toff[j] + p * tpart + 64 * s, true);
+#pragma unroll
+                    for (int i = 0; i < TN; ++i)
+#pragma unroll
+                        for (int p = 0; p < P; ++p) x[i] = mfma_bf16(bf[i], tf[p], x[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) d[i][j][r] = mine[j] == cur ? x[i][r] : d[i][j][r];
+            }
+        });
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s_sum[wave - kLoraMain][i][j][lane] = d[i][j];
+        __syncthreads();
+        return;
+    }
+    const int64_t row0 = m0 + wave * (16 * TM);
+    const bool any = row0 < g.m;
+    v4f acc[TN][TM];
+    float wsc[TN][4];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t c = n0 + i * 16 + 4 * q + r;
+            wsc[i][r] = g.w_scale[(c < g.n ? c : g.n - 1) * g.ws_step];
+        }
+    }
+    const float sa = *g.a_scale;
+    if (any) {
+        const int nk = (int)((g.k + 127) / 128);
+        const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc((void*)g.w, (short)0, (int)(g.n * g.k), 0x00020000);
+        const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc((void*)g.a, (short)0, (int)(g.m * g.lda), 0x00020000);
+        uint32_t off[TN + TM];            // this lane's k bytes of a step, as the panel kernel's
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            const int64_t wrow = n0 + i * 16 + r16;
+            off[i] = wrow < g.n ? (uint32_t)(wrow * g.k + 16 * q) : kOutOfRange;
+        }
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const int64_t row = row0 + j * 16 + r16;
+            off[TN + j] = row < g.m ? (uint32_t)(row * g.lda + 16 * q) : kOutOfRange;
+        }
+        uint4 v[D][TN + TM][2];
+        auto fetch = [&](int s, uint4 (&dst)[TN + TM][2]) {
+            const int64_t kb = (int64_t)s * 128 + 16 * q;
+#pragma unroll
+            for (int i = 0; i < TN + TM; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    dst[i][h] = bload(i < TN ? wrs : ars, kb + 64 * h < g.k ? off[i] + (uint32_t)s * 128 + 64 * h : kOutOfRange);
+        };
+#pragma unroll
+        for (int s = 0; s < D; ++s) fetch(s, v[s]);
+        for (int k0 = 0; k0 < nk; k0 += D) {
+#pragma unroll
+            for (int u = 0; u < D; ++u) {   // steps past k add zeros
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+#pragma unroll
+                    for (int j = 0; j < TM; ++j)
+                        acc[i][j] = mfma16_step<kExact>(cat8(v[u][i][0], v[u][i][1]), cat8(v[u][TN + j][0], v[u][TN + j][1]), acc[i][j]);
+                fetch(k0 + u + D, v[u]);
+            }
+        }
+    }
+    __syncthreads();
+    if (!any) return;
+    const float one[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        const int64_t row = row0 + j * 16 + r16;
+        const bool mine = lora_row(g.lora, row, g.m) >= 0;   // other rows keep their sums' bits
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            v4f x = acc[i][j];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] *= sa * wsc[i][r];
+            v4f sum = s_sum[0][i][wave * TM + j][lane];
+#pragma unroll
+            for (int o = 1; o < kLoraSide; ++o) sum += s_sum[o][i][wave * TM + j][lane];
+            if (mine) x += sum;
+            const int64_t nb = n0 + i * 16 + 4 * q;
+            const bool full = g.vec_out && row0 + j * 16 + 16 <= g.m && n0 + 16 * (i + 1) <= g.n;
+            if constexpr (P == 3) store_tile_f32(g.out_f32, g.ld_out, row, nb, g.m, g.n, x, one, full);
+            else store_tile(g.out, g.ld_out, row, nb, g.m, g.n, x, one, full);
+        }
     }
 }
 
@@ -1268,23 +1408,47 @@ nhm_status launch_gemm(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* 
     return exact ? dispatch_gemm<true, 0>(g, st, part, part_bytes) : dispatch_gemm<false, 0>(g, st, part, part_bytes);
 }
 
+// The decode batch's kernel where the panel kernel would run, while its workgroups of 48 features are not
+// more than the CUs. Past that the CUs' operand bytes decide, and the panel kernel has fewer (32 adapters of rank
+// 32, this kernel against the panel's, us: 61 x 2,688 x 4,096 27 and 51, 61 x 10,304 x 2,688 31 and 45, 256 x
+// 2,688 x 4,096 43 and 53, but 64 x 20,000 x 1,024 37 and 35, 64 x 30,000 x 1,024 52 and 38, 100 x 10,304 x 2,688
+// 47 and 46; one adapter: 128 x 2,688 x 4,096 30 and 32, 640 x 512 x 512 12 and 14, but 256 x 2,688 x 4,096 30 and
+// 27, 64 x 20,000 x 1,024 24 and 18).
+static bool lora_rows_serve(const GemmArgs& g) {
+    constexpr int64_t k2G = int64_t(1) << 31;
+    const int64_t nmt = (g.m + 63) / 64;
+    return g.m <= 640 && (g.n + 191) / 192 * ((g.m + 127) / 128) < 160 && g.n * g.k < k2G && g.m * g.lda < k2G &&
+           (g.n + 47) / 48 * nmt <= 256;
+}
+
+// As many features per workgroup as keep the bytes on the busiest CU, (rounds of 256 workgroups) x (rows +
+// features), lowest.
+template <int P>
+static nhm_status launch_lora_rows(const GemmArgs& g, bool exact, hipStream_t st) {
+    const int64_t nmt = (g.m + 63) / 64, rows = min((g.m + 15) / 16 * 16, (int64_t)64);
+    auto cost = [&](int f) { return ((g.n + f - 1) / f * nmt + 255) / 256 * (rows + f); };
+    int tn = 1;
+    for (int t = 2; t <= 3; ++t)
+        if (cost(16 * t) < cost(16 * tn)) tn = t;
+    const dim3 grid((unsigned)((g.n + 16 * tn - 1) / (16 * tn)), (unsigned)nmt), block((kLoraMain + kLoraSide) * 64);
+    auto run = [&](auto kernel) { kernel<<<grid, block, 0, st>>>(g); };
+    if (exact) run(tn == 1 ? lora_rows_kernel<1, true, P> : tn == 2 ? lora_rows_kernel<2, true, P> : lora_rows_kernel<3, true, P>);
+    else run(tn == 1 ? lora_rows_kernel<1, false, P> : tn == 2 ? lora_rows_kernel<2, false, P> : lora_rows_kernel<3, false, P>);
+    count_launch(exact ? Kern::kLoraRowsExact : Kern::kLoraRows, g.m);
+    return check_launch("gemm (adapters' rows)");
+}
+
 nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* w, const float* w_scale,
                             const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
-                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora, float* delta) {
+                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora) {
     GemmArgs g{a, lda, m, w, w_scale, a_scale, n, k, out, ld_out,
                out_f32 ? ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out_f32) % 16 == 0
                        : ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0,
                out_f32};
     g.ws_step = ws_step;
     g.lora = lora;
-    if (lora_apart(m, n, k) && m * lda < (int64_t(1) << 31)) {
-        const nhm_status s = launch_lora_up(lora, m, n, delta, st);
-        if (s != NHM_OK) return s;
-        g.delta = delta;
-        if (exact) launch_panel<64, 32, true, 3>(g, st);
-        else launch_panel<64, 32, false, 3>(g, st);
-        return check_launch("gemm (panel, adapters)");
-    }
+    if (lora_rows_serve(g))
+        return lora.parts == 3 ? launch_lora_rows<3>(g, exact, st) : launch_lora_rows<2>(g, exact, st);
     if (out_f32) return exact ? dispatch_gemm<true, 2>(g, st, nullptr, 0) : dispatch_gemm<false, 2>(g, st, nullptr, 0);
     return exact ? dispatch_gemm<true, 1>(g, st, nullptr, 0) : dispatch_gemm<false, 1>(g, st, nullptr, 0);
 }

@@ -1,6 +1,6 @@
 // The low-rank product of many requests' adapters, t = scale x A_e^T (nhm_fp8_linear_lora), and in the
 // same pass over x the e4m3 codes the projection reads. The projection's own kernels add
-// t B_e^T in their epilogues (lora_device.h); for a decode batch in front of the tiled GEMM a kernel here forms it.
+// t B_e^T in their epilogues (lora_device.h).
 //
 // Matrix instructions with 16 ranks as the A operand and 16 rows of x as the B operand. Rows in a
 // tile may have any adapters: the tile is taken once per distinct adapter, and each time only its rows
@@ -16,7 +16,6 @@
 // consecutive values (two matrix instructions' worth; any deal of k to lanes will do that is the same for
 // both operands), so that the first of its two loads asks for whole 128-byte lines: with 32-wide steps
 // the halves of a line were fetched apart (15,360 rows from HBM: 62 us).
-#include "lora_device.h"
 #include "nhm_device.h"
 #include "nhm_internal.h"
 
@@ -296,82 +295,6 @@ nhm_status launch_lora_down(const LoraDownArgs& g, hipStream_t st) {
     else launch_down<uint8_t>(g, st);
     count_launch(Kern::kLoraDown, g.m);
     return check_launch("lora down");
-}
-
-// ---------------------------------------------------------------- the adapters' part of a decode batch
-//
-// A batch of up to 64 rows may have an adapter per row. In the epilogue of the tiled GEMM, whose few workgroups
-// own 64 to 128 features each, the adapters follow one another (61 rows, 32 adapters, rank 32, 2,688 x
-// 4,096: 51 us with its low-rank product, here 41, of them 6.8 this kernel); here a workgroup owns 16 features, and its waves share the adapters out, so the
-// whole chip reads B. A wave takes each of its adapters' 16 x rank values once, and t of the row tiles that have
-// rows of it; each lane keeps the sums of its own row only. The waves' sums meet in LDS, in wave order.
-
-// 16 waves; 8 for the widest ranks, whose operands need the registers of two
-constexpr int up_waves(int S) { return S == 4 ? 8 : 16; }
-
-template <int S, int P>     // rp / 32, t's parts
-__global__ __launch_bounds__(up_waves(S) * 64) void lora_up_kernel(const LoraEpi e, int64_t m, int64_t n, float* delta) {
-    constexpr int kUpWaves = up_waves(S);
-    __shared__ v4f s_sum[kUpWaves][4][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r16 = lane & 15, q8 = 8 * (lane >> 4);
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int id[1] = {lora_row(e, lane, m)};        // of row `lane`
-    int mine[4];                                     // of this lane's row of each tile
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mine[j] = __shfl(id[0], 16 * j + r16);
-    const char* const tb = reinterpret_cast<const char*>(e.t);
-    const uint32_t tpart = (uint32_t)e.rp * 2;
-    const uint32_t boff = lora_b_off(e, r16, n0, n) + q8 * 2;
-    v4f d[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = v4f{0.f, 0.f, 0.f, 0.f};
-    int turn = 0;
-    lora_each(id, [&](int cur) {
-        if (turn++ % kUpWaves != wave) return;
-        const char* const bb = lora_b_base(e, cur, n0, n);
-        const uint64_t rows = __ballot(id[0] == cur);
-        bf16x8 bf[S];
-#pragma unroll
-        for (int s = 0; s < S; ++s) bf[s] = lora_load(bb, boff + 64 * s, 32 * s + q8 < e.rank);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (((rows >> (16 * j)) & 0xffffu) == 0) continue;
-            const int row = 16 * j + r16;
-            const uint32_t toff = (uint32_t)(row < m ? row : (int)m - 1) * P * tpart + q8 * 2;
-            bf16x8 tf[P][S];
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int s = 0; s < S; ++s) tf[p][s] = lora_load(tb, toff + p * tpart + 64 * s, true);
-            v4f x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int s = 0; s < S; ++s) x = mfma_bf16(bf[s], tf[p][s], x);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) d[j][r] = mine[j] == cur ? x[r] : d[j][r];
-        }
-    });
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s_sum[wave][j][lane] = d[j];
-    __syncthreads();
-    if (wave >= 4) return;
-    v4f sum = s_sum[0][wave][lane];                  // wave j finishes row tile j
-#pragma unroll
-    for (int w = 1; w < kUpWaves; ++w) sum += s_sum[w][wave][lane];
-    const int row = 16 * wave + r16;
-    if (row < m) *reinterpret_cast<v4f*>(delta + row * lora_ld(n) + n0 + 4 * (lane >> 4)) = sum;
-}
-
-nhm_status launch_lora_up(const LoraEpi& e, int64_t m, int64_t n, float* delta, hipStream_t st) {
-    const dim3 grid((unsigned)((n + 15) / 16));
-    auto run = [&](int S, auto kernel) { kernel<<<grid, dim3(up_waves(S) * 64), 0, st>>>(e, m, n, delta); };
-    if (e.rp == 32) run(1, e.parts == 2 ? lora_up_kernel<1, 2> : lora_up_kernel<1, 3>);
-    else if (e.rp == 64) run(2, e.parts == 2 ? lora_up_kernel<2, 2> : lora_up_kernel<2, 3>);
-    else run(4, e.parts == 2 ? lora_up_kernel<4, 2> : lora_up_kernel<4, 3>);
-    count_launch(Kern::kLoraUp, m);
-    return check_launch("lora up");
 }
 
 }  // namespace nhm

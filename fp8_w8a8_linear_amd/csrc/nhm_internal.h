@@ -28,7 +28,7 @@ enum class Kern : int {
     kQuantVec8, kQuantScalar, kDequantChannel, kGemv, kRing192x128, kRing192x128Exact, kRing256x128,
     kRing256x128Exact, kRing256x256, kRing256x256Exact, kPanel64x128, kPanel64x128Exact, kTile128,
     kTile128Exact, kSplitkReduce, kDecodeSsm, kGnormQuant, kClear, kConvFwd, kSsdState, kSsdPass, kSsdOut,
-    kLoraDown, kLoraUp, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan, kCount
+    kLoraDown, kLoraRows, kLoraRowsExact, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan, kCount
 };
 void count_launch(Kern k, int64_t rows);
 
@@ -237,27 +237,14 @@ struct LoraDownArgs {
 };
 nhm_status launch_lora_down(const LoraDownArgs& g, hipStream_t st);
 
-// Past the GEMV and up to the 64 rows of one panel tile, where the weight is too narrow for 160 wider tiles
-// (the GEMM's own choice of its panel kernel): the adapters' part in f32 by a kernel of its own, delta[i, j] =
-// t B_e^T at i * lora_ld(n) + j (rows without an adapter hold what was there), for the panel kernel to add.
-constexpr int64_t lora_ld(int64_t n) { return (n + 15) / 16 * 16; }
-inline bool lora_apart(int64_t m, int64_t n, int64_t k) {
-    return m > 0 && m <= 64 && n > 0 && n <= 159 * 192 && k > 0 && k < (int64_t(1) << 31) / n && !use_gemv(m, n, k);
-}
-inline size_t lora_delta_bytes(int64_t m, int64_t n, int64_t k) {
-    return lora_apart(m, n, k) ? align_up((size_t)m * (size_t)lora_ld(n) * sizeof(float), 256) : 0;
-}
-nhm_status launch_lora_up(const LoraEpi& e, int64_t m, int64_t n, float* delta, hipStream_t st);
-
 // The projections with the adapters' part (the same kernels and choices as without, no split over k).
-// delta: lora_delta_bytes(m, n, k) of workspace.
 nhm_status launch_gemv_lora(const uint8_t* a, int64_t lda, int m, const uint8_t* w, const float* w_scale,
                             const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
                             float* out_f32, int ws_step, const LoraEpi& lora, uint32_t* clear = nullptr,
                             int clear_n = 0);
 nhm_status launch_gemm_lora(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* w, const float* w_scale,
                             const float* a_scale, int64_t n, int64_t k, uint16_t* out, int64_t ld_out, hipStream_t st,
-                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora, float* delta);
+                            float* out_f32, bool exact, int ws_step, const LoraEpi& lora);
 
 // ---- beam search (beam.hip)
 struct BeamArgs {

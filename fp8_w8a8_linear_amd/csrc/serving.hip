@@ -11,14 +11,12 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 
 bool rank_ok(int32_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
 
-// Regions of the adapter call's workspace: the activation codes of a bf16 input, the low-rank product,
-// the adapters' part in f32 where it is formed apart.
-struct LoraWs { size_t t, delta, total; };
-LoraWs lora_ws(int64_t m, int64_t n, int64_t k, nhm_dtype a_type, int32_t rank) {
+// Regions of the adapter call's workspace: the activation codes of a bf16 input, the low-rank product.
+struct LoraWs { size_t t, total; };
+LoraWs lora_ws(int64_t m, int64_t k, nhm_dtype a_type, int32_t rank) {
     LoraWs w{};
     w.t = align_up(linear_codes_ws(m, k, a_type), 256);
-    w.delta = w.t + align_up((size_t)m * 3 * lora_rp(rank) * sizeof(uint16_t), 256);
-    w.total = w.delta + lora_delta_bytes(m, n, k);
+    w.total = w.t + align_up((size_t)m * 3 * lora_rp(rank) * sizeof(uint16_t), 256);
     return w;
 }
 
@@ -34,13 +32,8 @@ nhm_status check_lora(const nhm_lora* l) {
 
 // ---- the mixer's projections with adapters
 
-// The adapters' workspace of m rows, bf16 outputs: the low-rank product, then the adapters' part in f32 of
-// the projection that needs more (in_proj [n1, k1], out_proj [n2, k2]).
+// The low-rank product's workspace of m rows, bf16 outputs.
 size_t mixer_t_bytes(int64_t m, int32_t rank) { return align_up((size_t)m * 2 * lora_rp(rank) * sizeof(uint16_t), 256); }
-size_t mixer_lora_bytes(int64_t m, int32_t rank, int64_t n1, int64_t k1, int64_t n2, int64_t k2) {
-    const size_t a = lora_delta_bytes(m, n1, k1), b = lora_delta_bytes(m, n2, k2);
-    return mixer_t_bytes(m, rank) + (a > b ? a : b);
-}
 
 LoraDownArgs down_args(const ProjectionHooks& h, const nhm_lora* l, const uint16_t* x, int64_t m, const nhm_fp8_weight& w,
                        uint8_t* q, char* ws) {
@@ -61,7 +54,7 @@ LoraDownArgs down_args(const ProjectionHooks& h, const nhm_lora* l, const uint16
 
 // One projection of m rows: up to 32 decode rows 16 at a time on the GEMV, as the mixer's own, else one call.
 nhm_status project_rows(const LoraDownArgs& d, const nhm_lora* l, const nhm_fp8_weight& w, const uint8_t* q, uint16_t* out,
-                        bool decode, bool exact, uint32_t* clear, int clear_n, char* ws, hipStream_t st) {
+                        bool decode, bool exact, uint32_t* clear, int clear_n, hipStream_t st) {
     const LoraEpi e{d.t, l->b, d.row_adapter, d.n_adapters, d.rank, d.rp, d.parts};
     const int64_t m = d.m;
     if (decode ? m <= 32 && use_gemv(16, w.n, w.k) : use_gemv(m, w.n, w.k)) {
@@ -77,8 +70,7 @@ nhm_status project_rows(const LoraDownArgs& d, const nhm_lora* l, const nhm_fp8_
         return NHM_OK;
     }
     if (clear && clear_n > 0) launch_clear(clear, clear_n, st);
-    return launch_gemm_lora(q, w.k, m, w.w, w.w_scale, w.a_scale, w.n, w.k, out, w.n, st, nullptr, exact, ws_step(w), e,
-                            reinterpret_cast<float*>(ws + mixer_t_bytes(m, l->rank)));
+    return launch_gemm_lora(q, w.k, m, w.w, w.w_scale, w.a_scale, w.n, w.k, out, w.n, st, nullptr, exact, ws_step(w), e);
 }
 
 nhm_status hook_in(const ProjectionHooks& h, const uint16_t* hidden, int64_t m, uint8_t* q, uint16_t* zx, uint32_t* clear,
@@ -86,14 +78,14 @@ nhm_status hook_in(const ProjectionHooks& h, const uint16_t* hidden, int64_t m, 
     const LoraDownArgs d = down_args(h, h.lora_in, hidden, m, h.p->in_proj, q, ws);
     const nhm_status s = launch_lora_down(d, st);
     // every product summed in f32, as the mixer's own in_proj
-    return s != NHM_OK ? s : project_rows(d, h.lora_in, h.p->in_proj, q, zx, h.decode, true, clear, clear_n, ws, st);
+    return s != NHM_OK ? s : project_rows(d, h.lora_in, h.p->in_proj, q, zx, h.decode, true, clear, clear_n, st);
 }
 
 nhm_status hook_out(const ProjectionHooks& h, const uint16_t* norm, const uint8_t* q, int64_t m, uint16_t* out, char* ws,
                     hipStream_t st) {
     const LoraDownArgs d = down_args(h, h.lora_out, norm, m, h.p->out_proj, nullptr, ws);
     const nhm_status s = launch_lora_down(d, st);
-    return s != NHM_OK ? s : project_rows(d, h.lora_out, h.p->out_proj, q, out, h.decode, false, nullptr, 0, ws, st);
+    return s != NHM_OK ? s : project_rows(d, h.lora_out, h.p->out_proj, q, out, h.decode, false, nullptr, 0, st);
 }
 
 // Checks the adapters of a mixer call and fills in its hooks (either set of adapters may be NULL).
@@ -111,7 +103,7 @@ nhm_status mixer_hooks(ProjectionHooks& h, const nhm_mixer_params* p, const nhm_
         if (s != NHM_OK) return s;
         if (n >= (int64_t(1) << 30) / l->rank)
             return fail(NHM_ERR_UNSUPPORTED, "lora: an adapter's b of 2 GiB or more");
-        const size_t t = mixer_lora_bytes(m, l->rank, p->in_proj.n, p->in_proj.k, p->out_proj.n, p->out_proj.k);
+        const size_t t = mixer_t_bytes(m, l->rank);
         h.extra = h.extra > t ? h.extra : t;
     }
     if ((in || out) && m > 0) {
@@ -139,7 +131,7 @@ extern "C" {
 
 size_t nhm_fp8_linear_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, nhm_dtype a_type, int32_t rank) {
     if (m <= 0 || n <= 0 || k <= 0 || !rank_ok(rank)) return 0;
-    return lora_ws(m, n, k, a_type, rank).total;
+    return lora_ws(m, k, a_type, rank).total;
 }
 
 nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64_t ld_a, const nhm_fp8_weight* w,
@@ -148,7 +140,7 @@ nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64
     clear_error();
     nhm_status s = check_lora(lora);
     if (s != NHM_OK) return s;
-    const size_t need = w && m > 0 && w->n > 0 && w->k > 0 ? lora_ws(m, w->n, w->k, a_type, lora->rank).total : 0;
+    const size_t need = w && m > 0 && w->n > 0 && w->k > 0 ? lora_ws(m, w->k, a_type, lora->rank).total : 0;
     s = linear_check(a, a_type, m, ld_a, w, out, out_type, ld_out, ws, ws_bytes, need);
     if (s != NHM_OK || m == 0) return s;
     if (m > INT_MAX) return fail(NHM_ERR_SHAPE, "m %lld out of range", (long long)m);
@@ -157,7 +149,7 @@ nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64
     if (w->n >= (int64_t(1) << 30) / lora->rank)       // 32-bit byte offsets within one adapter's B
         return fail(NHM_ERR_UNSUPPORTED, "lora: an adapter's b of 2 GiB or more");
     hipStream_t st = (hipStream_t)stream;
-    const LoraWs l = lora_ws(m, w->n, w->k, a_type, lora->rank);
+    const LoraWs l = lora_ws(m, w->k, a_type, lora->rank);
     char* wsb = static_cast<char*>(ws);
     const bool bf16 = a_type == NHM_BF16;
     const uint8_t* q = bf16 ? reinterpret_cast<uint8_t*>(wsb) : static_cast<const uint8_t*>(a);
@@ -182,16 +174,14 @@ nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t m, int64
     if (use_gemv(m, w->n, w->k))
         return launch_gemv_lora(q, ld_q, (int)m, w->w, w->w_scale, w->a_scale, w->n, w->k, ob, ld_out, st, of, ws_step(*w), epi);
     return launch_gemm_lora(q, ld_q, m, w->w, w->w_scale, w->a_scale, w->n, w->k, ob, ld_out, st, of, exact != 0, ws_step(*w),
-                            epi, reinterpret_cast<float*>(wsb + l.delta));
+                            epi);
 }
 
 nhm_status nhm_mixer_decode_lora_ws_layout(const nhm_geometry* g, int32_t batch, int32_t rank, nhm_ws_layout* out) {
     const nhm_status s = nhm_mixer_decode_ws_layout(g, batch, out);
     if (s != NHM_OK) return s;
     if (!rank_ok(rank)) return fail(NHM_ERR_UNSUPPORTED, "lora: rank %d: a multiple of 8 in 8 .. 128", rank);
-    nhm_layout l;
-    fill_layout(g, &l);
-    out->total += mixer_lora_bytes(batch, rank, l.d_in_proj, g->hidden, g->hidden, l.d_inner);
+    out->total += mixer_t_bytes(batch, rank);
     return NHM_OK;
 }
 
@@ -200,9 +190,7 @@ nhm_status nhm_mixer_prefill_lora_ws_layout(const nhm_geometry* g, int64_t n_tok
     const nhm_status s = nhm_mixer_prefill_ws_layout(g, n_tokens, n_seqs, chunk, out);
     if (s != NHM_OK) return s;
     if (!rank_ok(rank)) return fail(NHM_ERR_UNSUPPORTED, "lora: rank %d: a multiple of 8 in 8 .. 128", rank);
-    nhm_layout l;
-    fill_layout(g, &l);
-    out->total += mixer_lora_bytes(n_tokens, rank, l.d_in_proj, g->hidden, g->hidden, l.d_inner);
+    out->total += mixer_t_bytes(n_tokens, rank);
     return NHM_OK;
 }
 

@@ -41,7 +41,7 @@ nhm_status launch_gemv_lora(const uint8_t*, int64_t, int, const uint8_t*, const 
     reached("launch_gemv_lora");
 }
 nhm_status launch_gemm_lora(const uint8_t*, int64_t, int64_t, const uint8_t*, const float*, const float*, int64_t, int64_t,
-                            uint16_t*, int64_t, hipStream_t, float*, bool, int, const LoraEpi&, float*) {
+                            uint16_t*, int64_t, hipStream_t, float*, bool, int, const LoraEpi&) {
     reached("launch_gemm_lora");
 }
 size_t beam_ws_bytes(int64_t rows, int64_t, int32_t) { return (size_t)rows * 16; }

@@ -84,6 +84,12 @@ LORA_CASES = [
     (8193, 77, 176, 128, 300, "mixed", True, True, True),
     (8200, 260, 48, 8, 12, "mixed", False, False, True),
     (15000, 64, 16, 64, 5, "runs", False, True, True),
+    (50, 8001, 272, 40, 20, "mixed", False, False, False),       # 32 and 48 features to a workgroup, rows past 64
+    (64, 10304, 336, 128, 70, "mixed", True, True, True),
+    (45, 10300, 144, 64, 3, "mixed", False, False, True),
+    (199, 2690, 1040, 16, 90, "mixed", True, False, False),
+    (640, 513, 528, 32, 300, "mixed", False, True, True),
+    (64, 20000, 272, 48, 30, "mixed", False, False, False),      # past it: the panel kernel
 ]
 
 
@@ -109,7 +115,9 @@ def test_lora_linear(nhm, m, n, k, rank, adapters, order, codes, f32, exact):
                                              (61, 2688, 4096, True, False), (61, 2688, 4096, False, False),
                                              (257, 10304, 2688, True, False), (257, 10304, 2688, False, True),
                                              (700, 10304, 336, True, False), (700, 10304, 336, False, False),
-                                             (641, 1000, 1040, False, True)])
+                                             (641, 1000, 1040, False, True), (50, 10304, 336, True, False),
+                                             (64, 8001, 528, False, True), (300, 2690, 272, False, False),
+                                             (64, 20000, 272, False, False)])
 def test_lora_rows_without_adapter(nhm, m, n, k, exact, f32):
     """Rows without an adapter (negative or past the set) hold the projection alone, bit for bit, whatever rows with
     one share their tiles."""
@@ -131,7 +139,8 @@ def test_lora_rows_without_adapter(nhm, m, n, k, exact, f32):
 
 
 @pytest.mark.parametrize("m,n,k", [(8, 2688, 4096), (61, 2688, 4096), (257, 10304, 272), (700, 10304, 336),
-                                   (641, 1000, 1040)])
+                                   (641, 1000, 1040), (50, 10304, 336), (64, 8001, 528), (300, 2690, 272),
+                                   (64, 20000, 272)])
 def test_lora_rows_keep_to_their_adapter(nhm, m, n, k):
     """NaN and infinities in other adapters, and in other rows, do not reach a row."""
     inp = list(lora_inputs(m, n, k, 24, 4, seed=9, bare=0.2))
@@ -153,7 +162,7 @@ def test_lora_rows_keep_to_their_adapter(nhm, m, n, k):
     assert bool(torch.isnan(got.view(torch.bfloat16)[1].float()).any())
 
 
-@pytest.mark.parametrize("m,n,k", [(7, 2690, 4096), (61, 2688, 4096), (257, 10304, 272), (700, 10304, 336), (641, 1000, 1040)])
+@pytest.mark.parametrize("m,n,k", [(7, 2690, 4096), (61, 2688, 4096), (60, 9999, 272), (64, 20000, 528), (257, 10304, 272), (700, 10304, 336), (641, 1000, 1040)])
 def test_lora_per_tensor_weight_scale(nhm, m, n, k):
     """One weight scale for the whole projection gives what the same value in every channel gives, bit for bit."""
     from tests.gpu_util import dev
