@@ -6,9 +6,9 @@
 // tile may have any adapters: the tile is taken once per distinct adapter, and each time only its rows
 // are stored, so another adapter's values reach nobody else. What it must read is x and the used
 // adapters' A, and with a bf16 x it writes the codes.
-//  * Few rows: latency bounds it. A workgroup owns 16 rows and 16 ranks over all of k, 16 waves
-//    that take the 32-wide k-steps round robin with all their loads in flight (up to k = 4,096 one round), and
-//    a share of the tile's distinct adapters.
+//  * Few rows: latency and the bytes a CU is handed bound it. A workgroup owns 16 rows and 4 to 16 ranks over all of
+//    k, 16 waves that take the 64-wide k-steps round robin with all their loads in flight (up to k = 4,096 one
+//    round), and a share of the tile's distinct adapters, of whose rows alone it reads x.
 //  * Many rows (8,192 or more fill half of the chip): x's bytes bound it. A workgroup owns 64 rows and up to 64 ranks,
 //    4 waves that each take whole 64 x 64 k-steps, so that x and A enter the CU once, the next
 //    step's operands on their way while one is multiplied.
@@ -67,7 +67,7 @@ constexpr int kFewWaves = 16, kFewSteps = 4;   // k-steps of a wave whose loads 
 // thread (in the same workgroups as the products they made the code long and the launch slow: 9.2 us
 // for 8 rows).
 template <typename X>
-__global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const LoraDownArgs g, int shares) {
+__global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const LoraDownArgs g, int shares, int ranks) {
     __shared__ v4f s_part[kFewWaves][64];
     const int64_t tile0 = (int64_t)blockIdx.x * 16;
     if constexpr (sizeof(X) == 2) {
@@ -92,8 +92,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
     int id = g.row_adapter[src];
     const X* const xr = x_rows<X>(g) + src * g.ld_x;
     const int steps = (int)((g.k + 63) / 64);
-    const int r = blockIdx.y * 16 + r16;                         // this lane's rank of A
-    const int64_t arow = r < g.rank ? r : g.rank - 1;
+    const int r = blockIdx.y * ranks + r16;                      // this lane's rank of A
+    const bool on = r16 < ranks && r < g.rank;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
     if (row >= g.m || id >= g.n_adapters) id = -1;
     uint64_t todo = __ballot(id >= 0) & 0xffffu;
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
         const float s = *reinterpret_cast<scalar_f32>(reinterpret_cast<uintptr_t>(g.a_scale));
         const float se = *reinterpret_cast<scalar_f32>(reinterpret_cast<uintptr_t>(g.scale ? g.scale + cur : g.a_scale));
         v4f acc = {0.f, 0.f, 0.f, 0.f};
-        const uint16_t* const ar = g.a + ((int64_t)cur * g.rank + arow) * g.k;
+        const uint16_t* const ar = g.a + ((int64_t)cur * g.rank + r) * g.k;
         for (int s0 = wave; s0 < steps; s0 += kFewWaves * kFewSteps) {
             bf16x8 xv[kFewSteps][2], av[kFewSteps][2];
 #pragma unroll
@@ -114,12 +114,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
                 const int kk = (s0 + u * kFewWaves) * 64 + q16;      // 16 divides k: all of a lane's 16 or none
 #pragma unroll
                 for (int h = 0; h < 2; ++h) xv[u][h] = av[u][h] = zero;
-                if (kk < g.k) {
+                if (kk < g.k && on) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        av[u][h] = x8(ar + kk + 8 * h);
-                        xv[u][h] = x8(xr + kk + 8 * h);
-                    }
+                    for (int h = 0; h < 2; ++h) av[u][h] = x8(ar + kk + 8 * h);
+                }
+                if (kk < g.k && id == cur) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) xv[u][h] = x8(xr + kk + 8 * h);
                 }
             }
 #pragma unroll
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_down_few_kernel(const Lor
 #pragma unroll
             for (int w = 1; w < kFewWaves; ++w) d += s_part[w][lane];
             const float sc = (g.scale ? se : 1.0f) * (sizeof(X) == 1 ? s : 1.0f);
-            if (id == cur) store_parts(g, row, blockIdx.y * 16 + 4 * (lane >> 4), d, sc);
+            const int r0 = 4 * (lane >> 4);
+            if (id == cur && r0 < ranks) store_parts(g, row, blockIdx.y * ranks + r0, d, sc);
         }
         __syncthreads();
     }
@@ -280,14 +282,17 @@ static void launch_down(const LoraDownArgs& g, hipStream_t st) {
         else lora_down_many_kernel<X, 4><<<grid, dim3(kManyWaves * 64), 0, st>>>(g);
         return;
     }
-    const unsigned groups = (unsigned)(g.rp / 16);
+    // Fewer ranks per workgroup while there are CUs for them (up to an adapter per row): 16, 8 and 4 ranks, us with
+    // the projection: 8 rows of rank 64 17.0, 16.3, 15.9, 61 rows of rank 32 26.2, 25.0, 28.6.
+    const int ranks = g.m * (g.rp / 4) <= 256 ? 4 : g.m * (g.rp / 8) <= 512 ? 8 : 16;
+    const unsigned groups = (unsigned)(g.rp / ranks);
     int64_t z = 1024 / (tiles * groups);
     z = z < 1 ? 1 : z > 16 ? 16 : z;
     // a vector of eight codes per thread, up to as many workgroups again
     const int64_t vecs = sizeof(X) == 2 && g.q ? (g.k / 8 * 16 + kFewWaves * 64 - 1) / (kFewWaves * 64) : 0;
     int64_t extra = (vecs + groups - 1) / groups;
     extra = extra > z ? z : extra;
-    lora_down_few_kernel<X><<<dim3((unsigned)tiles, groups, (unsigned)(z + extra)), dim3(kFewWaves * 64), 0, st>>>(g, (int)z);
+    lora_down_few_kernel<X><<<dim3((unsigned)tiles, groups, (unsigned)(z + extra)), dim3(kFewWaves * 64), 0, st>>>(g, (int)z, ranks);
 }
 
 nhm_status launch_lora_down(const LoraDownArgs& g, hipStream_t st) {
