@@ -329,31 +329,34 @@ def mixer_prefill(params: MixerParams, hidden, cu_seqlens, slot_idx, has_initial
 def _on(dev, shapes):
     """Checks (tensor, name, dtypes, shape) entries: contiguous, on `dev`, of one of the dtypes and of the shape
     (None: not checked). Optional tensors may be None."""
+    import torch
     index = dev.index
     for t, name, dtypes, shape in shapes:
-        if t is None:
+        if t is None or (isinstance(t, torch.Tensor) and t.get_device() == index and t.is_contiguous()
+                         and t.dtype in dtypes and (shape is None or t.shape == shape)):
             continue
         _dev_tensor(t, name)
         if t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
         if t.dtype not in dtypes:
             raise TypeError(f"{name} of dtype {t.dtype}: expected {' or '.join(str(d) for d in dtypes)}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} of shape {tuple(t.shape)}: expected {shape}")
+        raise ValueError(f"{name} of shape {tuple(t.shape)}: expected {shape}")
 
 
 def _call(dev, stream, fn, *args):
     """One library call on `stream` (default: the current stream of `dev`) with `dev` current."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)     # torch.cuda.current_stream(dev) builds an object: 1.8 us
     elif stream.device != dev:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, stream.cuda_stream))
+        _check(fn(*args, handle))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream.cuda_stream))
+            _check(fn(*args, handle))
 
 
 def _bf16_types():
@@ -531,8 +534,9 @@ def beam_reorder(parents, slots, ssm_pools, conv_pools, new_slots=None, g=GEOMET
     conv_dim = geom.n_heads * geom.head_dim + 2 * geom.n_groups * geom.d_state
     st = _ssm_type(ssm_pools[0])
     row, win = geom.n_heads * geom.head_dim * geom.d_state, (geom.conv_width - 1) * conv_dim
+    st_types, bf16 = (ssm_pools[0].dtype,), _bf16_types()
     for i, (sp, cp) in enumerate(zip(ssm_pools, conv_pools)):
-        _on(dev, [(sp, f"ssm_pools[{i}]", (ssm_pools[0].dtype,), None), (cp, f"conv_pools[{i}]", _bf16_types(), None)])
+        _on(dev, ((sp, "an SSM pool", st_types, None), (cp, "a conv pool", bf16, None)))
         if sp.shape[0] != S or sp.numel() != S * row or cp.numel() != S * win:
             raise ValueError(f"layer {i}: pools of shapes {tuple(sp.shape)} and {tuple(cp.shape)} do not hold {S} rows")
     i32, shape = (torch.int32,), tuple(parents.shape)
