@@ -48,7 +48,7 @@ struct GemvArgs {
     LoraEpi lora;      // the kernels with adapters only
 };
 
-// The adapters' part of the workgroup's kTiles row tiles, split over the waves: wave w takes the
+// The adapters' part of the workgroup's kTiles row tiles, split over kWaves waves: wave w takes the
 // w-th, (w + kWaves)-th, ... distinct adapter among the tokens. d[t] register r of lane l is
 // feature n0 + 16 t + 4 (l / 16) + r of token l % 16; lanes of other tokens stay as they are.
 template <int S, int kWaves, int kTiles>
@@ -86,24 +86,51 @@ __device__ __forceinline__ void gemv_lora(v4f (&d)[kTiles], const GemvArgs& g, i
     });
 }
 
+// Wave `wave` of kWaves: its sums, to LDS.
+template <int kWaves, int kTiles>
+__device__ __forceinline__ void gemv_lora_part(v4f (*part)[64], const GemvArgs& g, int64_t n0, int wave, int lane) {
+    v4f d[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (g.lora.rp == 32) gemv_lora<1, kWaves, kTiles>(d, g, n0, wave, lane);
+    else if (g.lora.rp == 64) gemv_lora<2, kWaves, kTiles>(d, g, n0, wave, lane);
+    else gemv_lora<4, kWaves, kTiles>(d, g, n0, wave, lane);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) part[t][lane] = d[t];
+}
+
 // Cache policy of the weight stream: the default. The non-temporal hint (nt) made the in_proj
 // GEMV at m = 8 slower, 9.24 against 8.37 us per launch (sc0 alone 8.39, sc1 9.76, nt with
 // either 9.23), although each weight row is read once per call.
 constexpr int kStreamAux = 0;
 
+// Waves beside the kWaves that stream the weight, for the adapters' part, formed while the weight arrives (by the
+// streaming waves afterwards: 8.0 us for one row of rank 16 and 10.8 for 8 rows with an adapter each of rank 64,
+// 10,304 x 2,688; beside them 6.9 and 10.2, and 7.7 with no adapter). Beside 16 waves there is no room; those do it
+// afterwards.
+constexpr int gemv_side(bool lora, int waves) { return lora && waves < 16 ? 4 : 0; }
+
 template <int kWaves, int kSteps, int kTiles, bool kLines, bool kLora>
-__global__ __launch_bounds__(kWaves * 64) void gemv_kernel(const GemvArgs g) {
+__global__ __launch_bounds__((kWaves + gemv_side(kLora, kWaves)) * 64) void gemv_kernel(const GemvArgs g) {
+    constexpr int kSide = gemv_side(kLora, kWaves), kParts = kSide ? kSide : kWaves;
     __shared__ v4f s_red[kWaves][kTiles][64];   // every wave's partial of every row tile
-    __shared__ v4f s_lora[kLora ? kWaves : 1][kLora ? kTiles : 1][kLora ? 64 : 1];   // and of the adapters' part
+    __shared__ v4f s_lora[kLora ? kParts : 1][kLora ? kTiles : 1][kLora ? 64 : 1];   // and of the adapters' part
     // kLines: this wave's transpose buffer, one k-step of the 16 kTiles rows
     __shared__ __attribute__((aligned(16))) uint8_t s_tr[kLines ? kWaves : 1][kLines ? 16 * kTiles * 128 : 16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = kSide ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : threadIdx.x >> 6;
     const int b = blockIdx.x;
     if (b == 0 && g.clear) {
-        for (int i = threadIdx.x; i < g.clear_n; i += kWaves * 64) g.clear[i] = 0u;
+        for (int i = threadIdx.x; i < g.clear_n; i += (kWaves + kSide) * 64) g.clear[i] = 0u;
     }
     const int64_t n0 = (int64_t)b * g.base + (b < g.extra ? b : g.extra);
     const int64_t nend = n0 + g.base + (b < g.extra ? 1 : 0);   // this workgroup's features end
+    if constexpr (kSide != 0) {
+        if (wave >= kWaves) {
+            gemv_lora_part<kSide, kTiles>(s_lora[wave - kWaves], g, n0, wave - kWaves, lane);
+            __syncthreads();
+            return;
+        }
+    }
     const int col = lane & 15;                  // B operand column (token)
     const int kq = (lane >> 4) * 32;
     // MFMA row tile t covers features n0 + 16 t .. + 15 (A operand row lane % 16; rows at or
@@ -210,16 +237,7 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_kernel(const GemvArgs g) {
     // (deterministic) and stores it, so the row tiles' epilogues run side by side.
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) s_red[wave][t][lane] = acc[t];
-    if constexpr (kLora) {
-        v4f dl[kTiles];
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) dl[t] = v4f{0.f, 0.f, 0.f, 0.f};
-        if (g.lora.rp == 32) gemv_lora<1, kWaves, kTiles>(dl, g, n0, wave, lane);
-        else if (g.lora.rp == 64) gemv_lora<2, kWaves, kTiles>(dl, g, n0, wave, lane);
-        else gemv_lora<4, kWaves, kTiles>(dl, g, n0, wave, lane);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) s_lora[wave][t][lane] = dl[t];
-    }
+    if constexpr (kLora && kSide == 0) gemv_lora_part<kWaves, kTiles>(s_lora[wave], g, n0, wave, lane);
     __syncthreads();
     if (wave >= kTiles) return;
     v4f d = s_red[0][wave][lane];
@@ -234,7 +252,7 @@ __global__ __launch_bounds__(kWaves * 64) void gemv_kernel(const GemvArgs g) {
     if constexpr (kLora) {   // the scaled projection plus the adapters' part (rows without one add nothing)
         v4f a = s_lora[0][wave][lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) a += s_lora[w][wave][lane];
+        for (int w = 1; w < kParts; ++w) a += s_lora[w][wave][lane];
         const bool has = lora_row(g.lora, col, g.m) >= 0;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -307,13 +325,13 @@ static nhm_status dispatch_gemv(GemvArgs g, hipStream_t st) {
     g.extra = (int)(n % wgs);
     const int tiles = (g.base + (g.extra ? 1 : 0) + 15) / 16;
     const dim3 grid((unsigned)wgs);
-#define NHM_GEMV_LAUNCH(W, S, T) gemv_kernel<W, S, T, (W == 8), kLora><<<grid, dim3(W * 64), 0, st>>>(g)
+#define NHM_GEMV_LAUNCH(W, S, T) gemv_kernel<W, S, T, (W == 8), kLora><<<grid, dim3((W + gemv_side(kLora, W)) * 64), 0, st>>>(g)
 #define NHM_GEMV_STEPS(W, T)                         \
     do {                                             \
         if (steps == 2) NHM_GEMV_LAUNCH(W, 2, T);    \
         else if (steps == 4) NHM_GEMV_LAUNCH(W, 4, T); \
         else if (steps == 6) NHM_GEMV_LAUNCH(W, 6, T); \
-        else NHM_GEMV_LAUNCH(W, 8, T);               \
+        else if constexpr (W != 4) NHM_GEMV_LAUNCH(W, 8, T); /* 4 waves: 6 steps at most */ \
     } while (0)
     if (waves == 4) {
         if (tiles == 1) NHM_GEMV_STEPS(4, 1);
