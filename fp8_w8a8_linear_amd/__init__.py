@@ -438,10 +438,20 @@ def prefill_lora_ws_layout(n_tokens, n_seqs, rank, chunk=128, g=GEOMETRY):
     return {n: int(getattr(out, n)) for n, _ in WsLayout._fields_}
 
 
+def _pool_rows(geom, ssm_pool, conv_pool, what):
+    """The rows (slots) of a layer's pools, which must hold equally many of the geometry's states and windows."""
+    rows = int(ssm_pool.shape[0])
+    row = geom.n_heads * geom.head_dim * geom.d_state
+    win = (geom.conv_width - 1) * (geom.n_heads * geom.head_dim + 2 * geom.n_groups * geom.d_state)
+    if ssm_pool.numel() != rows * row or conv_pool.numel() != rows * win:
+        raise ValueError(f"{what}: pools of shapes {tuple(ssm_pool.shape)} and {tuple(conv_pool.shape)} do not hold {rows} rows")
+    return rows
+
+
 def _mixer_lora(params, lora_in, lora_out, row_adapter, hidden, slot_idx, ssm_pool, conv_pool, out, ws):
     """Checks a mixer call with adapters; the C arguments of the two sets and the row map."""
     import torch
-    dev, shape = hidden.device, (hidden.shape[0], params.geometry["hidden"])
+    dev, shape = _dev_tensor(hidden, "hidden").device, (hidden.shape[0], params.geometry["hidden"])
     for lo, w, name in ((lora_in, params.in_proj, "lora_in"), (lora_out, params.out_proj, "lora_out")):
         if lo is not None and (lo.n, lo.k) != (w.n, w.k):
             raise ValueError(f"{name} is for a [{lo.n}, {lo.k}] projection, the block's is [{w.n}, {w.k}]")
@@ -451,6 +461,7 @@ def _mixer_lora(params, lora_in, lora_out, row_adapter, hidden, slot_idx, ssm_po
               (row_adapter, "row_adapter", (torch.int32,), (shape[0],)), (slot_idx, "slot_idx", (torch.int32,), None),
               (ssm_pool, "ssm_pool", _bf16_types() + (torch.float32,), None), (conv_pool, "conv_pool", _bf16_types(), None),
               (ws, "ws", (torch.uint8,), None)])
+    _pool_rows(_geom(params.geometry), ssm_pool, conv_pool, "the mixer")
     ref = lambda lo: None if lo is None else C.byref(lo.struct)  # noqa: E731
     return ref(lora_in), ref(lora_out), None if row_adapter is None else row_adapter.data_ptr()
 
@@ -530,15 +541,13 @@ def beam_reorder(parents, slots, ssm_pools, conv_pools, new_slots=None, g=GEOMET
     if parents.dim() != 2:
         raise ValueError(f"parents of shape {tuple(parents.shape)}: expected [groups, beams]")
     geom = _geom(g)
-    S = int(ssm_pools[0].shape[0])
-    conv_dim = geom.n_heads * geom.head_dim + 2 * geom.n_groups * geom.d_state
     st = _ssm_type(ssm_pools[0])
-    row, win = geom.n_heads * geom.head_dim * geom.d_state, (geom.conv_width - 1) * conv_dim
     st_types, bf16 = (ssm_pools[0].dtype,), _bf16_types()
+    S = int(ssm_pools[0].shape[0])
     for i, (sp, cp) in enumerate(zip(ssm_pools, conv_pools)):
         _on(dev, ((sp, "an SSM pool", st_types, None), (cp, "a conv pool", bf16, None)))
-        if sp.shape[0] != S or sp.numel() != S * row or cp.numel() != S * win:
-            raise ValueError(f"layer {i}: pools of shapes {tuple(sp.shape)} and {tuple(cp.shape)} do not hold {S} rows")
+        if _pool_rows(geom, sp, cp, "a layer") != S:
+            raise ValueError(f"layer {i}: pools of {int(sp.shape[0])} rows, the first layer's hold {S}")
     i32, shape = (torch.int32,), tuple(parents.shape)
     _on(dev, [(parents, "parents", i32, None), (slots, "slots", i32, shape), (new_slots, "new_slots", i32, shape)])
     if new_slots is None:

@@ -92,6 +92,8 @@ NHM_API size_t nhm_beam_select_workspace_bytes(int64_t n_groups, int32_t n_beams
  * ordered by score, highest first, equal scores by beam and then token, lowest first. Scores are
  * formed and compared in f64 (the sum of the exponentials from f32 terms) and returned in f32.
  * A NaN logit counts as -inf; where a row holds +inf, its +inf entries share the probability.
+ * Of one beam's continuations whose logits differ too little for their f64 scores to differ, those
+ * of the larger logits are kept.
  * Continuations whose score is -inf or NaN are none: places they would take get score -inf,
  * parent -1 and token -1.
  *   logits    (device) [n_groups * n_beams, ld] of type NHM_BF16 or NHM_F32, ld >= vocab

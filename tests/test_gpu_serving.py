@@ -498,3 +498,55 @@ def test_batch_plan_saturates(nhm):
     assert st == 0
     torch.cuda.synchronize()
     assert int(cu[1]) == 2 ** 31 - 1 and int(cu[4000]) == 2 ** 31 - 1 and int(has[:4000].sum()) == 0
+
+
+# ---------------------------------------------------------------- the binding's refusals
+
+
+def refused(error, f, *a, **kw):
+    with pytest.raises(error):
+        f(*a, **kw)
+
+
+def test_binding_refuses_other_tensors(nhm):
+    """Wrong shapes, types, orders and devices are errors ahead of any launch, and leave the outputs as they were."""
+    x, W, L, ids = lora_device(nhm, lora_inputs(5, 64, 48, 8, 2, seed=1))
+    out = torch.full((5, 64), 7, dtype=torch.int16, device="cuda")
+    call = nhm.fp8_linear_lora
+    refused(TypeError, call, x.cpu(), W, L, ids)
+    refused(TypeError, call, x, W, L, ids.long(), out=out)
+    refused(TypeError, call, x, W, L, ids.cpu(), out=out)
+    refused(ValueError, call, x, W, L, ids[:4], out=out)
+    refused(ValueError, call, x[:, :32].contiguous(), W, L, ids, out=out)
+    refused(ValueError, call, x, W, L, ids, out=out[:, :32])
+    refused(ValueError, call, x, W, L, ids, out=out.t().contiguous().t())
+    refused(TypeError, call, x, W, L, ids, out=out, out_type=nhm.NHM_F32)
+    refused(nhm.NhmError, call, x, W, L, ids, out=out, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    refused(ValueError, nhm.Lora, L.a, L.b[:1], None)
+    refused(ValueError, nhm.Lora, L.a, L.b, torch.ones(3, device="cuda"))
+    refused(ValueError, call, x, W, nhm.Lora(L.a, L.b[:, :32].contiguous()), ids)
+
+    logits, cum = torch.zeros((6, 100), device="cuda"), torch.zeros((2, 3), device="cuda")
+    refused(ValueError, nhm.beam_select, logits, cum[0], 4)
+    refused(ValueError, nhm.beam_select, logits[:5], cum, 4)
+    refused(TypeError, nhm.beam_select, logits.double(), cum, 4)
+    refused(ValueError, nhm.beam_select, logits, cum, 4, scores=torch.zeros((2, 3), device="cuda"))
+    refused(nhm.NhmError, nhm.beam_select, logits, cum, 65)
+    refused(nhm.NhmError, nhm.beam_select, logits, cum, 4, finished=torch.zeros((2, 3), dtype=torch.int32, device="cuda"), eos=100)
+
+    g = dict(hidden=256, n_heads=8, head_dim=64, d_state=128, n_groups=2, conv_width=4, rms_eps=1e-5)
+    ssm = torch.zeros((6, 8, 64, 128), device="cuda")
+    conv = torch.zeros((6, 3, 8 * 64 + 2 * 2 * 128), dtype=torch.int16, device="cuda")
+    par = torch.zeros((2, 3), dtype=torch.int32, device="cuda")
+    slots = torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3)
+    refused(ValueError, nhm.beam_reorder, par, slots, [ssm], [conv[:5]], g=g)
+    refused(ValueError, nhm.beam_reorder, par, slots, [ssm, ssm[:5]], [conv, conv[:5]], g=g)
+    refused(ValueError, nhm.beam_reorder, par, slots, [ssm], [], g=g)
+    refused(TypeError, nhm.beam_reorder, par, slots, [ssm, ssm.to(torch.bfloat16)], [conv, conv], g=g)
+    refused(nhm.NhmError, nhm.beam_reorder, par, slots, [ssm], [conv], new_slots=slots, g=g)
+
+    n = torch.ones(4, dtype=torch.int32, device="cuda")
+    refused(ValueError, nhm.batch_plan, n, nhm.BatchPlan(5, 8))
+    refused(TypeError, nhm.batch_plan, n.long(), nhm.BatchPlan(4, 8))
+    torch.cuda.synchronize()
+    assert bool((out == 7).all()) and bool((ssm == 0).all())

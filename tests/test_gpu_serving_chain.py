@@ -264,3 +264,27 @@ def test_requests_from_plan_to_beams(nhm):
                     assert rel_l2(ly["spd"][int(ns[i, j])].cpu().numpy(), sr) <= 5e-3, (step, i, j)
             new_beams.append(row)
         beams, slots, slots_d, cum, rows = new_beams, ns, new_slots, scores, x
+
+
+def test_mixer_binding_refuses_other_tensors(nhm):
+    """The mixer calls with adapters check their tensors ahead of any launch."""
+    from tests.gpu_util import dev
+    p, P, ai, ao, h, ssm, conv = block(nhm, SMALL, 3, 4, 4)
+    li, lo = lora(nhm, ai), lora(nhm, ao)
+    x, ssm, conv = dev(h), dev(ssm), dev(conv)
+    ids, slots = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.arange(4, dtype=torch.int32, device="cuda")
+    out = torch.full_like(x, 7)
+    ws = torch.empty(nhm.decode_lora_ws_layout(4, 24, SMALL)["total"], dtype=torch.uint8, device="cuda")
+    good = dict(lora_in=li, lora_out=lo, row_adapter=ids, hidden=x, slot_idx=slots, ssm_pool=ssm, conv_pool=conv, out=out, ws=ws)
+    for bad, error in [(dict(lora_in=lo), ValueError), (dict(lora_out=li), ValueError), (dict(row_adapter=ids[:3]), ValueError),
+                       (dict(row_adapter=ids.long()), TypeError), (dict(slot_idx=slots[:3]), ValueError),
+                       (dict(conv_pool=conv[:3]), ValueError), (dict(ssm_pool=ssm.double()), TypeError),
+                       (dict(out=out[:3]), ValueError), (dict(hidden=x[:, :128].contiguous()), ValueError),
+                       (dict(hidden=x.cpu()), TypeError), (dict(ws=ws[:1024]), nhm.NhmError),
+                       (dict(row_adapter=None), nhm.NhmError)]:
+        with pytest.raises(error):
+            nhm.mixer_decode_lora(P, **{**good, **bad})
+    torch.cuda.synchronize()
+    assert bool((out == 7).all())
+    nhm.mixer_decode_lora(P, **good)
+    torch.cuda.synchronize()
