@@ -94,6 +94,47 @@ int main() {
     lb.n_adapters = INT_MIN;
     EXPECT(lora(32, &w, &lb, P<void>(0x40000), need), NHM_ERR_SHAPE);
 
+    // the mixer with adapters
+    {
+        const nhm_geometry geo = {2688, 64, 64, 128, 8, 4, 1e-5f};
+        nhm_mixer_params mp = {geo, {P<uint8_t>(0x1000), P<float>(0x2000), P<float>(0x3000), 10304, 2688, 0},
+                               {P<uint8_t>(0x1000), P<float>(0x2000), P<float>(0x3000), 2688, 4096, 0},
+                               P<uint16_t>(0x4000), P<uint16_t>(0x5000), P<uint16_t>(0x6000), P<float>(0x7000),
+                               P<float>(0x8000), P<float>(0x9000)};
+        nhm_ws_layout lay;
+        EXPECT(nhm_mixer_decode_lora_ws_layout(&geo, 8, 16, &lay), NHM_OK);
+        const size_t dec = lay.total;
+        EXPECT(nhm_mixer_prefill_lora_ws_layout(&geo, 512, 2, 128, 16, &lay), NHM_OK);
+        const size_t pre = lay.total;
+        EXPECT(nhm_mixer_decode_lora_ws_layout(&geo, 8, INT_MIN, &lay), NHM_ERR_UNSUPPORTED);
+        EXPECT(nhm_mixer_decode_lora_ws_layout(nullptr, 8, 16, &lay), NHM_ERR_NULL);
+        EXPECT(nhm_mixer_prefill_lora_ws_layout(&geo, 512, 2, 128, INT_MAX, &lay), NHM_ERR_UNSUPPORTED);
+        auto decode = [&](const nhm_lora* in, const nhm_lora* out, int32_t batch, size_t wsb, const int32_t* ids) {
+            return nhm_mixer_decode_lora(&mp, in, out, ids, P<uint16_t>(0x10000), batch, P<int32_t>(0x20000),
+                                         P<void>(0x30000), NHM_F32, P<uint16_t>(0x40000), 16, P<uint16_t>(0x50000),
+                                         P<void>(0x60000), wsb, nullptr);
+        };
+        auto prefill = [&](const nhm_lora* in, const nhm_lora* out, int64_t T, size_t wsb) {
+            return nhm_mixer_prefill_lora(&mp, in, out, P<int32_t>(0x70000), P<uint16_t>(0x10000), T, P<int32_t>(0x80000), 2,
+                                          P<int32_t>(0x20000), P<int32_t>(0x90000), 128, P<void>(0x30000), NHM_F32,
+                                          P<uint16_t>(0x40000), 16, P<uint16_t>(0x50000), P<void>(0x60000), wsb, nullptr);
+        };
+        EXPECT(decode(&l, &l, 0, 0, nullptr), NHM_OK);
+        EXPECT(decode(&l, &l, 8, dec - 1, P<int32_t>(0x70000)), NHM_ERR_WORKSPACE);
+        EXPECT(decode(&l, &l, 8, dec, nullptr), NHM_ERR_NULL);
+        EXPECT(decode(&l, &l, 8, dec, P<int32_t>(0x70001)), NHM_ERR_ALIGN);
+        EXPECT(decode(&l, &l, INT_MIN, dec, P<int32_t>(0x70000)), NHM_ERR_SHAPE);
+        EXPECT(decode(&l, &l, INT_MAX, dec, P<int32_t>(0x70000)) != NHM_OK, 1);
+        EXPECT(decode(nullptr, &lb, 8, dec, P<int32_t>(0x70000)), NHM_ERR_SHAPE);
+        EXPECT(prefill(&l, &l, 512, pre - 1), NHM_ERR_WORKSPACE);
+        EXPECT(prefill(&l, &l, INT64_MAX, SIZE_MAX), NHM_ERR_SHAPE);
+        EXPECT(prefill(&l, &l, INT64_MIN, SIZE_MAX), NHM_ERR_SHAPE);
+        mp.in_proj.n = INT64_MAX;
+        EXPECT(decode(&l, nullptr, 8, dec, P<int32_t>(0x70000)), NHM_ERR_UNSUPPORTED);
+        mp.in_proj.n = INT64_MIN;
+        EXPECT(decode(&l, nullptr, 8, dec, P<int32_t>(0x70000)), NHM_ERR_SHAPE);
+    }
+
     // selection
     auto select = [&](nhm_dtype t, int64_t ld, int64_t G, int32_t K, int64_t V, int32_t n, void* ws, size_t wsb) {
         return nhm_beam_select(P<void>(0x1000), t, ld, G, K, V, P<float>(0x2000), nullptr, 0, n, P<float>(0x3000),
