@@ -489,19 +489,22 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
 // Few rows with an adapter per row, at a weight too narrow for the wide tiles. The panel kernel's few
 // workgroups take the adapters one after another in their epilogues (61 rows, 32 adapters, 2,688 x 4,096: 0.65 us
 // each). Here a workgroup owns 64 rows and 16 TN features, so that there are enough of them to fill the chip, and
-// its waves have two trades: two multiply 32 rows each, straight from memory, and kLoraSide others form
-// t B_e^T at the same time, the adapters shared out among them. A lane of those keeps the product of its own
-// row's adapter only, so all but one of the side waves hold zeros for an output, and their sum, taken in LDS
-// in wave order, is exact. Bound by the operand bytes a CU is handed, TN 16 features once per multiplying
-// wave and the 64 rows: four multiplying waves of 16 rows 29.5 us with the low-rank product, two 27.3, one
-// of 64 rows 29.2, the panel kernel 51 (21 without adapters); four steps in flight, six took 31.2 for 29.5.
-constexpr int kLoraMain = 2, kLoraSide = 8;
+// its waves have two trades: kLoraMain multiply, 16 rows each, and kLoraSide others form t B_e^T at the same
+// time, the adapters shared out among them. A lane of those keeps the product of its own row's adapter only, so
+// all but one of the side waves hold zeros for an output, and their sum, taken in LDS in wave order, is
+// exact. Bound by the operand bytes a CU is handed, 64 rows and each multiplying wave's 16 TN features: loads
+// take whole lines, and a wave-private piece of LDS turns them into operands without a barrier. Those 61 rows,
+// us with the low-rank product: this 19.8; loads in operand order, 64 bytes of a row at a time, 25.0; two
+// multiplying waves 21.5 (one code conversion of W and two of the rows per wave bound those); six or eight steps
+// in flight 22.3, 23.5; the panel kernel 51 (21 without adapters).
+constexpr int kLoraMain = 4, kLoraSide = 8;
 
 template <int TN, bool kExact, int P>     // P: t's parts
 __global__ __launch_bounds__((kLoraMain + kLoraSide) * 64) void lora_rows_kernel(const GemmArgs g) {
     constexpr int TM = 4 / kLoraMain;         // row tiles of a multiplying wave
     constexpr int D = TN == 1 ? 4 : 2;    // k-steps in flight per wave
     __shared__ v4f s_sum[kLoraSide][TN][4][64];
+    __shared__ __attribute__((aligned(16))) uint8_t s_tr[kLoraMain][(TN + TM) * 16 * 128];   // a step's rows of a wave
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, r16 = lane & 15;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * TN), m0 = (int64_t)blockIdx.y * 64;
@@ -562,56 +565,66 @@ __global__ __launch_bounds__((kLoraMain + kLoraSide) * 64) void lora_rows_kernel
     const int64_t row0 = m0 + wave * (16 * TM);
     const bool any = row0 < g.m;
     v4f acc[TN][TM];
-    float wsc[TN][4];
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t c = n0 + i * 16 + 4 * q + r;
-            wsc[i][r] = g.w_scale[(c < g.n ? c : g.n - 1) * g.ws_step];
-        }
-    }
-    const float sa = *g.a_scale;
     if (any) {
         const int nk = (int)((g.k + 127) / 128);
         const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc((void*)g.w, (short)0, (int)(g.n * g.k), 0x00020000);
         const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc((void*)g.a, (short)0, (int)(g.m * g.lda), 0x00020000);
-        uint32_t off[TN + TM];            // this lane's k bytes of a step, as the panel kernel's
+        // a load takes whole 128-byte lines of 8 rows: this lane's row and 16-byte chunk of each half of a
+        // 16-row tile, the chunk that swz128 places at slot lane % 8 of the row
+        const int lr = lane >> 3, slot = lane & 7;
+        uint32_t off[TN + TM][2];
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            const int64_t wrow = n0 + i * 16 + r16;
-            off[i] = wrow < g.n ? (uint32_t)(wrow * g.k + 16 * q) : kOutOfRange;
-        }
+        for (int i = 0; i < TN + TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const int64_t row = row0 + j * 16 + r16;
-            off[TN + j] = row < g.m ? (uint32_t)(row * g.lda + 16 * q) : kOutOfRange;
-        }
+            for (int h = 0; h < 2; ++h) {
+                const int64_t r = (i < TN ? n0 + 16 * i : row0 + 16 * (i - TN)) + 8 * h + lr;
+                off[i][h] = r < (i < TN ? g.n : g.m) ? (uint32_t)(r * (i < TN ? g.k : g.lda) + 16 * (slot ^ lr ^ h)) : kOutOfRange;
+            }
         uint4 v[D][TN + TM][2];
         auto fetch = [&](int s, uint4 (&dst)[TN + TM][2]) {
-            const int64_t kb = (int64_t)s * 128 + 16 * q;
+            const int64_t kb = (int64_t)s * 128;
 #pragma unroll
             for (int i = 0; i < TN + TM; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    dst[i][h] = bload(i < TN ? wrs : ars, kb + 64 * h < g.k ? off[i] + (uint32_t)s * 128 + 64 * h : kOutOfRange);
+                    dst[i][h] = bload(i < TN ? wrs : ars, kb + 16 * (slot ^ lr ^ h) < g.k ? off[i][h] + (uint32_t)kb : kOutOfRange);
         };
+        uint8_t* const tb = s_tr[wave];
 #pragma unroll
         for (int s = 0; s < D; ++s) fetch(s, v[s]);
         for (int k0 = 0; k0 < nk; k0 += D) {
 #pragma unroll
             for (int u = 0; u < D; ++u) {   // steps past k add zeros
 #pragma unroll
+                for (int i = 0; i < TN + TM; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<uint4*>(tb + (16 * i + 8 * h + lr) * 128 + slot * 16) = v[u][i][h];
+                fetch(k0 + u + D, v[u]);
+                v8i op[TN + TM];            // as the panel kernel's: k bytes [16 q, 16 q + 16) and [64 + 16 q, 80 + 16 q)
+#pragma unroll
+                for (int i = 0; i < TN + TM; ++i)
+                    op[i] = cat8(lds16(tb + swz128(16 * i + r16, q)), lds16(tb + swz128(16 * i + r16, q + 4)));
+#pragma unroll
                 for (int i = 0; i < TN; ++i)
 #pragma unroll
-                    for (int j = 0; j < TM; ++j)
-                        acc[i][j] = mfma16_step<kExact>(cat8(v[u][i][0], v[u][i][1]), cat8(v[u][TN + j][0], v[u][TN + j][1]), acc[i][j]);
-                fetch(k0 + u + D, v[u]);
+                    for (int j = 0; j < TM; ++j) acc[i][j] = mfma16_step<kExact>(op[i], op[TN + j], acc[i][j]);
             }
         }
     }
+    float wsc[TN][4];                     // read here: there are no registers for them during the loop
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t c = n0 + i * 16 + 4 * q + r;
+            wsc[i][r] = g.w_scale[(c < g.n ? c : g.n - 1) * g.ws_step];
+        }
+    const float sa = *g.a_scale;
     __syncthreads();
     if (!any) return;
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
@@ -1411,11 +1424,11 @@ nhm_status launch_gemm(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* 
 }
 
 // The decode batch's kernel where the panel kernel would run, while its workgroups of 48 features are not
-// more than the CUs. Past that the CUs' operand bytes decide, and the panel kernel has fewer (32 adapters of rank
-// 32, this kernel against the panel's, us: 61 x 2,688 x 4,096 27 and 51, 61 x 10,304 x 2,688 31 and 45, 256 x
-// 2,688 x 4,096 43 and 53, but 64 x 20,000 x 1,024 37 and 35, 64 x 30,000 x 1,024 52 and 38, 100 x 10,304 x 2,688
-// 47 and 46; one adapter: 128 x 2,688 x 4,096 30 and 32, 640 x 512 x 512 12 and 14, but 256 x 2,688 x 4,096 30 and
-// 27, 64 x 20,000 x 1,024 24 and 18).
+// more than the CUs. Past that the CUs' operand bytes decide, and the panel kernel has fewer: it leads with one
+// adapter and trails with many (us, this kernel against the panel's, 32 adapters of rank 32: 61 x 2,688 x 4,096 20 and
+// 51, 61 x 10,304 x 2,688 24 and 45, 256 x 2,688 x 4,096 34 and 53; one adapter: 128 x 2,688 x 4,096 23 and 32,
+// 256 x 2,688 x 4,096 27 and 27; past it, 32 adapters and one: 100 x 10,304 x 2,688 41 and 48, 35 and 29, 64 x
+// 30,000 x 1,024 43 and 38, 27 and 19, 500 x 2,688 x 4,096 63 and 67, 43 and 32).
 static bool lora_rows_serve(const GemmArgs& g) {
     constexpr int64_t k2G = int64_t(1) << 31;
     const int64_t nmt = (g.m + 63) / 64;
