@@ -494,9 +494,9 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
 // all but one of the side waves hold zeros for an output, and their sum, taken in LDS in wave order, is
 // exact. Bound by the operand bytes a CU is handed, 64 rows and each multiplying wave's 16 TN features: loads
 // take whole lines, and a wave-private piece of LDS turns them into operands without a barrier. Those 61 rows,
-// us with the low-rank product: this 19.8; loads in operand order, 64 bytes of a row at a time, 25.0; two
-// multiplying waves 21.5 (one code conversion of W and two of the rows per wave bound those); six or eight steps
-// in flight 22.3, 23.5; the panel kernel 51 (21 without adapters).
+// us with the low-rank product: this 19.8; with two multiplying waves of 32 rows 21.5, of those with six or eight
+// steps in flight for four 22.3, 23.5, with loads in operand order, 64 bytes of a row at a time, 25.0; the panel
+// kernel 51 (21 without adapters).
 constexpr int kLoraMain = 4, kLoraSide = 8;
 
 template <int TN, bool kExact, int P>     // P: t's parts

@@ -11,13 +11,13 @@
 //    round), and a share of the tile's distinct adapters, of whose rows alone it reads x.
 //  * Many rows (8,192 or more fill half of the chip): x's bytes bound it. A workgroup owns 64 rows and up to 64 ranks,
 //    4 waves that each take whole 64 x 64 k-steps, so that x and A enter the CU once, the next
-//    step's operands on their way while one is multiplied.
-// The waves' sums meet in LDS and are added in wave order. A lane's share of a 64-wide k-step is 16
-// consecutive values (two matrix instructions' worth; any deal of k to lanes will do that is the same for
-// both operands), so that the first of its two loads asks for whole 128-byte lines: with 32-wide steps
-// the halves of a line were fetched apart.
+//    step's operands on their way while one is multiplied. Loads take whole lines, which turn into operands in
+//    a wave-private piece of LDS (with the few rows' deal instead 60 us for 48).
+// The waves' sums meet in LDS and are added in wave order. With few rows a lane's share of a 64-wide k-step is
+// 16 consecutive values (two matrix instructions' worth; any deal of k to lanes will do that is the same
+// for both operands), so that the first of its two loads asks for whole 128-byte lines.
 // k = 2,688, codes formed: one row of rank 16 4.1 us (an empty launch 2.6), 8 rows with an adapter each of rank 64
-// 5.3, 477 rows of rank 24 8.4, 15,360 rows of rank 64 60 (eight waves 69).
+// 5.3, 477 rows of rank 24 8.4, 15,360 rows of rank 64 48.
 #include "nhm_device.h"
 #include "nhm_internal.h"
 
@@ -152,35 +152,48 @@ constexpr int kManyWaves = 4, kManyRows = 4;   // row tiles of 16 per workgroup
 template <typename X, int NR>
 __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const LoraDownArgs g) {
     __shared__ v4f s_part[kManyWaves][kManyRows * NR][64];
+    __shared__ __attribute__((aligned(16))) uint8_t s_tr[kManyWaves][(kManyRows + NR) * 16 * 128];   // a wave's step
+    constexpr bool kCodes = sizeof(X) == 1;        // x is given as codes
+    constexpr int kXLoads = kCodes ? kManyRows : 2 * kManyRows;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r16 = lane & 15, q16 = 16 * (lane >> 4);
+    const int r16 = lane & 15, q = lane >> 4;
     const int64_t row0 = (int64_t)blockIdx.x * (16 * kManyRows);
     const int rank0 = blockIdx.y * 16 * NR;
     const float s = *g.a_scale;
     const bool fast = fast_scale(s);
     const float rs = __fdiv_rn(1.0f, s);
     int id[kManyRows];
-    const X* xr[kManyRows];
 #pragma unroll
     for (int i = 0; i < kManyRows; ++i) {
         const int64_t row = row0 + 16 * i + r16;
         id[i] = row < g.m ? g.row_adapter[row] : -1;
         if (id[i] >= g.n_adapters) id[i] = -1;
-        xr[i] = x_rows<X>(g) + (row < g.m ? row : g.m - 1) * g.ld_x;
+    }
+    // A load of bf16 values takes whole 128-byte lines of 8 rows: lane l row l / 8 and the chunk of 8 values that
+    // swz128 places at slot l % 8; one of codes 64 bytes of 16 rows: row l / 4 and 16 values.
+    const int lr = lane >> 3, slot = lane & 7, cr = lane >> 2, cc = lane & 3;
+    auto chunk = [&](int u) { return slot ^ lr ^ (u & 1); };       // of 8-row unit u
+    const X* xr[kXLoads];
+#pragma unroll
+    for (int u = 0; u < kXLoads; ++u) {
+        const int64_t row = row0 + (kCodes ? 16 * u + cr : 8 * u + lr);
+        xr[u] = x_rows<X>(g) + (row < g.m ? row : g.m - 1) * g.ld_x + (kCodes ? 16 * cc : 8 * chunk(u));
     }
     const int full = (int)(g.k / 64);              // whole 64-wide steps; a part of one may follow
     const int steps = (int)((g.k + 63) / 64);
-    const bf16x8 zero = __builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u});
-    bool codes = sizeof(X) == 2 && g.q && blockIdx.y == 0;
+    const v4u zero = {0u, 0u, 0u, 0u};
+    bool codes = !kCodes && g.q && blockIdx.y == 0;
+    uint8_t* const tx = s_tr[wave];
+    uint8_t* const ta = tx + kManyRows * 16 * 128;
 
-    struct Ops { bf16x8 x[kManyRows][2], a[NR][2]; };
+    struct Ops { v4u x[kXLoads], a[2 * NR]; };
     v4f acc[kManyRows][NR];
     auto pass = [&](int cur, bool with_codes) {
-        const uint16_t* ar[NR];
+        const uint16_t* ar[2 * NR];
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-            const int r = rank0 + 16 * j + r16;
-            ar[j] = g.a + ((int64_t)(cur < 0 ? 0 : cur) * g.rank + (r < g.rank ? r : g.rank - 1)) * g.k;
+        for (int v = 0; v < 2 * NR; ++v) {
+            const int r = rank0 + 8 * v + lr;
+            ar[v] = g.a + ((int64_t)(cur < 0 ? 0 : cur) * g.rank + (r < g.rank ? r : g.rank - 1)) * g.k + 8 * chunk(v);
         }
 #pragma unroll
         for (int i = 0; i < kManyRows; ++i)
@@ -189,32 +202,53 @@ __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const L
         // a step past the last whole one reads that again and is not used: loads under a branch would
         // all be waited for at the next use of any
         auto load = [&](Ops& o, int step) {
-            const int kk = min(step, full - 1) * 64 + q16;
+            const int kk = min(step, full - 1) * 64;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int u = 0; u < kXLoads; ++u) o.x[u] = *reinterpret_cast<const v4u*>(xr[u] + kk);
 #pragma unroll
-                for (int i = 0; i < kManyRows; ++i) o.x[i][h] = x8(xr[i] + kk + 8 * h);
-#pragma unroll
-                for (int j = 0; j < NR; ++j) o.a[j][h] = x8(ar[j] + kk + 8 * h);
-            }
+            for (int v = 0; v < 2 * NR; ++v) o.a[v] = *reinterpret_cast<const v4u*>(ar[v] + kk);
         };
         auto use = [&](const Ops& o, int step) {
-            const int kk = step * 64 + q16;
-            if (with_codes) {
+            const int kk = step * 64;
+            if constexpr (!kCodes) {
+                if (with_codes) {
 #pragma unroll
-                for (int i = 0; i < kManyRows; ++i) {
-                    const int64_t row = row0 + 16 * i + r16;
-                    const uint2 c0 = codes8(o.x[i][0], s, rs, fast), c1 = codes8(o.x[i][1], s, rs, fast);
-                    if (kk < g.k && row < g.m) *reinterpret_cast<v4u*>(g.q + row * g.k + kk) = v4u{c0.x, c0.y, c1.x, c1.y};
+                    for (int u = 0; u < kXLoads; ++u) {
+                        const int64_t row = row0 + 8 * u + lr;
+                        const int at = kk + 8 * chunk(u);
+                        const uint2 c = codes8(__builtin_bit_cast(bf16x8, o.x[u]), s, rs, fast);
+                        if (at < g.k && row < g.m) *reinterpret_cast<uint2*>(g.q + row * g.k + at) = c;
+                    }
                 }
             }
             if (cur >= 0) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int u = 0; u < kXLoads; ++u) {
+                    if constexpr (kCodes) {
+                        *reinterpret_cast<v4u*>(tx + swz128(16 * u + cr, 2 * cc)) =
+                            __builtin_bit_cast(v4u, e4m3x8_to_bf16(o.x[u][0], o.x[u][1]));
+                        *reinterpret_cast<v4u*>(tx + swz128(16 * u + cr, 2 * cc + 1)) =
+                            __builtin_bit_cast(v4u, e4m3x8_to_bf16(o.x[u][2], o.x[u][3]));
+                    } else {
+                        *reinterpret_cast<v4u*>(tx + (8 * u + lr) * 128 + slot * 16) = o.x[u];
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 2 * NR; ++v) *reinterpret_cast<v4u*>(ta + (8 * v + lr) * 128 + slot * 16) = o.a[v];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    bf16x8 xf[kManyRows], af[NR];
+#pragma unroll
+                    for (int i = 0; i < kManyRows; ++i)
+                        xf[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4u*>(tx + swz128(16 * i + r16, q + 4 * h)));
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+                        af[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4u*>(ta + swz128(16 * j + r16, q + 4 * h)));
 #pragma unroll
                     for (int i = 0; i < kManyRows; ++i)
 #pragma unroll
-                        for (int j = 0; j < NR; ++j) acc[i][j] = mfma_bf16(o.a[j][h], o.x[i][h], acc[i][j]);
+                        for (int j = 0; j < NR; ++j) acc[i][j] = mfma_bf16(af[j], xf[i], acc[i][j]);
+                }
             }
         };
         Ops o0, o1;
@@ -227,15 +261,13 @@ __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const L
                 if (st + kManyWaves < full) use(o1, st + kManyWaves);
             }
         }
-        if (full < steps && wave == full % kManyWaves) {     // the rest of a k that 64 does not divide
-            const int kk = full * 64 + q16;
+        if (full < steps && wave == full % kManyWaves) {     // the rest of a k that 64 does not divide (16 does)
+            const int kk = full * 64;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int u = 0; u < kXLoads; ++u)
+                o0.x[u] = kk + (kCodes ? 16 * cc : 8 * chunk(u)) < g.k ? *reinterpret_cast<const v4u*>(xr[u] + kk) : zero;
 #pragma unroll
-                for (int i = 0; i < kManyRows; ++i) o0.x[i][h] = kk < g.k ? x8(xr[i] + kk + 8 * h) : zero;
-#pragma unroll
-                for (int j = 0; j < NR; ++j) o0.a[j][h] = kk < g.k ? x8(ar[j] + kk + 8 * h) : zero;
-            }
+            for (int v = 0; v < 2 * NR; ++v) o0.a[v] = kk + 8 * chunk(v) < g.k ? *reinterpret_cast<const v4u*>(ar[v] + kk) : zero;
             use(o0, full);
         }
     };
