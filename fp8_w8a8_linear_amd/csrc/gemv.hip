@@ -23,6 +23,8 @@
 // MFMA, so a wave keeps its whole share in flight. The per-wave partial tiles are
 // summed through LDS in wave order -- deterministic, and no communication between
 // workgroups (an agent-scope fence would write back the L2 of every XCD).
+#include <type_traits>
+
 #include "lora_device.h"
 #include "nhm_device.h"
 #include "nhm_internal.h"
@@ -51,39 +53,67 @@ struct GemvArgs {
 // The adapters' part of the workgroup's kTiles row tiles, split over kWaves waves: wave w takes the
 // w-th, (w + kWaves)-th, ... distinct adapter among the tokens. d[t] register r of lane l is
 // feature n0 + 16 t + 4 (l / 16) + r of token l % 16; lanes of other tokens stay as they are.
-template <int S, int kWaves, int kTiles>
+template <int S, int P, int kWaves, int kTiles>     // S: rp / 32, P: t's parts
 __device__ __forceinline__ void gemv_lora(v4f (&d)[kTiles], const GemvArgs& g, int64_t n0, int wave, int lane) {
     const int r16 = lane & 15, q8 = 8 * (lane >> 4);
     const int id[1] = {lora_row(g.lora, r16, g.m)};
     const char* const tb = reinterpret_cast<const char*>(g.lora.t);
     const uint32_t tpart = (uint32_t)g.lora.rp * 2;
-    const uint32_t toff = (uint32_t)(r16 < g.m ? r16 : g.m - 1) * g.lora.parts * tpart + q8 * 2;
+    const uint32_t toff = (uint32_t)(r16 < g.m ? r16 : g.m - 1) * P * tpart + q8 * 2;
+    uint64_t todo = __ballot(id[0] >= 0);
     int turn = 0;
-    lora_each(id, [&](int cur) {
-        if (turn++ % kWaves != wave) return;
+    auto next = [&] {                   // this wave's next adapter, -1 after the last
+        while (todo) {
+            const int cur = __builtin_amdgcn_readlane(id[0], __builtin_ctzll(todo));
+            todo &= ~__ballot(id[0] == cur);
+            if (turn++ % kWaves == wave) return cur;
+        }
+        return -1;
+    };
+    // Loads without a branch (ranks past the end read the last ones and become zeros), so that the next
+    // adapter's are on their way while one is worked on.
+    struct Ops { v4u b[S][kTiles], t[P][S]; };
+    auto load = [&](Ops& o, int cur) {
         const char* const bb = lora_b_base(g.lora, cur, n0, g.n);
-        bf16x8 bf[S][kTiles], tf[3][S];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int s = 0; s < S; ++s) {
+            const int at = min(32 * s + q8, g.lora.rank - 8) * 2;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
-                bf[s][t] = lora_load(bb, lora_b_off(g.lora, 16 * t + r16, n0, g.n) + q8 * 2 + 64 * s, 32 * s + q8 < g.lora.rank);
+                o.b[s][t] = *reinterpret_cast<const v4u*>(bb + (lora_b_off(g.lora, 16 * t + r16, n0, g.n) + at));
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-#pragma unroll
-            for (int s = 0; s < S; ++s) tf[p][s] = lora_load(tb, toff + (p < g.lora.parts ? p : 0) * tpart + 64 * s, true);
+            for (int p = 0; p < P; ++p) o.t[p][s] = *reinterpret_cast<const v4u*>(tb + (toff + p * tpart + 64 * s));
+        }
+    };
+    auto use = [&](const Ops& o, int cur) {
+        const v4u zero = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             v4f x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+            for (int p = 0; p < P; ++p)
 #pragma unroll
                 for (int s = 0; s < S; ++s)
-                    if (p < g.lora.parts) x = mfma_bf16(bf[s][t], tf[p][s], x);
+                    x = mfma_bf16(__builtin_bit_cast(bf16x8, 32 * s + q8 < g.lora.rank ? o.b[s][t] : zero),
+                                  __builtin_bit_cast(bf16x8, o.t[p][s]), x);
 #pragma unroll
             for (int r = 0; r < 4; ++r) d[t][r] = id[0] == cur ? x[r] : d[t][r];
         }
-    });
+    };
+    int cur = next();
+    if (cur < 0) return;
+    Ops o0, o1;
+    load(o0, cur);
+    for (;;) {
+        const int then = next();
+        load(o1, then < 0 ? cur : then);
+        use(o0, cur);
+        if (then < 0) break;
+        cur = next();
+        load(o0, cur < 0 ? then : cur);
+        use(o1, then);
+        if (cur < 0) break;
+    }
 }
 
 // Wave `wave` of kWaves: its sums, to LDS.
@@ -92,9 +122,14 @@ __device__ __forceinline__ void gemv_lora_part(v4f (*part)[64], const GemvArgs& 
     v4f d[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (g.lora.rp == 32) gemv_lora<1, kWaves, kTiles>(d, g, n0, wave, lane);
-    else if (g.lora.rp == 64) gemv_lora<2, kWaves, kTiles>(d, g, n0, wave, lane);
-    else gemv_lora<4, kWaves, kTiles>(d, g, n0, wave, lane);
+    auto run = [&](auto parts) {
+        constexpr int P = decltype(parts)::value;
+        if (g.lora.rp == 32) gemv_lora<1, P, kWaves, kTiles>(d, g, n0, wave, lane);
+        else if (g.lora.rp == 64) gemv_lora<2, P, kWaves, kTiles>(d, g, n0, wave, lane);
+        else gemv_lora<4, P, kWaves, kTiles>(d, g, n0, wave, lane);
+    };
+    if (g.lora.parts == 2) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 3>{});
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) part[t][lane] = d[t];
 }
@@ -106,8 +141,8 @@ constexpr int kStreamAux = 0;
 
 // Waves beside the kWaves that stream the weight, for the adapters' part, formed while the weight arrives (by the
 // streaming waves afterwards: 8.0 us for one row of rank 16 and 10.8 for 8 rows with an adapter each of rank 64,
-// 10,304 x 2,688; beside them 6.9 and 10.2, and 7.7 with no adapter). Beside 16 waves there is no room; those do it
-// afterwards.
+// 10,304 x 2,688; beside them 7.1 and 10.1, with the next adapter's loads ahead of this one's products 9.2; 7.7 with
+// no adapter). Beside 16 waves there is no room; those do it afterwards.
 constexpr int gemv_side(bool lora, int waves) { return lora && waves < 16 ? 4 : 0; }
 
 template <int kWaves, int kSteps, int kTiles, bool kLines, bool kLora>
