@@ -277,7 +277,7 @@ __device__ __forceinline__ void lora_mma16(v4f (&acc)[TNW][TMW], const LoraEpi& 
 #pragma unroll
         for (int i = 0; i < TNW; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] += id[j] == cur ? x[i][r] : 0.f;
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = id[j] == cur ? acc[i][j][r] + x[i][r] : acc[i][j][r];   // -0 stays
     };
 #pragma unroll
     for (int j = 0; j < TMW; ++j) {
@@ -318,7 +318,7 @@ __device__ __forceinline__ void lora_mma32(v16f (&acc)[NI][NJ], const LoraEpi& e
                     x = mfma32_bf16(b, __builtin_bit_cast(bf16x8, lds16(tl + p * TM * 128 + swz128(mw + 32 * jx + r32, 2 * h + q))), x);
             }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][jx][r] += id[jx] == cur ? x[r] : 0.f;
+            for (int r = 0; r < 16; ++r) acc[i][jx][r] = id[jx] == cur ? acc[i][jx][r] + x[r] : acc[i][jx][r];
             asm volatile("" : "+v"(acc[i][jx]));   // added here, not after the last tile's products
         }
 }

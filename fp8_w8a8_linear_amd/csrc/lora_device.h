@@ -25,13 +25,13 @@ __device__ __forceinline__ bf16x8 lora_load(const char* base, uint32_t off, bool
     if (on) v = *reinterpret_cast<const v4u*>(base + off);
     return __builtin_bit_cast(bf16x8, v);
 }
-// Adapter cur's features from n0 on (uniform): feature n0 + i at byte lora_b_off(e, i, n0, n), the last
+// Adapter cur's features from n0 < n on (uniform): feature n0 + i at byte lora_b_off(e, i, n0, n), the last
 // feature of the weight standing in for those past it (they are not stored).
 __device__ __forceinline__ const char* lora_b_base(const LoraEpi& e, int cur, int64_t n0, int64_t n) {
     return reinterpret_cast<const char*>(e.b + ((int64_t)cur * n + n0) * e.rank);
 }
 __device__ __forceinline__ uint32_t lora_b_off(const LoraEpi& e, int i, int64_t n0, int64_t n) {
-    const int64_t last = n - 1 - n0;       // negative for a tile part past the weight: one feature back and further
+    const int64_t last = n - 1 - n0;
     return (uint32_t)((i < last ? i : last) * e.rank * 2);
 }
 

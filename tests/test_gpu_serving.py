@@ -138,6 +138,24 @@ def test_lora_rows_without_adapter(nhm, m, n, k, exact, f32):
     assert not torch.equal(got[~bare], base[~bare]) or not bool((~bare).any())
 
 
+@pytest.mark.parametrize("m,n,k", [(7, 300, 272), (50, 300, 272), (64, 20000, 272), (257, 10304, 272), (641, 1000, 1040),
+                                   (700, 10304, 336)])
+def test_lora_rows_without_adapter_keep_the_sign_of_zero(nhm, m, n, k):
+    """A zero row without an adapter under negative weight scales is -0 with and without its neighbours' adapters."""
+    inp = list(lora_inputs(m, n, k, 16, 3, seed=15))
+    inp[0][::2] = 0
+    inp[2] = -np.abs(inp[2])
+    inp[7] = np.where(np.arange(m) % 2 == 0, -1, 1).astype(np.int32)
+    x, W, L, idd = lora_device(nhm, inp)
+    for t in (nhm.NHM_BF16, nhm.NHM_F32):
+        got = nhm.fp8_linear_lora(x, W, L, idd, out_type=t)
+        base = nhm.fp8_linear(x, W, out_type=t)
+        torch.cuda.synchronize()
+        bits_of = lambda o: o[::2].view(torch.int32 if t == nhm.NHM_F32 else torch.int16)  # noqa: E731
+        assert torch.equal(bits_of(got), bits_of(base))
+        assert bool((bits_of(base) < 0).all())
+
+
 @pytest.mark.parametrize("m,n,k", [(8, 2688, 4096), (61, 2688, 4096), (257, 10304, 272), (700, 10304, 336),
                                    (641, 1000, 1040), (50, 10304, 336), (64, 8001, 528), (300, 2690, 272),
                                    (64, 20000, 272)])
