@@ -132,11 +132,12 @@ __device__ __forceinline__ i32x4 buffer_desc(const void* base, int64_t bytes) {
 // 16 bytes per lane from byte offset voff of the buffer into LDS at lds + 16 * lane (an
 // offset past the range writes zeros). Issued as asm so that the compiler's wait insertion
 // does not hold every later LDS read behind it; the kernel waits for these loads itself. The
-// compiler does not see what is in the asm, so the wait state between the write of M0 and the
-// load that takes its LDS address from it stands there too.
+// compiler does not see what is in the asm, so the wait states ahead of the load stand there too:
+// one after the write of M0, which holds the LDS address, and five after a vector instruction that
+// wrote a register of the descriptor (lora_tile's readfirstlane, or the reload of a spilled one).
 __device__ __forceinline__ void dma16(const i32x4& rs, const uint8_t* lds, uint32_t voff) {
     const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)lds;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(rs)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(rs)
                  : "memory", "m0");
 }
 

@@ -93,7 +93,25 @@ def m0_before_lds(code):
     return out
 
 
-RULES = {"m0_before_lds": m0_before_lds}
+def sgpr_before_vmem(code):
+    """A scalar register that a vector instruction writes (v_readfirstlane, v_readlane, a spilled one's reload), then
+    a memory instruction that reads it, in its descriptor or offset: five wait states."""
+    out = []
+    for n, i in enumerate(code):
+        mine = valu_sgprs(i)
+        if not mine:
+            continue
+
+        def visit(j, w, left=mine):
+            if j.vmem and regs(",".join(j.args), "s") & left:
+                out.append((w, 5, i.text(), j.text()))
+                return True
+            return False
+        paths(code, n, 5, visit)
+    return out
+
+
+RULES = {"m0_before_lds": m0_before_lds, "sgpr_before_vmem": sgpr_before_vmem}
 
 
 def parse(lines):
@@ -181,6 +199,10 @@ def listing(text):
     ("m0_before_lds", "s_mov_b32 m0, s4\nbuffer_load_dwordx4 v1, s[0:3], 0 offen lds", 0),
     ("m0_before_lds", "s_mov_b32 m0, s4\ns_nop 0\nbuffer_load_dwordx4 v1, s[0:3], 0 offen lds", None),
     ("m0_before_lds", "s_mov_b32 m0, s4\nbuffer_load_dwordx4 v[4:7], v1, s[0:3], 0 offen", None),
+    ("sgpr_before_vmem", "v_readfirstlane_b32 s6, v2\ns_nop 3\nbuffer_load_dwordx4 v0, s[4:7], 0 offen lds", 4),
+    ("sgpr_before_vmem", "v_readfirstlane_b32 s6, v2\ns_nop 4\nbuffer_load_dwordx4 v0, s[4:7], 0 offen lds", None),
+    ("sgpr_before_vmem", "v_cmp_lt_i32_e64 s[8:9], v0, v1\ns_nop 4\nglobal_load_dword v0, v1, s[8:9]", None),
+    ("sgpr_before_vmem", "a:\nbuffer_load_dword v0, v1, s[4:7], 0 offen\nv_readlane_b32 s7, v2, 3\ns_cbranch_scc1 a", 1),
 ])
 def test_rules(rule, text, worst):
     """What each rule finds in a listing: the fewest wait states of a pair that is too close, None without one."""
