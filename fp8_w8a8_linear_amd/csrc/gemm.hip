@@ -256,8 +256,11 @@ __device__ __forceinline__ void lora_tile(const LoraEpi& e, const LoraRows<TM>& 
 
 // compute() of waves with 16 x 16 tiles: acc[i][j] register r of lane l is feature nw + 16 i +
 // 4 (l / 16) + r of row mw + 16 j + l % 16 of the workgroup's tile. The products are formed apart and
-// added in the lanes they belong to; kParts matrix instructions per 32 ranks, written out (as a loop over the
-// parts their sums were carried around in copies that a read overtook: wrong sums in one register).
+// added in the lanes they belong to; kParts matrix instructions per 32 ranks, written out: as a loop over a
+// number of parts known at run time their sums are carried around it in copies, and across the loop's back edge the
+// compiler leaves seven wait states between a matrix instruction and the copy of its last register, where eight
+// are needed (and stand in all straight-line code): that register's sums came out wrong. lora_mma32's loop over the ranks
+// has its twelve; tests/test_wait_states.py counts both in the built kernels.
 template <int TM, int kParts, int TNW, int TMW>
 __device__ __forceinline__ void lora_mma16(v4f (&acc)[TNW][TMW], const LoraEpi& e, const int (&id)[TMW], int cur, int c0,
                                            const uint8_t* tl, const uint8_t* bl, int mw, int nw, int lane) {

@@ -111,7 +111,36 @@ def sgpr_before_vmem(code):
     return out
 
 
-RULES = {"m0_before_lds": m0_before_lds, "sgpr_before_vmem": sgpr_before_vmem}
+# Wait states until a matrix instruction's result may be read or overwritten by others: four per pass and four more
+# stand between them wherever the compiler issues a result's use in a straight line.
+MFMA_WAIT = {"v_mfma_f32_16x16x32_bf16": 8, "v_mfma_f32_16x16x128_f8f6f4": 12, "v_mfma_f32_32x32x16_bf16": 12,
+             "v_mfma_f32_32x32x64_f8f6f4": 20}
+
+
+def mfma_result(code):
+    """A matrix instruction, then a read of its result that is not the sum of another one, or a write over it."""
+    out = []
+    for n, i in enumerate(code):
+        if not i.op.startswith("v_mfma"):
+            continue
+        want, mine = MFMA_WAIT[i.op], regs(i.args[0], "va")
+
+        def visit(j, w, i=i, want=want, mine=mine):
+            if not j.args or j.op.startswith("s_"):
+                return False
+            load = (j.vmem or j.op.startswith("ds_")) and not j.store
+            to_lds = j.vmem and j.args[-1].endswith(" lds")
+            reads = regs(",".join(j.args if j.store or to_lds else j.args[1:3] if j.op.startswith("v_mfma") else j.args[1:]), "va")
+            writes = set() if j.store or to_lds else regs(j.args[0], "va")
+            if reads & mine or (writes & mine and not load and not j.op.startswith("v_mfma")):
+                out.append((w, want, i.text(), j.text()))
+                return True
+            return bool(writes & mine)
+        paths(code, n, want, visit)
+    return out
+
+
+RULES = {"m0_before_lds": m0_before_lds, "sgpr_before_vmem": sgpr_before_vmem, "mfma_result": mfma_result}
 
 
 def parse(lines):
@@ -203,6 +232,14 @@ def listing(text):
     ("sgpr_before_vmem", "v_readfirstlane_b32 s6, v2\ns_nop 4\nbuffer_load_dwordx4 v0, s[4:7], 0 offen lds", None),
     ("sgpr_before_vmem", "v_cmp_lt_i32_e64 s[8:9], v0, v1\ns_nop 4\nglobal_load_dword v0, v1, s[8:9]", None),
     ("sgpr_before_vmem", "a:\nbuffer_load_dword v0, v1, s[4:7], 0 offen\nv_readlane_b32 s7, v2, 3\ns_cbranch_scc1 a", 1),
+    ("mfma_result", "v_mfma_f32_16x16x32_bf16 a[0:3], v[0:3], v[4:7], a[0:3]\ns_nop 6\nv_accvgpr_read_b32 v8, a3", 7),
+    ("mfma_result", "v_mfma_f32_16x16x32_bf16 a[0:3], v[0:3], v[4:7], a[0:3]\ns_nop 7\nv_accvgpr_read_b32 v8, a3", None),
+    ("mfma_result", "v_mfma_f32_32x32x16_bf16 v[0:15], v[20:23], v[24:27], 0\nv_mfma_f32_32x32x16_bf16 v[0:15], v[20:23], "
+     "v[24:27], v[0:15]", None),
+    # a loop over the parts of an adapter's product, as the compiler left it: seven ahead of the read across the back edge
+    ("mfma_result", "a:\nds_read_b128 v[158:161], v156\nv_accvgpr_read_b32 v174, a8\nv_accvgpr_read_b32 v170, a4\ns_nop 2\n"
+     "v_accvgpr_read_b32 v165, a3\nv_accvgpr_write_b32 a3, v165\ns_nop 1\n"
+     "v_mfma_f32_16x16x32_bf16 a[0:3], v[0:3], v[158:161], a[0:3]\ns_cbranch_scc1 a", 7),
 ])
 def test_rules(rule, text, worst):
     """What each rule finds in a listing: the fewest wait states of a pair that is too close, None without one."""
