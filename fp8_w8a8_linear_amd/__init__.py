@@ -157,6 +157,20 @@ def _dev_tensor(x, name):
     return x
 
 
+def _empty(shape, dtype, dev, stream, kept=True):
+    """Memory that a call on `stream` (None: the current one) writes, taken under that stream, so that no earlier tenant's
+    work is still in it and none gets it while the call runs. kept: it goes to the caller, who may use it on the current
+    stream too."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if kept:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 class Fp8Weight:
     """One FP8 W8A8 projection on the device: e4m3 codes [n, k] (uint8), f32 weight scale [n] (per
     output channel) or [1] (per tensor), f32 a_scale [1]."""
@@ -204,7 +218,7 @@ def quantize_static(x, scale, q=None, stream=None):
     x = _dev_tensor(x, "x")
     rows, cols = (x.shape[0], x.shape[1]) if x.dim() == 2 else (1, x.numel())
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, cols), torch.uint8, x.device, stream)
     _check(lib.nhm_fp8_quantize_static(_ptr(x), rows, cols, cols, _ptr(scale), _ptr(q), cols, _stream(stream)))
     return q
 
@@ -226,10 +240,10 @@ def fp8_linear(a, weight: Fp8Weight, out=None, ws=None, a_type=None, stream=None
         out_type = NHM_F32 if out is not None and out.dtype == torch.float32 else NHM_BF16
     m = int(a.shape[0])
     if out is None:
-        out = torch.empty((m, weight.n), dtype=torch.float32 if out_type == NHM_F32 else torch.int16, device=a.device)
+        out = _empty((m, weight.n), torch.float32 if out_type == NHM_F32 else torch.int16, a.device, stream)
     need = fp8_linear_workspace_bytes(m, weight.n, weight.k, a_type)
     if ws is None and need > 0:
-        ws = torch.zeros(need, dtype=torch.uint8, device=a.device)
+        ws = _empty(need, torch.uint8, a.device, stream, kept=False)
     fn = lib.nhm_fp8_linear_exact if exact else lib.nhm_fp8_linear_ex
     _check(fn(_ptr(a), a_type, m, a.shape[1], C.byref(weight.struct), _ptr(out), out_type, out.shape[1], _ptr(ws),
               0 if ws is None else ws.numel(), _stream(stream)))
@@ -242,7 +256,7 @@ def fp8_dequant_channel_bf16(w, w_scale, out=None, stream=None):
     w = _dev_tensor(w, "w")
     n, k = int(w.shape[0]), int(w.shape[1])
     if out is None:
-        out = torch.empty((n, k), dtype=torch.int16, device=w.device)
+        out = _empty((n, k), torch.int16, w.device, stream)
     _check(lib.nhm_fp8_dequant_channel_bf16(_ptr(w), _ptr(w_scale), n, k, w.stride(0), _ptr(out), out.stride(0),
                                             _stream(stream)))
     return out
@@ -364,10 +378,10 @@ def _bf16_types():
     return (torch.bfloat16, torch.int16, torch.uint16)
 
 
-def _workspace(ws, need, dev):
+def _workspace(ws, need, dev, stream):
     import torch
     if ws is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        return _empty(max(need, 1), torch.uint8, dev, stream, kept=False)
     _on(dev, [(ws, "ws", (torch.uint8,), None)])
     return ws
 
@@ -415,11 +429,11 @@ def fp8_linear_lora(a, weight: Fp8Weight, lora: Lora, row_adapter, out=None, ws=
     if (lora.n, lora.k) != (weight.n, weight.k):
         raise ValueError(f"adapters of a [{lora.n}, {lora.k}] projection beside a [{weight.n}, {weight.k}] weight")
     if out is None:
-        out = torch.empty((m, weight.n), dtype=torch.float32 if out_type == NHM_F32 else torch.int16, device=dev)
+        out = _empty((m, weight.n), torch.float32 if out_type == NHM_F32 else torch.int16, dev, stream)
     else:
         _on(dev, [(out, "out", (torch.float32,) if out_type == NHM_F32 else _bf16_types(), (m, weight.n))])
     ws = _workspace(ws, 0 if ws is not None else fp8_linear_lora_workspace_bytes(m, weight.n, weight.k, a_type, lora.rank),
-                    dev)
+                    dev, stream)
     _call(dev, stream, lib.nhm_fp8_linear_lora, a.data_ptr(), a_type, m, weight.k, C.byref(weight.struct),
           C.byref(lora.struct), row_adapter.data_ptr(), out.data_ptr(), out_type, weight.n, 1 if exact else 0,
           ws.data_ptr(), ws.numel())
@@ -517,12 +531,12 @@ def beam_select(logits, cum, n_cand, finished=None, eos=0, scores=None, parents=
               (scores, "scores", f32, (G, n_cand)), (parents, "parents", i32, (G, n_cand)),
               (tokens, "tokens", i32, (G, n_cand))])
     if scores is None:
-        scores = torch.empty((G, n_cand), dtype=torch.float32, device=dev)
+        scores = _empty((G, n_cand), torch.float32, dev, stream)
     if parents is None:
-        parents = torch.empty((G, n_cand), dtype=torch.int32, device=dev)
+        parents = _empty((G, n_cand), torch.int32, dev, stream)
     if tokens is None:
-        tokens = torch.empty((G, n_cand), dtype=torch.int32, device=dev)
-    ws = _workspace(ws, 0 if ws is not None else beam_select_workspace_bytes(G, K, V, n_cand), dev)
+        tokens = _empty((G, n_cand), torch.int32, dev, stream)
+    ws = _workspace(ws, 0 if ws is not None else beam_select_workspace_bytes(G, K, V, n_cand), dev, stream)
     _call(dev, stream, lib.nhm_beam_select, logits.data_ptr(), NHM_F32 if logits.dtype == torch.float32 else NHM_BF16, V,
           G, K, V, cum.data_ptr(), None if finished is None else finished.data_ptr(), int(eos), n_cand,
           scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), ws.data_ptr(), ws.numel())
@@ -551,7 +565,7 @@ def beam_reorder(parents, slots, ssm_pools, conv_pools, new_slots=None, g=GEOMET
     i32, shape = (torch.int32,), tuple(parents.shape)
     _on(dev, [(parents, "parents", i32, None), (slots, "slots", i32, shape), (new_slots, "new_slots", i32, shape)])
     if new_slots is None:
-        new_slots = torch.empty_like(slots)
+        new_slots = _empty(shape, torch.int32, dev, stream)
     arr = (_StatePool * len(ssm_pools))(*[(sp.data_ptr(), cp.data_ptr()) for sp, cp in zip(ssm_pools, conv_pools)])
     _call(dev, stream, lib.nhm_beam_reorder, C.byref(geom), parents.data_ptr(), slots.data_ptr(), shape[0], shape[1], arr,
           len(arr), st, S, new_slots.data_ptr())
