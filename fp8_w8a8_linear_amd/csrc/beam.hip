@@ -382,6 +382,7 @@ __global__ __launch_bounds__(kStripWaves * 64, F32 ? 3 : 4) void beam_strip_kern
 // bar for the others; what reaches it collects and is merged as in the strips, and once none of the
 // last entries read does, the rest of the lists is left.
 constexpr int kPickWaves = 8, kPlaces = 8;
+constexpr int64_t kPickGroups = int64_t(1) << 22;   // groups per launch: a launch holds fewer than 2^32 threads
 
 __global__ __launch_bounds__(kPickWaves * 64) void beam_pick_kernel(const BeamArgs g) {
     __shared__ double s_lse[32];                    // each beam's log(sum exp(x - top)) (finished: not used)
@@ -540,7 +541,20 @@ nhm_status launch_beam_select(BeamArgs g, void* ws, hipStream_t st) {
     count_launch(Kern::kBeamRows, rows);
     nhm_status s = check_launch("beam strips");
     if (s != NHM_OK) return s;
-    beam_pick_kernel<<<dim3((unsigned)g.n_groups), dim3(kPickWaves * 64), 0, st>>>(g);
+    for (int64_t g0 = 0; g0 < g.n_groups; g0 += kPickGroups) {
+        BeamArgs p = g;
+        const int64_t row0 = g0 * g.n_beams, id0 = row0 * g.n_strips;
+        p.cum += row0;
+        if (p.finished) p.finished += row0;
+        p.strip_keys += id0 * g.n_cand;
+        p.strip_sum += id0;
+        p.strip_top += id0;
+        p.scores += g0 * g.n_cand;
+        p.parents += g0 * g.n_cand;
+        p.tokens += g0 * g.n_cand;
+        const int64_t ng = g.n_groups - g0 < kPickGroups ? g.n_groups - g0 : kPickGroups;
+        beam_pick_kernel<<<dim3((unsigned)ng), dim3(kPickWaves * 64), 0, st>>>(p);
+    }
     count_launch(Kern::kBeamPick, g.n_groups);
     return check_launch("beam pick");
 }
