@@ -223,7 +223,7 @@ nhm_status nhm_mixer_prefill_lora(const nhm_mixer_params* p, const nhm_lora* lor
 
 size_t nhm_beam_select_workspace_bytes(int64_t n_groups, int32_t n_beams, int64_t vocab, int32_t n_cand) {
     if (n_groups <= 0 || n_beams < 1 || n_beams > kMaxBeams || vocab < 1 || vocab > kMaxVocab || n_cand < 1 ||
-        n_cand > kMaxCand || n_groups > kMaxRows / n_beams)
+        n_cand > kMaxCand || n_groups > (kMaxRows - 1) / n_beams)
         return 0;
     return beam_ws_bytes(n_groups * n_beams, vocab, n_cand);
 }
@@ -236,9 +236,9 @@ nhm_status nhm_beam_select(const void* logits, nhm_dtype type, int64_t ld, int64
     if (n_groups < 0 || vocab < 1 || n_cand < 1 || n_beams < 1 || ld < vocab)
         return fail(NHM_ERR_SHAPE, "groups %lld, beams %d, vocab %lld (ld %lld), candidates %d out of range",
                     (long long)n_groups, n_beams, (long long)vocab, (long long)ld, n_cand);
-    if (n_beams > kMaxBeams || n_cand > kMaxCand || vocab > kMaxVocab || n_groups > kMaxRows / n_beams)
-        return fail(NHM_ERR_UNSUPPORTED, "at most %d beams, %d candidates, a vocabulary of 2^24 and 2^24 rows", kMaxBeams,
-                    kMaxCand);
+    if (n_beams > kMaxBeams || n_cand > kMaxCand || vocab > kMaxVocab || n_groups > (kMaxRows - 1) / n_beams)
+        return fail(NHM_ERR_UNSUPPORTED, "at most %d beams, %d candidates, a vocabulary of 2^24 and fewer than 2^24 rows",
+                    kMaxBeams, kMaxCand);
     if (n_groups == 0) return NHM_OK;
     if (!logits || !cum || !scores || !parents || !tokens)
         return fail(NHM_ERR_NULL, "logits, cum, scores, parents or tokens is NULL");

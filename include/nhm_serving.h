@@ -132,7 +132,7 @@ typedef struct nhm_state_pool {
  *              read nor written
  *   pools      (host) [n_layers] device pointers, 1 .. 64 layers
  *   new_slots  (device) int32 [n_groups, n_beams]; must not overlap parents or slots
- * Limits: n_beams 1 .. 32. n_groups == 0 is a valid no-op.
+ * Limits: n_beams 1 .. 32, n_groups * n_beams <= 2^24. n_groups == 0 is a valid no-op.
  * Errors: NHM_ERR_NULL, NHM_ERR_SHAPE, NHM_ERR_ALIGN, NHM_ERR_UNSUPPORTED, NHM_ERR_HIP. */
 NHM_API nhm_status nhm_beam_reorder(const nhm_geometry* g, const int32_t* parents, const int32_t* slots,
                                     int64_t n_groups, int32_t n_beams, const nhm_state_pool* pools, int32_t n_layers,

@@ -193,3 +193,19 @@ def test_validation_under_asan_ubsan(tmp_path):
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1", UBSAN_OPTIONS="print_stacktrace=1")
     r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=120)
     assert r.returncode == 0 and "serving validation ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_limits_are_the_documented_ones(nhm):
+    """n_groups * n_beams below 2^24 for a selection, up to 2^24 for a reorder."""
+    size = nhm.lib.nhm_beam_select_workspace_bytes
+    assert size(1 << 24, 1, 10, 1) == 0 and size((1 << 24) - 1, 1, 10, 1) > 0
+    assert size(1 << 22, 4, 10, 1) == 0 and size((1 << 22) - 1, 4, 10, 1) > 0
+    assert size(1 << 19, 32, 10, 1) == 0 and size(((1 << 24) - 1) // 32, 32, 10, 1) > 0
+    X, CU, SC, PA, TO, WS = [0x10000 * i for i in range(1, 7)]
+    for G, K in [(1 << 24, 1), (1 << 22, 4), (1 << 19, 32)]:
+        st = nhm.lib.nhm_beam_select(X, nhm.NHM_F32, 10, G, K, 10, CU, None, 0, 1, SC, PA, TO, WS, 1 << 60, None)
+        assert st == 4, (G, K, nhm.lib.nhm_last_error())
+    geo = nhm.Geometry(**nhm.GEOMETRY)
+    pool = (nhm._StatePool * 1)((X, X))
+    for G, K in [((1 << 24) + 1, 1), ((1 << 22) + 1, 4)]:
+        assert nhm.lib.nhm_beam_reorder(C.byref(geo), PA, SC, G, K, pool, 1, nhm.NHM_F32, 16, TO, None) == 4
