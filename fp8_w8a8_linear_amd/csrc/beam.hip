@@ -149,13 +149,6 @@ __device__ __forceinline__ void merge64(T& list, const T& sorted, int lane) {
     halve<64, 32>(list, lane);
 }
 
-// Between a wave's LDS writes and its reads of other lanes' entries: LDS serves a wave's accesses
-// in order, this keeps the compiler from moving them past each other.
-__device__ __forceinline__ void wave_lds_order() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 __device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }

@@ -610,11 +610,13 @@ __global__ __launch_bounds__((kLoraMain + kLoraSide) * 64) void lora_rows_kernel
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         *reinterpret_cast<uint4*>(tb + (16 * i + 8 * h + lr) * 128 + slot * 16) = v[u][i][h];
+                wave_lds_order();
                 fetch(k0 + u + D, v[u]);
                 v8i op[TN + TM];            // as the panel kernel's: k bytes [16 q, 16 q + 16) and [64 + 16 q, 80 + 16 q)
 #pragma unroll
                 for (int i = 0; i < TN + TM; ++i)
                     op[i] = cat8(lds16(tb + swz128(16 * i + r16, q)), lds16(tb + swz128(16 * i + r16, q + 4)));
+                wave_lds_order();
 #pragma unroll
                 for (int i = 0; i < TN; ++i)
 #pragma unroll

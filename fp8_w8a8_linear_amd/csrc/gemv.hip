@@ -252,12 +252,14 @@ __global__ __launch_bounds__((kWaves + gemv_side(kLora, kWaves)) * 64) void gemv
                 *reinterpret_cast<uint4*>(tb + (16 * t + 8 + lr) * 128 + slot * 16) =
                     make_uint4(wa[i][t][4], wa[i][t][5], wa[i][t][6], wa[i][t][7]);
             }
+            wave_lds_order();
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
                 const uint4 w0 = *reinterpret_cast<const uint4*>(tb + swz128(16 * t + col, 2 * (lane >> 4)));
                 const uint4 w1 = *reinterpret_cast<const uint4*>(tb + swz128(16 * t + col, 2 * (lane >> 4) + 1));
                 wa[i][t] = v8i{(int)w0.x, (int)w0.y, (int)w0.z, (int)w0.w, (int)w1.x, (int)w1.y, (int)w1.z, (int)w1.w};
             }
+            wave_lds_order();
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

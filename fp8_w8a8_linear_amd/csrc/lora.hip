@@ -235,6 +235,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const L
                 }
 #pragma unroll
                 for (int v = 0; v < 2 * NR; ++v) *reinterpret_cast<v4u*>(ta + (8 * v + lr) * 128 + slot * 16) = o.a[v];
+                wave_lds_order();
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     bf16x8 xf[kManyRows], af[NR];
@@ -249,6 +250,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void lora_down_many_kernel(const L
 #pragma unroll
                         for (int j = 0; j < NR; ++j) acc[i][j] = mfma_bf16(af[j], xf[i], acc[i][j]);
                 }
+                wave_lds_order();
             }
         };
         Ops o0, o1;

@@ -225,4 +225,11 @@ __device__ __forceinline__ void wait_vmcnt() {
 // parities sit 64 bytes apart, and bit 3 of the row flips the slot's lowest bit).
 __device__ __forceinline__ int swz128(int row, int c) { return row * 128 + ((c ^ (row & 7) ^ ((row >> 3) & 1)) << 4); }
 
+// Between a wave's LDS writes and its reads of other lanes' entries, and back: LDS serves a wave's
+// accesses in order, this keeps the compiler from moving them past each other (no instruction).
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 }  // namespace nhm
