@@ -1330,6 +1330,11 @@ static void launch_panel(GemmArgs g, hipStream_t st) {
 // 160 of its tiles (m = 1024 for in_proj, m = 4096 for out_proj: 45 vs 54 us and
 // 60 vs 74 us; at m = 15,360 477 vs 652 us and 187 vs 253 us) and trails below
 // (123 tiles at m = 641: 43 vs 36 us).
+constexpr int64_t kRingTiles = 160;   // workgroups from which a ring tile leads
+static int64_t tiles_256x128(int64_t m, int64_t n) { return ((n + kWT - 1) / kWT) * ((m + 127) / 128); }
+static int64_t tiles_192x128(int64_t m, int64_t n) { return ((n + 191) / 192) * ((m + 127) / 128); }
+static bool ring_fills(int64_t m, int64_t n) { return tiles_256x128(m, n) >= kRingTiles || tiles_192x128(m, n) >= kRingTiles; }
+
 // Split k for m <= 640 where the ring tiles are too few to fill the chip (the panel kernel's
 // case): the 192 x 128 ring tile over S k ranges puts fewer operand bytes on the busiest CU
 // than a 64 x 128 panel over all of k, at the price of the f32 partials and the reduction.
@@ -1342,9 +1347,8 @@ static void launch_panel(GemmArgs g, hipStream_t st) {
 // (7/8 of the chip idle). Returns the S that minimises the estimate there, else 1.
 static int split_k(int64_t m, int64_t n, int64_t k) {
     if (m > 640 || m <= 0 || n <= 0 || k <= 0) return 1;
-    const int64_t half_tiles = ((n + kWT - 1) / kWT) * ((m + 127) / 128);
-    const int64_t t192 = ((n + 191) / 192) * ((m + 127) / 128);
-    if (half_tiles >= 160 || t192 >= 160) return 1;
+    const int64_t t192 = tiles_192x128(m, n);
+    if (ring_fills(m, n)) return 1;
     constexpr int64_t kSK = 128;   // k bytes per stage of the split kernel (ring128_kernel)
     const int64_t nk = (k + kSK - 1) / kSK;
     const int64_t panel_wgs = 8 * ((m + 63) / 64) * (((n + 127) / 128 + 7) / 8);
@@ -1366,19 +1370,20 @@ size_t gemm_part_bytes(int64_t m, int64_t n, int64_t k) {
     return S > 1 ? (size_t)S * (size_t)m * (size_t)n * sizeof(float) : 0;
 }
 
+// Buffer descriptors address the operands with 32-bit offsets.
+static bool offsets_fit(const GemmArgs& g) { return g.n * g.k < (int64_t(1) << 31) && g.m * g.lda < (int64_t(1) << 31); }
+
 template <bool kExact, int kLora>
 static nhm_status dispatch_gemm(GemmArgs g, hipStream_t st, float* part, size_t part_bytes) {
-    const int64_t m = g.m, n = g.n, k = g.k, lda = g.lda;
-    // buffer descriptors address the operands with 32-bit offsets
-    const bool offsets_fit = n * k < (int64_t(1) << 31) && m * lda < (int64_t(1) << 31);
-    // m <= 640: a ring tile when it gives >= 160 workgroups; of 256 x 128 and 192 x 128 the one
+    const int64_t m = g.m, n = g.n, k = g.k;
+    const bool fit = offsets_fit(g);
+    // m <= 640: a ring tile when it gives kRingTiles workgroups; of 256 x 128 and 192 x 128 the one
     // whose busiest CU pulls the fewest operand bytes, (workgroups per CU) x (tile n + tile m) x k
     // (each CU's delivery rate is bounded by the requests it keeps in flight)
-    const int64_t half_tiles = ((n + kWT - 1) / kWT) * ((m + 127) / 128);
-    const int64_t t192 = ((n + 191) / 192) * ((m + 127) / 128);
-    if (m <= 640 && offsets_fit && (half_tiles >= 160 || t192 >= 160)) {
-        const int64_t c256 = half_tiles >= 160 ? ((half_tiles + 255) / 256) * (256 + 128) : INT64_MAX;
-        const int64_t c192 = t192 >= 160 ? ((t192 + 255) / 256) * (192 + 128) : INT64_MAX;
+    const int64_t half_tiles = tiles_256x128(m, n), t192 = tiles_192x128(m, n);
+    if (m <= 640 && fit && ring_fills(m, n)) {
+        const int64_t c256 = half_tiles >= kRingTiles ? ((half_tiles + 255) / 256) * (256 + 128) : INT64_MAX;
+        const int64_t c192 = t192 >= kRingTiles ? ((t192 + 255) / 256) * (192 + 128) : INT64_MAX;
         if (c192 < c256) {
             ring128_kernel<192, 128, kExact, kLora><<<dim3((unsigned)t192), dim3(512), 0, st>>>(g);
             count_launch(kExact ? Kern::kRing192x128Exact : Kern::kRing192x128, m);
@@ -1388,7 +1393,7 @@ static nhm_status dispatch_gemm(GemmArgs g, hipStream_t st, float* part, size_t 
         count_launch(kExact ? Kern::kRing256x128Exact : Kern::kRing256x128, m);
         return check_launch("gemm (256 x 128)");
     }
-    if (m <= 640 && offsets_fit) {   // too few ring tiles to fill the chip
+    if (m <= 640 && fit) {   // too few ring tiles to fill the chip
         if constexpr (kLora == 0) {
             const int S = split_k(m, n, k);
             if (S > 1 && part && part_bytes >= gemm_part_bytes(m, n, k) && (reinterpret_cast<uintptr_t>(part) & 15) == 0) {
@@ -1407,12 +1412,12 @@ static nhm_status dispatch_gemm(GemmArgs g, hipStream_t st, float* part, size_t 
         return check_launch("gemm (panel)");
     }
     const int64_t wide_tiles = ((n + kWT - 1) / kWT) * ((m + kWT - 1) / kWT);
-    if (offsets_fit && wide_tiles >= 160) {
+    if (fit && wide_tiles >= kRingTiles) {
         tile256_kernel<256, 256, kExact, kLora><<<dim3((unsigned)wide_tiles), dim3(512), 0, st>>>(g);
         count_launch(kExact ? Kern::kRing256x256Exact : Kern::kRing256x256, m);
         return check_launch("gemm (256 x 256)");
     }
-    if (!offsets_fit)   // refused by the callers' host checks before anything is enqueued
+    if (!fit)   // refused by the callers' host checks before anything is enqueued
         return fail(NHM_ERR_UNSUPPORTED, "gemm: an operand of 2 GiB or more");
     const dim3 grid((unsigned)((n + kTile - 1) / kTile), (unsigned)((m + kTile - 1) / kTile));
     gemm_kernel<kExact, kLora><<<grid, dim3(256), 0, st>>>(g);
@@ -1438,10 +1443,8 @@ nhm_status launch_gemm(const uint8_t* a, int64_t lda, int64_t m, const uint8_t* 
 // 256 x 2,688 x 4,096 27 and 27; past it, 32 adapters and one: 100 x 10,304 x 2,688 41 and 48, 35 and 29, 64 x
 // 30,000 x 1,024 43 and 38, 27 and 19, 500 x 2,688 x 4,096 63 and 67, 43 and 32).
 static bool lora_rows_serve(const GemmArgs& g) {
-    constexpr int64_t k2G = int64_t(1) << 31;
     const int64_t nmt = (g.m + 63) / 64;
-    return g.m <= 640 && (g.n + 191) / 192 * ((g.m + 127) / 128) < 160 && g.n * g.k < k2G && g.m * g.lda < k2G &&
-           (g.n + 47) / 48 * nmt <= 256;
+    return g.m <= 640 && offsets_fit(g) && !ring_fills(g.m, g.n) && (g.n + 47) / 48 * nmt <= 256;
 }
 
 // As many features per workgroup as keep the bytes on the busiest CU, (rounds of 256 workgroups) x (rows +

@@ -9,7 +9,7 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-bool rank_ok(int32_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
+bool rank_ok(int32_t rank) { return rank >= 8 && rank <= kLoraMaxRank && rank % 8 == 0; }
 
 // Regions of the adapter call's workspace: the activation codes of a bf16 input, the low-rank product.
 struct LoraWs { size_t t, total; };
