@@ -165,6 +165,7 @@ struct GnormArgs {
     const int32_t* slot_idx = nullptr;
     uint16_t* conv_pool = nullptr;   // [S, W-1, conv_dim]
     int32_t conv_dim = 0, xbc_off = 0, b_off = 0, c_off = 0, d_state = 0;
+    const int32_t* n_real = nullptr;   // prefill: tokens of all sequences (device); zeros from there to T
 };
 nhm_status launch_gnorm_quant(const GnormArgs& a, hipStream_t st);
 

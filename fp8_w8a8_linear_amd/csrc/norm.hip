@@ -24,6 +24,8 @@ __global__ __launch_bounds__(256) void gnorm_quant_kernel(const GnormArgs a) {
     const uint16_t* yr = a.y + tok * a.d_inner + (int64_t)g * gw;
     const uint16_t* zr = a.zxbcdt + tok * a.d_in_proj + a.z_off + (int64_t)g * gw;
     const float so = *a.out_a_scale;
+    // prefill: rows behind the last sequence have no y; their norm is zero
+    const bool real = !a.n_real || tok < *a.n_real;
     // decode: this token's slot's conv windows of group g's B (lanes 0-31) and C (32-63)
     // channels, four per lane, shifted by one row (the decode state kernel, which reads them,
     // has finished; the x channels' windows it shifts itself). Loads go out with y and z.
@@ -77,7 +79,7 @@ __global__ __launch_bounds__(256) void gnorm_quant_kernel(const GnormArgs a) {
             float y[8], z[8];
             unpack8(yv[it], y);
             unpack8(zv[it], z);
-            const bool in = lane * 8 + it * 512 < gw;
+            const bool in = real && lane * 8 + it * 512 < gw;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[it][j] = in ? y[j] * silu(z[j]) : 0.f;
@@ -98,7 +100,7 @@ __global__ __launch_bounds__(256) void gnorm_quant_kernel(const GnormArgs a) {
             unpack8(*reinterpret_cast<const uint4*>(zr + c), z);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float v = y[j] * silu(z[j]);
+                const float v = real ? y[j] * silu(z[j]) : 0.f;
                 ss += v * v;
             }
         }
@@ -109,7 +111,7 @@ __global__ __launch_bounds__(256) void gnorm_quant_kernel(const GnormArgs a) {
             unpack8(*reinterpret_cast<const uint4*>(yr + c), y);
             unpack8(*reinterpret_cast<const uint4*>(zr + c), z);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = y[j] * silu(z[j]);
+            for (int j = 0; j < 8; ++j) v[j] = real ? y[j] * silu(z[j]) : 0.f;
             emit(c, v, r, *reinterpret_cast<const uint4*>(a.norm_w + (int64_t)g * gw + c));
         }
     }

@@ -265,6 +265,7 @@ nhm_status launch_prefill_mid(const PrefillArgs& a, hipStream_t st) {
     if (s != NHM_OK || a.T == 0) return s;
     GnormArgs ga{a.T, a.n_groups, a.d_inner, a.d_in_proj, a.z_off, a.eps, a.y, a.zxbcdt, a.norm_w, a.out_a_scale,
                  a.norm, a.q_out};
+    ga.n_real = a.cu_seqlens + a.n_seqs;
     return launch_gnorm_quant(ga, st);
 }
 

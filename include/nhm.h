@@ -357,7 +357,9 @@ NHM_API nhm_status nhm_mixer_prefill_ws_layout(const nhm_geometry* g, int64_t n_
  * chunks of `chunk` tokens that start at each sequence's first token.
  *   hidden      (device) bf16 [n_tokens, g.hidden]
  *   cu_seqlens  (device) int32 [n_seqs+1]. Contract: cu_seqlens[0] == 0,
- *               non-decreasing, cu_seqlens[n_seqs] == n_tokens.
+ *               non-decreasing, cu_seqlens[n_seqs] <= n_tokens. Rows behind the last
+ *               sequence (a padded batch) belong to none: whatever hidden holds there,
+ *               their output rows are zero and no state depends on them.
  *   slot_idx    (device) int32 [n_seqs]. Contract: distinct, in [0, n_slots).
  *   has_initial (device) int32 [n_seqs]: 0 starts sequence i from zero SSM state and
  *               a zero conv window; non-zero continues from pool row slot_idx[i].

@@ -63,8 +63,8 @@ NHM_API nhm_status nhm_fp8_linear_lora(const void* a, nhm_dtype a_type, int64_t 
  * [batch] or [n_tokens] as for nhm_fp8_linear_lora (nhm_batch_plan's token_adapter is one), the same
  * for both sets, which may differ in rank and number. in_proj sums every product in f32, out_proj as in
  * the calls without adapters; where those split out_proj over k, these do not.
- * A padded decode row (negative slot) has a zero norm output, so its output stays zero with any
- * finite adapter. ws: the layout calls below, with the larger rank of the two sets.
+ * A padded decode row (negative slot) and a prefill row behind the last sequence have a zero norm output, so
+ * their output stays zero with any finite adapter. ws: the layout calls below, with the larger rank of the two sets.
  * Errors: those of the calls without adapters and of nhm_fp8_linear_lora. */
 NHM_API nhm_status nhm_mixer_decode_lora_ws_layout(const nhm_geometry* g, int32_t batch, int32_t rank,
                                                    nhm_ws_layout* out);
