@@ -24,8 +24,9 @@ __global__ __launch_bounds__(256) void gnorm_quant_kernel(const GnormArgs a) {
     const uint16_t* yr = a.y + tok * a.d_inner + (int64_t)g * gw;
     const uint16_t* zr = a.zxbcdt + tok * a.d_in_proj + a.z_off + (int64_t)g * gw;
     const float so = *a.out_a_scale;
-    // prefill: rows behind the last sequence have no y; their norm is zero
-    const bool real = !a.n_real || tok < *a.n_real;
+    // prefill: rows behind the last sequence have no y; their norm is zero. The count is loaded like the scale,
+    // without a branch that would wait for it ahead of the loads below.
+    const int n_real = *(a.n_real ? a.n_real : reinterpret_cast<const int32_t*>(a.out_a_scale));
     // decode: this token's slot's conv windows of group g's B (lanes 0-31) and C (32-63)
     // channels, four per lane, shifted by one row (the decode state kernel, which reads them,
     // has finished; the x channels' windows it shifts itself). Loads go out with y and z.
@@ -74,6 +75,7 @@ __global__ __launch_bounds__(256) void gnorm_quant_kernel(const GnormArgs a) {
         }
         // the scale's scalar load goes out with them, not after the reduction
         asm volatile("" ::"s"(so) : "memory");
+        const bool real = !a.n_real || tok < n_real;
 #pragma unroll
         for (int it = 0; it < kIt; ++it) {
             float y[8], z[8];
@@ -94,6 +96,7 @@ __global__ __launch_bounds__(256) void gnorm_quant_kernel(const GnormArgs a) {
             if (c < gw) emit(c, v[it], r, wv[it]);
         }
     } else {
+        const bool real = !a.n_real || tok < n_real;
         for (int c = lane * 8; c < gw; c += 64 * 8) {
             float y[8], z[8];
             unpack8(*reinterpret_cast<const uint4*>(yr + c), y);
