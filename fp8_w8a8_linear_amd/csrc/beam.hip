@@ -13,8 +13,9 @@ namespace nhm {
 // scores is the order of the logits, so one pass over the logits is enough: a wave walks a strip
 // of a row and keeps, beside the running maximum and sum of the softmax, the strip's n_cand
 // largest logits. A second kernel joins each row's strips into its lse and picks each group's best
-// from the strips' lists. The pass is bound by the logits' bytes: 512 rows of 131,072 bf16 logits, 134 MB, take 32 us
-// (4.2 TB/s) and the picking 11 us, a chain of latencies (64 workgroups; one alone takes 6.6 us).
+// from the strips' lists. The pass is bound by bytes: 512 rows of 131,072 bf16 logits take 32 us, in which
+// memory hands over 167 MB (5.2 TB/s): the logits' 134 MB and the lines of the cells that are read again. The picking
+// takes 11 us, a chain of latencies (64 workgroups; one alone takes 6.6 us).
 //
 // A lane's share of a 2,048-logit piece is a cell of 32; the pass keeps each cell's maximum in LDS.
 // After a span of 8 pieces the n_cand-th largest of the 64 lanes' maxima is a bar that at least

@@ -498,9 +498,10 @@ __global__ __launch_bounds__(256) void panel_kernel(const GemmArgs g) {
 // its waves have two trades: kLoraMain multiply, 16 rows each, and kLoraSide others form t B_e^T at the same
 // time, the adapters shared out among them. A lane of those keeps the product of its own row's adapter only, so
 // all but one of the side waves hold zeros for an output, and their sum, taken in LDS in wave order, is
-// exact. Bound by the operand bytes a CU is handed, 64 rows and each multiplying wave's 16 TN features: loads
+// exact. Bound by the operand bytes a CU is handed, 64 rows and each multiplying wave's 16 TN features (those 61 rows:
+// 512 KB asked for, 380 KB of them from L2, in 12.3 us): loads
 // take whole lines, and a wave-private piece of LDS turns them into operands without a barrier. Those 61 rows,
-// us with the low-rank product: this 19.8; with two multiplying waves of 32 rows 21.5, of those with six or eight
+// us with the low-rank product: this 17.9 to 19.8; with two multiplying waves of 32 rows 21.5, of those with six or eight
 // steps in flight for four 22.3, 23.5, with loads in operand order, 64 bytes of a row at a time, 25.0; the panel
 // kernel 51 (21 without adapters).
 constexpr int kLoraMain = 4, kLoraSide = 8;
