@@ -16,7 +16,10 @@ __all__ = ["lib", "LIB_PATH", "NhmError", "Geometry", "Layout", "WsLayout", "Fp8
            "NHM_F32", "fp8_dequant_channel_bf16", "mixer_decode_noalloc", "mixer_decode_q",
            "dispatch_counters", "Lora", "fp8_linear_lora", "fp8_linear_lora_workspace_bytes", "beam_select",
            "beam_select_workspace_bytes", "beam_reorder", "BatchPlan", "batch_plan", "mixer_decode_lora",
-           "mixer_prefill_lora", "decode_lora_ws_layout", "prefill_lora_ws_layout"]
+           "mixer_prefill_lora", "decode_lora_ws_layout", "prefill_lora_ws_layout", "NHM_MXFP4", "Mxfp4Weight",
+           "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_linear_workspace_bytes", "causal_conv_decode",
+           "causal_conv_prefill", "ScanParams", "selective_scan_decode", "selective_scan_prefill",
+           "selective_scan_prefill_workspace_bytes", "token_logprobs", "token_logprobs_workspace_bytes"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnhm.so")
 if not os.path.exists(LIB_PATH):
@@ -24,7 +27,7 @@ if not os.path.exists(LIB_PATH):
                       "(or __graft_entry__.build()); this package has no non-HIP fallback")
 lib = C.CDLL(LIB_PATH)
 
-NHM_BF16, NHM_E4M3, NHM_F32 = 0, 1, 2
+NHM_BF16, NHM_E4M3, NHM_F32, NHM_MXFP4 = 0, 1, 2, 3
 _STATUS = {0: "NHM_OK", 1: "NHM_ERR_NULL", 2: "NHM_ERR_SHAPE", 3: "NHM_ERR_ALIGN", 4: "NHM_ERR_UNSUPPORTED",
            5: "NHM_ERR_WORKSPACE", 6: "NHM_ERR_HIP"}
 
@@ -74,6 +77,15 @@ class _StatePool(C.Structure):
     _fields_ = [("ssm", C.c_void_p), ("conv", C.c_void_p)]
 
 
+class _Mxfp4Weight(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("scale", C.c_void_p), ("n", C.c_int64), ("k", C.c_int64)]
+
+
+class _ScanParams(C.Structure):
+    _fields_ = [("A_log", C.c_void_p), ("D", C.c_void_p), ("dt_bias", C.c_void_p), ("dim", C.c_int32),
+                ("d_state", C.c_int32)]
+
+
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
 _SIGS = {
     "nhm_status_str": (C.c_char_p, [C.c_int]),
@@ -114,6 +126,20 @@ _SIGS = {
     "nhm_beam_reorder": (C.c_int, [C.POINTER(Geometry), _p, _p, _i64, _i32, C.POINTER(_StatePool), _i32, C.c_int, _i32,
                                    _p, _p]),
     "nhm_batch_plan": (C.c_int, [_p, _p, _p, _i32, _i64, _p, _p, _p, _p, _p, _p]),
+    "nhm_mxfp4_quantize": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p]),
+    "nhm_mxfp4_dequantize": (C.c_int, [_p, _i64, _p, _i64, _i64, _i64, _p, _i64, _p]),
+    "nhm_mxfp4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, C.c_int]),
+    "nhm_mxfp4_linear": (C.c_int, [_p, C.c_int, _p, _i64, _i64, C.POINTER(_Mxfp4Weight), _p, C.c_int, _i64, _p, _sz, _p]),
+    "nhm_causal_conv_decode": (C.c_int, [_p, _i64, _p, _p, _i32, _i32, _i32, _i32, _p, _p, _i32, _p, _i64, _p]),
+    "nhm_causal_conv_prefill": (C.c_int, [_p, _i64, _i64, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p, _p, _i32, _p, _i64,
+                                          _p]),
+    "nhm_selective_scan_decode": (C.c_int, [C.POINTER(_ScanParams), _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i32,
+                                            _p, _p, C.c_int, _i32, _p, _i64, _p]),
+    "nhm_selective_scan_prefill_workspace_bytes": (_sz, [_i32, _i32, _i64, _i32]),
+    "nhm_selective_scan_prefill": (C.c_int, [C.POINTER(_ScanParams), _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64,
+                                             _p, _i32, _p, _p, _p, C.c_int, _i32, _p, _i64, _p, _sz, _p]),
+    "nhm_token_logprobs_workspace_bytes": (_sz, [_i64, _i64, _i32]),
+    "nhm_token_logprobs": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i32, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -597,3 +623,264 @@ def batch_plan(lengths, plan: BatchPlan, past=None, adapters=None, stream=None):
           plan.cu_seqlens.data_ptr(), plan.has_initial.data_ptr(), plan.token_seq.data_ptr(), plan.token_pos.data_ptr(),
           plan.token_adapter.data_ptr())
     return plan
+
+
+# ---- operators of a selective-scan layer in 4 bits (include/nhm_layer.h)
+
+def _row_view(t, name, dev, dtypes, rows, cols):
+    """Checks a [rows, cols] tensor whose rows may be slices of wider ones; its row stride in elements."""
+    import torch
+    if isinstance(t, torch.Tensor) and t.get_device() == dev.index and t.dtype in dtypes and t.shape == (rows, cols):
+        ld, step = t.stride()
+        if rows == 0 or (rows == 1 and step == 1):
+            return cols
+        if step == 1 and ld >= cols:
+            return ld
+        raise ValueError(f"{name} of strides {t.stride()}: expected rows of consecutive elements")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    if t.get_device() != dev.index:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} of dtype {t.dtype}: expected {' or '.join(str(d) for d in dtypes)}")
+    raise ValueError(f"{name} of shape {tuple(t.shape)}: expected {(rows, cols)}")
+
+
+def _shape2(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} of shape {tuple(t.shape)}: expected two dimensions")
+    return int(t.shape[0]), int(t.shape[1])
+
+
+def _device_of(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    return t.device
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_ctypes_byref = C.byref          # the scans have an argument named C
+
+
+class Mxfp4Weight:
+    """One MXFP4 projection on the device: codes uint8 [n, k / 2] (two a byte, the lower index in the low four bits) and
+    scale codes uint8 [n, k / 32], as mxfp4_quantize makes them."""
+
+    def __init__(self, w, scale):
+        import torch
+        dev = _device_of(w, "w")
+        n, kb = _shape2(w, "w")
+        _on(dev, [(w, "w", (torch.uint8,), None), (scale, "scale", (torch.uint8,), (n, kb // 16))])
+        self.w, self.scale, self.n, self.k = w, scale, n, 2 * kb
+        self._s = _Mxfp4Weight(w.data_ptr(), scale.data_ptr(), n, 2 * kb)
+
+    @property
+    def struct(self):
+        return self._s
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """(codes uint8 [rows, cols / 2], scales uint8 [rows, cols / 32]) of x [rows, cols], bf16 (bits or bfloat16) or float32;
+    rows of x may be slices of wider ones."""
+    import torch
+    dev = _device_of(x, "x")
+    rows, cols = _shape2(x, "x")
+    u8 = (torch.uint8,)
+    ld = _row_view(x, "x", dev, _bf16_types() + (torch.float32,), rows, cols)
+    _on(dev, [(codes, "codes", u8, (rows, cols // 2)), (scales, "scales", u8, (rows, cols // 32))])
+    if codes is None:
+        codes = _empty((rows, cols // 2), torch.uint8, dev, stream)
+    if scales is None:
+        scales = _empty((rows, cols // 32), torch.uint8, dev, stream)
+    _call(dev, stream, lib.nhm_mxfp4_quantize, x.data_ptr(), NHM_F32 if x.dtype == torch.float32 else NHM_BF16, rows, cols, ld,
+          codes.data_ptr(), cols // 2, scales.data_ptr(), cols // 32)
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, out=None, stream=None):
+    """bf16 [rows, cols] (bits, int16, unless out is given): the values of mxfp4_quantize's codes and scales, exact."""
+    import torch
+    dev = _device_of(codes, "codes")
+    rows, half = _shape2(codes, "codes")
+    u8 = (torch.uint8,)
+    _on(dev, [(codes, "codes", u8, None), (scales, "scales", u8, (rows, half // 16)),
+              (out, "out", _bf16_types(), (rows, 2 * half))])
+    if out is None:
+        out = _empty((rows, 2 * half), torch.int16, dev, stream)
+    _call(dev, stream, lib.nhm_mxfp4_dequantize, codes.data_ptr(), half, scales.data_ptr(), half // 16, rows, 2 * half,
+          out.data_ptr(), 2 * half)
+    return out
+
+
+def mxfp4_linear_workspace_bytes(m, n, k, a_type):
+    return int(lib.nhm_mxfp4_linear_workspace_bytes(m, n, k, a_type))
+
+
+def mxfp4_linear(a, weight: Mxfp4Weight, a_scale=None, out=None, ws=None, out_type=None, stream=None):
+    """[m, n] = a [m, k] times an MXFP4 weight. a: bf16 (bits or bfloat16), quantized within the call, or codes
+    (uint8 [m, k / 2]) with their scale codes a_scale (uint8 [m, k / 32]). Rows of a may be slices of wider ones.
+
+    The output is bf16 bits (int16) unless out_type is NHM_F32 (or out is a float32 tensor)."""
+    import torch
+    dev = _device_of(a, "a")
+    m, n, k = _shape2(a, "a")[0], weight.n, weight.k
+    u8 = (torch.uint8,)
+    codes = a.dtype == torch.uint8
+    ld = _row_view(a, "a", dev, u8 if codes else _bf16_types(), m, k // 2 if codes else k)
+    if codes != (a_scale is not None):
+        raise ValueError("a_scale goes with codes, and codes with a_scale")
+    _on(dev, [(a_scale, "a_scale", u8, (m, k // 32)), (weight.w, "weight", u8, None)])
+    if out_type is None:
+        out_type = NHM_F32 if out is not None and out.dtype == torch.float32 else NHM_BF16
+    if out is None:
+        out = _empty((m, n), torch.float32 if out_type == NHM_F32 else torch.int16, dev, stream)
+        ld_out = n
+    else:
+        ld_out = _row_view(out, "out", dev, (torch.float32,) if out_type == NHM_F32 else _bf16_types(), m, n)
+    a_type = NHM_MXFP4 if codes else NHM_BF16
+    ws = _workspace(ws, 0 if ws is not None else mxfp4_linear_workspace_bytes(m, n, k, a_type), dev, stream)
+    _call(dev, stream, lib.nhm_mxfp4_linear, a.data_ptr(), a_type, _addr(a_scale), m, ld, C.byref(weight.struct),
+          out.data_ptr(), out_type, ld_out, ws.data_ptr(), ws.numel())
+    return out
+
+
+def _conv(x, conv_w, conv_b, slot_idx, conv_pool, out, stream, n_seqs, index):
+    """Checks a convolution's arguments: (device, rows, dim, width, ld_x, out, ld_out)."""
+    import torch
+    dev = _device_of(x, "x")
+    rows, dim = _shape2(x, "x")
+    bf, i32 = _bf16_types(), (torch.int32,)
+    width = _shape2(conv_w, "conv_w")[1]
+    if conv_pool.dim() != 3:
+        raise ValueError(f"conv_pool of shape {tuple(conv_pool.shape)}: expected [slots, width - 1, dim]")
+    ld_x = _row_view(x, "x", dev, bf, rows, dim)
+    _on(dev, [(conv_w, "conv_w", bf, (dim, width)), (conv_b, "conv_b", bf, (dim,)), (slot_idx, "slot_idx", i32, (n_seqs,)),
+              (conv_pool, "conv_pool", bf, (conv_pool.shape[0], width - 1, dim))] + [(t, n, i32, s) for t, n, s in index])
+    if out is None:
+        return dev, rows, dim, width, ld_x, _empty((rows, dim), torch.int16, dev, stream), dim
+    return dev, rows, dim, width, ld_x, out, _row_view(out, "out", dev, bf, rows, dim)
+
+
+def causal_conv_decode(x, conv_w, conv_b, slot_idx, conv_pool, out=None, silu=True, stream=None):
+    """The short causal convolution of one token per sequence: x bf16 [batch, dim] (rows may be slices of wider ones),
+    conv_w bf16 [dim, width], conv_b bf16 [dim] or None, slot_idx int32 [batch] (outside the pool: padding, zero rows),
+    conv_pool bf16 [slots, width - 1, dim], updated in place. The output is bf16 bits (int16) unless out is given."""
+    dev, rows, dim, width, ld, out, ld_out = _conv(x, conv_w, conv_b, slot_idx, conv_pool, out, stream, x.shape[0], ())
+    _call(dev, stream, lib.nhm_causal_conv_decode, x.data_ptr(), ld, conv_w.data_ptr(), _addr(conv_b), dim, width,
+          1 if silu else 0, rows, slot_idx.data_ptr(), conv_pool.data_ptr(), int(conv_pool.shape[0]), out.data_ptr(), ld_out)
+    return out
+
+
+def causal_conv_prefill(x, conv_w, conv_b, cu_seqlens, slot_idx, has_initial, conv_pool, out=None, silu=True, stream=None):
+    """causal_conv_decode over packed sequences: x bf16 [n_tokens, dim], cu_seqlens int32 [n_seqs + 1], slot_idx and
+    has_initial int32 [n_seqs] as mixer_prefill takes them. Rows behind the last sequence are zero."""
+    n = int(slot_idx.shape[0])
+    dev, rows, dim, width, ld, out, ld_out = _conv(x, conv_w, conv_b, slot_idx, conv_pool, out, stream, n,
+                                                   ((cu_seqlens, "cu_seqlens", (n + 1,)), (has_initial, "has_initial", (n,))))
+    _call(dev, stream, lib.nhm_causal_conv_prefill, x.data_ptr(), ld, rows, conv_w.data_ptr(), _addr(conv_b), dim, width,
+          1 if silu else 0, cu_seqlens.data_ptr(), n, slot_idx.data_ptr(), has_initial.data_ptr(), conv_pool.data_ptr(),
+          int(conv_pool.shape[0]), out.data_ptr(), ld_out)
+    return out
+
+
+class ScanParams:
+    """A selective scan's parameters on the device: A_log f32 [dim, d_state] (A = -exp(A_log)), D f32 [dim] or None (0),
+    dt_bias f32 [dim] or None (0)."""
+
+    def __init__(self, A_log, D=None, dt_bias=None):
+        import torch
+        dev, f32 = _device_of(A_log, "A_log"), (torch.float32,)
+        self.dim, self.d_state = _shape2(A_log, "A_log")
+        _on(dev, [(A_log, "A_log", f32, None), (D, "D", f32, (self.dim,)), (dt_bias, "dt_bias", f32, (self.dim,))])
+        self.A_log, self.D, self.dt_bias = A_log, D, dt_bias
+        self._s = _ScanParams(A_log.data_ptr(), _addr(D), _addr(dt_bias), self.dim, self.d_state)
+
+    @property
+    def struct(self):
+        return self._s
+
+
+def _scan(params, u, dt, B, C_, z, slot_idx, ssm_pool, out, stream, n_seqs, index):
+    """Checks a scan's arguments: (device, rows, the C arguments of u, dt, B, C and z, out, ld_out)."""
+    import torch
+    dev = _device_of(u, "u")
+    rows, dim, n = _shape2(u, "u")[0], params.dim, params.d_state
+    bf, i32 = _bf16_types(), (torch.int32,)
+    args = []
+    for t, name, cols in ((u, "u", dim), (dt, "dt", dim), (B, "B", n), (C_, "C", n), (z, "z", dim)):
+        args += [None, 0] if t is None and name == "z" else [t, _row_view(t, name, dev, bf, rows, cols)]
+    if ssm_pool.dim() != 3:
+        raise ValueError(f"ssm_pool of shape {tuple(ssm_pool.shape)}: expected [slots, dim, d_state]")
+    _on(dev, [(params.A_log, "params", (torch.float32,), None), (slot_idx, "slot_idx", i32, (n_seqs,)),
+              (ssm_pool, "ssm_pool", bf + (torch.float32,), (ssm_pool.shape[0], dim, n))] + [(t, m, i32, s) for t, m, s in index])
+    args = [_addr(a) if isinstance(a, torch.Tensor) else a for a in args]
+    if out is None:
+        return dev, rows, args, _empty((rows, dim), torch.int16, dev, stream), dim
+    return dev, rows, args, out, _row_view(out, "out", dev, bf, rows, dim)
+
+
+def selective_scan_decode(params: ScanParams, u, dt, B, C, slot_idx, ssm_pool, z=None, out=None, stream=None):
+    """The selective scan of one token per sequence: u, dt and z (or None) bf16 [batch, dim], B and C bf16 [batch, d_state]
+    (rows may be slices of wider ones), slot_idx int32 [batch] (outside the pool: padding, zero rows), ssm_pool float32 or bf16
+    [slots, dim, d_state], updated in place. The output is bf16 bits (int16) unless out is given."""
+    dev, rows, args, out, ld_out = _scan(params, u, dt, B, C, z, slot_idx, ssm_pool, out, stream, u.shape[0], ())
+    _call(dev, stream, lib.nhm_selective_scan_decode, _ctypes_byref(params.struct), *args, rows, slot_idx.data_ptr(), ssm_pool.data_ptr(),
+          _ssm_type(ssm_pool), int(ssm_pool.shape[0]), out.data_ptr(), ld_out)
+    return out
+
+
+def selective_scan_prefill_workspace_bytes(dim, d_state, n_tokens, n_seqs):
+    return int(lib.nhm_selective_scan_prefill_workspace_bytes(dim, d_state, n_tokens, n_seqs))
+
+
+def selective_scan_prefill(params: ScanParams, u, dt, B, C, cu_seqlens, slot_idx, has_initial, ssm_pool, z=None, out=None,
+                           ws=None, stream=None):
+    """selective_scan_decode over packed sequences: u, dt, z [n_tokens, dim], B, C [n_tokens, d_state], cu_seqlens int32
+    [n_seqs + 1], slot_idx and has_initial int32 [n_seqs] as mixer_prefill takes them. Rows behind the last sequence are zero."""
+    n = int(slot_idx.shape[0])
+    dev, rows, args, out, ld_out = _scan(params, u, dt, B, C, z, slot_idx, ssm_pool, out, stream, n,
+                                         ((cu_seqlens, "cu_seqlens", (n + 1,)), (has_initial, "has_initial", (n,))))
+    ws = _workspace(ws, 0 if ws is not None else selective_scan_prefill_workspace_bytes(params.dim, params.d_state, rows, n),
+                    dev, stream)
+    _call(dev, stream, lib.nhm_selective_scan_prefill, _ctypes_byref(params.struct), *args, rows, cu_seqlens.data_ptr(), n, slot_idx.data_ptr(),
+          has_initial.data_ptr(), ssm_pool.data_ptr(), _ssm_type(ssm_pool), int(ssm_pool.shape[0]), out.data_ptr(), ld_out,
+          ws.data_ptr(), ws.numel())
+    return out
+
+
+def token_logprobs_workspace_bytes(rows, vocab, n_top):
+    return int(lib.nhm_token_logprobs_workspace_bytes(rows, vocab, n_top))
+
+
+def token_logprobs(logits, tokens, n_top=0, logprobs=None, ranks=None, entropy=None, top_logprobs=None, top_tokens=None,
+                   ws=None, stream=None):
+    """(logprobs f32, ranks int32, entropy f32 [rows], top_logprobs f32, top_tokens int32 [rows, n_top]) of logits [rows, vocab],
+    bf16 (bits or bfloat16) or float32 (rows may be slices of wider ones), and tokens int32 [rows] (outside the vocabulary:
+    none) or None. Ranks count from 1; the alternatives come best first, equal logits by index."""
+    import torch
+    dev = _device_of(logits, "logits")
+    rows, vocab = _shape2(logits, "logits")
+    i32, f32 = (torch.int32,), (torch.float32,)
+    ld = _row_view(logits, "logits", dev, _bf16_types() + f32, rows, vocab)
+    _on(dev, [(tokens, "tokens", i32, (rows,)), (logprobs, "logprobs", f32, (rows,)), (ranks, "ranks", i32, (rows,)),
+              (entropy, "entropy", f32, (rows,)), (top_logprobs, "top_logprobs", f32, (rows, n_top)),
+              (top_tokens, "top_tokens", i32, (rows, n_top))])
+    if logprobs is None:
+        logprobs = _empty((rows,), torch.float32, dev, stream)
+    if ranks is None:
+        ranks = _empty((rows,), torch.int32, dev, stream)
+    if entropy is None:
+        entropy = _empty((rows,), torch.float32, dev, stream)
+    if top_logprobs is None:
+        top_logprobs = _empty((rows, max(n_top, 0)), torch.float32, dev, stream)
+    if top_tokens is None:
+        top_tokens = _empty((rows, max(n_top, 0)), torch.int32, dev, stream)
+    ws = _workspace(ws, 0 if ws is not None else token_logprobs_workspace_bytes(rows, vocab, n_top), dev, stream)
+    _call(dev, stream, lib.nhm_token_logprobs, logits.data_ptr(), NHM_F32 if logits.dtype == torch.float32 else NHM_BF16, ld,
+          rows, vocab, _addr(tokens), n_top, logprobs.data_ptr(), ranks.data_ptr(), entropy.data_ptr(), _addr(top_logprobs),
+          _addr(top_tokens), ws.data_ptr(), ws.numel())
+    return logprobs, ranks, entropy, top_logprobs, top_tokens

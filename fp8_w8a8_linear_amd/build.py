@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnhm.so")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "quant.hip", "gemv.hip", "gemm.hip", "decode.hip", "norm.hip", "prefill.hip", "ssd.hip",
-           "serving.hip", "lora.hip", "beam.hip", "plan.hip"]
+           "serving.hip", "lora.hip", "beam.hip", "plan.hip", "layer.hip", "mxfp4.hip", "scan.hip", "score.hip"]
 
 
 def hipcc():

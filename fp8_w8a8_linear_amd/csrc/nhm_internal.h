@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/nhm.h"
+#include "../../include/nhm_layer.h"
 #include "../../include/nhm_serving.h"
 
 namespace nhm {
@@ -28,7 +29,9 @@ enum class Kern : int {
     kQuantVec8, kQuantScalar, kDequantChannel, kGemv, kRing192x128, kRing192x128Exact, kRing256x128,
     kRing256x128Exact, kRing256x256, kRing256x256Exact, kPanel64x128, kPanel64x128Exact, kTile128,
     kTile128Exact, kSplitkReduce, kDecodeSsm, kGnormQuant, kClear, kConvFwd, kSsdState, kSsdPass, kSsdOut,
-    kLoraDown, kLoraRows, kLoraRowsExact, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan, kCount
+    kLoraDown, kLoraRows, kLoraRowsExact, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan,
+    kMxQuant, kMxDequant, kMxRows, kMxTile, kConvPrefill, kConvDecode, kScanPrefill, kScanDecode, kScoreRows,
+    kScoreJoin, kCount
 };
 void count_launch(Kern k, int64_t rows);
 
@@ -295,5 +298,107 @@ struct PlanArgs {
     int32_t* token_adapter;
 };
 nhm_status launch_batch_plan(const PlanArgs& g, hipStream_t st);
+
+// ---- selective scan and causal conv (scan.hip)
+struct ConvArgs {
+    const uint16_t* x;             // bf16 [tokens, ld_x]
+    int64_t ld_x, n_tokens;
+    const uint16_t* w;             // bf16 [dim, width]
+    const uint16_t* b;             // bf16 [dim] or nullptr
+    int32_t dim, n_seqs, n_slots;
+    bool silu;
+    const int32_t* cu_seqlens;     // prompts only
+    const int32_t* slot_idx;
+    const int32_t* has_initial;    // prompts only
+    uint16_t* pool;                // bf16 [n_slots, width - 1, dim]
+    uint16_t* out;                 // bf16 [tokens, ld_out]
+    int64_t ld_out;
+};
+nhm_status launch_conv_prefill(const ConvArgs& a, int32_t width, hipStream_t st);
+nhm_status launch_conv_decode(const ConvArgs& a, int32_t width, int32_t batch, hipStream_t st);
+
+struct ScanDecodeArgs {
+    const uint16_t *u, *dt, *B, *C, *z;   // bf16 rows; z may be nullptr
+    int64_t ld_u, ld_dt, ld_b, ld_c, ld_z;
+    const float *A_log, *D, *dt_bias;     // [dim, d_state], [dim] or nullptr, [dim] or nullptr
+    int32_t dim, d_state, n_slots;
+    const int32_t* slot_idx;
+    float* pool;                          // f32 [n_slots, dim, d_state], or nullptr with pool_bf16
+    uint16_t* pool_bf16;
+    uint16_t* out;
+    int64_t ld_out;
+};
+nhm_status launch_scan_decode(const ScanDecodeArgs& a, int32_t batch, hipStream_t st);
+
+struct ScanPrefillArgs : ScanDecodeArgs {
+    int64_t n_tokens;
+    int32_t n_seqs;
+    const int32_t* cu_seqlens;
+    const int32_t* has_initial;
+    // sequences cut into chunks: their number in the longest possible sequence, and length
+    int32_t n_chunks;
+    int64_t chunk;
+    float* ws_state;                      // [n_seqs, n_chunks + 1, dim, d_state]
+    float* ws_dt;                         // [n_seqs, n_chunks, dim]
+};
+struct ScanSplit { int64_t n_chunks, chunk; };
+ScanSplit scan_split(int64_t dim, int64_t n_tokens, int64_t n_seqs);
+size_t scan_ws_bytes(int64_t dim, int32_t d_state, int64_t n_tokens, int64_t n_seqs);
+nhm_status launch_scan_prefill(ScanPrefillArgs a, void* ws, hipStream_t st);
+
+// ---- MXFP4 (mxfp4.hip)
+struct MxQuantArgs {
+    const void* x;                 // bf16 or f32 [rows, ld_x]
+    int64_t rows, cols, ld_x;
+    uint8_t* codes;                // [rows, ld_codes] bytes
+    int64_t ld_codes;
+    uint8_t* scales;               // [rows, ld_scales]
+    int64_t ld_scales;
+};
+nhm_status launch_mx_quant(const MxQuantArgs& a, bool f32, hipStream_t st);
+struct MxDequantArgs {
+    const uint8_t* codes;
+    int64_t ld_codes;
+    const uint8_t* scales;
+    int64_t ld_scales, rows, cols;
+    uint16_t* out;                 // bf16 [rows, ld_out]
+    int64_t ld_out;
+};
+nhm_status launch_mx_dequant(const MxDequantArgs& a, hipStream_t st);
+struct MxGemmArgs {
+    const uint8_t* a;              // codes [m, ld_a bytes], 16-byte aligned rows
+    int64_t ld_a;
+    const uint8_t* a_scale;        // [m, ld_as]
+    int64_t ld_as, m;
+    const uint8_t* w;              // codes [n, k / 2]
+    const uint8_t* w_scale;        // [n, k / 32]
+    int64_t n, k;
+    uint16_t* out;                 // bf16 [m, ld_out], or nullptr with out_f32
+    float* out_f32;
+    int64_t ld_out;
+    bool vec_out;                  // rows aligned for stores of four features
+};
+nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st);
+
+// ---- scoring of tokens (score.hip)
+struct ScoreStrip { double sum, mom; float top; uint32_t count; };
+struct ScoreArgs {
+    const void* logits;            // bf16 or f32 [rows, ld]
+    bool f32;
+    int64_t ld, rows, vocab;
+    const int32_t* tokens;         // [rows] or nullptr
+    int32_t n_top;
+    float* logprobs;               // [rows], each of the three may be nullptr
+    int32_t* ranks;
+    float* entropy;
+    float* top_logprobs;           // [rows, n_top]
+    int32_t* top_tokens;
+    // workspace: per strip (a run of a row) its sums and n_top best entries
+    ScoreStrip* strips;            // [rows, n_strips]
+    uint64_t* strip_keys;          // [rows, n_strips, n_top]
+    int32_t n_strips, strip_pieces;
+};
+size_t score_ws_bytes(int64_t rows, int64_t vocab, int32_t n_top);
+nhm_status launch_score(ScoreArgs g, void* ws, hipStream_t st);
 
 }  // namespace nhm

@@ -66,6 +66,8 @@ typedef enum nhm_dtype {
     NHM_BF16 = 0,            /* bfloat16 bit patterns (uint16_t)                   */
     NHM_E4M3 = 1,            /* OCP FP8 E4M3FN codes (uint8_t)                      */
     NHM_F32 = 2,             /* IEEE binary32 (float): GEMM output, SSM state       */
+    NHM_MXFP4 = 3,           /* OCP MXFP4: e2m1 codes, two a byte, and an e8m0 scale
+                                code per 32 (nhm_layer.h)                           */
     /* Not types: they make every 32-bit int a value of the enum, so that any integer a
      * caller passes is well defined on the library side and reaches validation
      * (NHM_ERR_UNSUPPORTED). */
