@@ -18,13 +18,18 @@ constexpr int64_t kMaxOperand = int64_t(1) << 31;      // bytes behind a buffer 
 constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxRows = int64_t(1) << 24;
 constexpr int kMaxTop = 64;
 
-// Codes and scales of a bf16 activation.
-struct MxWs { size_t scales, total; };
-MxWs mx_ws(int64_t m, int64_t k, nhm_dtype t) {
-    MxWs w{0, 0};
-    if (t != NHM_BF16) return w;
-    w.scales = align_up((size_t)m * (k / 2), 256);
-    w.total = w.scales + align_up((size_t)m * (k / 32), 256);
+// Codes and scales of a bf16 activation (rows of scales a multiple of 4 bytes), and on the tile kernels copies of scale codes
+// with such rows: of the weight's where k is not a multiple of 128 or they are not 4-byte aligned, and of an MXFP4 input's.
+struct MxWs { size_t scales, pad, total; };
+MxWs mx_ws(int64_t m, int64_t n, int64_t k, nhm_dtype t) {
+    MxWs w{0, 0, 0};
+    const size_t ld = align_up((size_t)k / 32, 4);
+    if (t == NHM_BF16) {
+        w.scales = align_up((size_t)m * (k / 2), 256);
+        w.pad = w.scales + align_up((size_t)m * ld, 256);
+    }
+    w.total = w.pad;
+    if (mx_tiled(m)) w.total += align_up((size_t)n * ld, 256) + (t == NHM_BF16 ? 0 : align_up((size_t)m * ld, 256));
     return w;
 }
 
@@ -133,8 +138,8 @@ nhm_status nhm_mxfp4_dequantize(const uint8_t* codes, int64_t ld_codes, const ui
 }
 
 size_t nhm_mxfp4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, nhm_dtype a_type) {
-    if (m <= 0 || n <= 0 || k <= 0 || m > INT_MAX || k > INT_MAX) return 0;
-    return mx_ws(m, k, a_type).total;
+    if (m <= 0 || n <= 0 || k <= 0 || m > INT_MAX || n > INT_MAX || k > INT_MAX) return 0;
+    return mx_ws(m, n, k, a_type).total;
 }
 
 nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_scale, int64_t m, int64_t ld_a,
@@ -159,7 +164,7 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
     const int64_t ld_q = bf16 ? w->k / 2 : ld_a;
     if (w->n >= kMaxOperand / (w->k / 2) || m >= kMaxOperand / ld_q)
         return fail(NHM_ERR_UNSUPPORTED, "mxfp4: an operand of 2 GiB or more");
-    const MxWs l = mx_ws(m, w->k, a_type);
+    const MxWs l = mx_ws(m, w->n, w->k, a_type);
     if (l.total > 0 && (!ws || ws_bytes < l.total))
         return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", l.total, ws ? ws_bytes : (size_t)0);
     if (l.total > 0 && !aligned(ws, 256)) return fail(NHM_ERR_ALIGN, "ws must be 256-byte aligned");
@@ -168,7 +173,7 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
     g.a = static_cast<const uint8_t*>(a); g.ld_a = ld_q;
     g.a_scale = a_scale; g.ld_as = w->k / 32;
     g.m = m; g.n = w->n; g.k = w->k;
-    g.w = w->w; g.w_scale = w->scale;
+    g.w = w->w; g.w_scale = w->scale; g.ld_ws = w->k / 32;
     g.out = out_type == NHM_BF16 ? static_cast<uint16_t*>(out) : nullptr;
     g.out_f32 = out_type == NHM_F32 ? static_cast<float*>(out) : nullptr;
     g.ld_out = ld_out;
@@ -177,12 +182,13 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
     if (bf16) {
         uint8_t* const codes = static_cast<uint8_t*>(ws);
         uint8_t* const scales = codes + l.scales;
-        const nhm_status s = launch_mx_quant(MxQuantArgs{a, m, w->k, ld_a, codes, ld_q, scales, w->k / 32}, false, st);
+        g.ld_as = (int64_t)align_up((size_t)w->k / 32, 4);
+        const nhm_status s = launch_mx_quant(MxQuantArgs{a, m, w->k, ld_a, codes, ld_q, scales, g.ld_as, (int32_t)(g.ld_as - w->k / 32)}, false, st);
         if (s != NHM_OK) return s;
         g.a = codes;
         g.a_scale = scales;
     }
-    return launch_mx_gemm(g, st);
+    return launch_mx_gemm(g, static_cast<uint8_t*>(ws) + l.pad, st);
 }
 
 nhm_status nhm_causal_conv_decode(const uint16_t* x, int64_t ld_x, const uint16_t* w, const uint16_t* b, int32_t dim,

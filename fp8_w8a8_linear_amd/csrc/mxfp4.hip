@@ -6,6 +6,8 @@
 // it multiplies 32 products of a block pair by 2^(sa + sw - 254). Measured on MI355X, its sums of up to
 // 128 products are within 2^-24 of sum |a w| of the exact ones, scales 2^50 apart among them: what is
 // summed is summed in f32.
+#include <type_traits>
+
 #include "nhm_device.h"
 #include "nhm_internal.h"
 
@@ -68,6 +70,8 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(const MxQuantArgs a) {
         const uint32_t s = mx_scale(quad_max(m));
         *reinterpret_cast<uint32_t*>(a.codes + row * a.ld_codes + c / 2) = mx_codes(f, s);
         if ((c & 31) == 0) a.scales[row * a.ld_scales + c / 32] = (uint8_t)s;
+        if (c + 8 == a.cols)
+            for (int p = 0; p < a.pad; ++p) a.scales[row * a.ld_scales + a.cols / 32 + p] = 0;
     }
 }
 
@@ -145,17 +149,16 @@ template <int TM>
 __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs g) {
     __shared__ v4f s_sum[kMxWaves][TM][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, q = lane >> 4;
-    const unsigned tiles = (unsigned)((g.n + 15) / 16);
-    const int64_t n0 = (int64_t)(blockIdx.x % tiles) * 16, m0 = (int64_t)(blockIdx.x / tiles) * (16 * TM);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t kb = g.k / 2, ks = g.k / 32;       // bytes of codes and of scales in a weight row
-    const auto wrs = mx_buffer(g.w, g.n * kb), wss = mx_buffer(g.w_scale, g.n * ks);
+    const auto wrs = mx_buffer(g.w, g.n * kb), wss = mx_buffer(g.w_scale, g.n * g.ld_ws);
     const auto ars = mx_buffer(g.a, g.m * g.ld_a), ass = mx_buffer(g.a_scale, g.m * g.ld_as);
     const int64_t wr = n0 + r16;
-    const uint32_t woff = wr < g.n ? (uint32_t)(wr * kb) : kPast, wsoff = wr < g.n ? (uint32_t)(wr * ks) : kPast;
+    const uint32_t woff = wr < g.n ? (uint32_t)(wr * kb) : kPast, wsoff = wr < g.n ? (uint32_t)(wr * g.ld_ws) : kPast;
     uint32_t aoff[TM], asoff[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-        const int64_t row = m0 + 16 * j + r16;
+        const int64_t row = 16 * j + r16;
         aoff[j] = row < g.m ? (uint32_t)(row * g.ld_a) : kPast;
         asoff[j] = row < g.m ? (uint32_t)(row * g.ld_as) : kPast;
     }
@@ -191,7 +194,7 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs
         v4f x = s_sum[0][j][lane];
 #pragma unroll
         for (int o = 1; o < kMxWaves; ++o) x += s_sum[o][j][lane];
-        const int64_t row = m0 + 16 * j + r16, nb = n0 + 4 * q;     // four consecutive features of one row
+        const int64_t row = 16 * j + r16, nb = n0 + 4 * q;     // four consecutive features of one row
         if (row >= g.m) continue;
         if (g.out_f32) {
             float* o = g.out_f32 + row * g.ld_out + nb;
@@ -211,12 +214,307 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs
     }
 }
 
-nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st) {
-    auto rows = [&](int tm) { return dim3((unsigned)((g.n + 15) / 16 * ((g.m + 16 * tm - 1) / (16 * tm)))); };
-    if (g.m <= 16) mx_rows_kernel<1><<<rows(1), dim3(kMxWaves * 64), 0, st>>>(g);
-    else if (g.m <= 32) mx_rows_kernel<2><<<rows(2), dim3(kMxWaves * 64), 0, st>>>(g);
-    else mx_rows_kernel<4><<<rows(4), dim3(kMxWaves * 64), 0, st>>>(g);
-    count_launch(Kern::kMxRows, g.m);
+// ---------------------------------------------------------------- tiles
+//
+// Many rows: a workgroup computes TN features x TM rows, its NWN x NWM waves TN / NWN x TM / NWM each, by the 32x32x64 matrix
+// instruction. Slices of k, KB bytes of codes of every row, stream into a ring of LDS stages by direct loads; the operands of
+// the next stage are read while the current one's products run. The scale codes travel as dwords, four blocks of a row, one
+// dword (KB = 64) or two (KB = 128) to a row and stage, so their rows are 4-byte aligned and padded (MxGemmArgs).
+// A lane's half of a stage's row is KB / 2 bytes, KB / 32 blocks, whose scale codes are adjacent bytes: with 128 byte
+// slices a dword of its own, which the matrix instruction takes bytes of.
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ i32x4 mx_desc(const void* base, int64_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    return i32x4{(int)(uint32_t)b, (int)((uint32_t)(b >> 32) & 0xffffu), (int)bytes, 0x00020000};
+}
+
+// kBytes (16 or 4) per lane from byte offset voff + soff of the buffer into LDS at lds + kBytes * lane (an offset past the
+// range writes zeros; soff itself must lie within it: the hardware compares voff with the range less soff). As asm, so that the compiler does not hold every later LDS read behind it; the kernel waits for these
+// loads itself, and the wait states ahead of the load stand here: one after the write of M0, five after a vector instruction
+// that wrote a register of the descriptor.
+template <int kBytes>
+__device__ __forceinline__ void dma(const i32x4& rs, const uint8_t* lds, uint32_t voff, uint32_t soff) {
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)lds;
+    if constexpr (kBytes == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(m0), "v"(voff), "s"(rs), "s"(soff)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(m0), "v"(voff), "s"(rs), "s"(soff)
+                     : "memory", "m0");
+}
+
+template <int S>
+__device__ __forceinline__ v16f mfma_mx32(const v4u& a, const v4u& b, const v16f& c, uint32_t sa, uint32_t sb) {
+    v8i x{}, y{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] = (int)a[i];
+        y[i] = (int)b[i];
+    }
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// 16-byte chunk c of row r of a stage: 16 rows read at one chunk cover all LDS banks.
+template <int KB>
+__device__ __forceinline__ int mx_slot(int row, int c) {
+    if constexpr (KB == 64) return row * 64 + ((c ^ (((row >> 1) ^ (row >> 2)) & 3)) << 4);
+    else return swz128(row, c);
+}
+
+template <int TN, int TM, int NWN, int NWM, int KB, int RING>
+__global__ __launch_bounds__(64 * NWN * NWM) void mx_tile_kernel(const MxGemmArgs g) {
+    constexpr int kWaves = NWN * NWM, kRows = TN + TM, kNI = TN / NWN / 32, kNJ = TM / NWM / 32;
+    constexpr int kCodes = kRows * KB, kPlanes = KB / 64, kStage = kCodes + kPlanes * kRows * 4;
+    constexpr int kBlockRows = 1024 / KB, kBlocks = kRows / kBlockRows, kLoads = kBlocks / kWaves;   // 1 KB a load
+    constexpr int kScales = kPlanes * kRows / 64, kScaleLoads = (kScales + kWaves - 1) / kWaves;      // 64 dwords a load
+    constexpr int kAll = kLoads + kScaleLoads, kSteps = KB / 32, kRowBytes = TN * 2;
+    static_assert(kBlocks % kWaves == 0 && TN % kBlockRows == 0 && kRows % 64 == 0 && TN % 64 == 0, "whole loads");
+    static_assert(RING >= 3 && (RING - 2) * kAll < 64, "ring depth and the vmcnt field");
+    constexpr int kSpare = kScales % kWaves ? 256 : 0;      // where the waves without a scale load put zeros
+    constexpr int kLds = RING * kStage + kSpare > TM * kRowBytes ? RING * kStage + kSpare : TM * kRowBytes;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wn = wave / NWM, wm = wave % NWM, r32 = lane & 31, q = lane >> 5;
+
+    // blocks go to the 8 XCDs round robin; each takes a contiguous share of the tiles in an order that walks 8 row tiles per
+    // feature tile, so that the tiles it holds at once share operands through its L2
+    const int ntn = (int)((g.n + TN - 1) / TN), ntm = (int)((g.m + TM - 1) / TM), total = ntn * ntm;
+    const int x = blockIdx.x & 7, loc = blockIdx.x >> 3, jt = x * (total >> 3) + min(x, total & 7) + loc;
+    const int grp = jt / (8 * ntn), in_grp = jt - grp * 8 * ntn, gms = min(8, ntm - grp * 8);
+    const int64_t m0 = (int64_t)(grp * 8 + in_grp % gms) * TM, n0 = (int64_t)(in_grp / gms) * TN;
+
+    const int kb = (int)(g.k / 2), ks = (int)(g.k / 32);
+    const i32x4 wrs = mx_desc(g.w, g.n * kb), ars = mx_desc(g.a, g.m * g.ld_a);
+    const i32x4 wss = mx_desc(g.w_scale, g.n * g.ld_ws), ass = mx_desc(g.a_scale, g.m * g.ld_as);
+    // this lane's source offset of each of the wave's loads at k = 0
+    constexpr int kPer = KB / 16;
+    uint32_t dbase[kLoads], sbase[kScaleLoads];
+    auto chunk = [&](int i) {       // byte offset in a row of the chunk that lands at slot lane % kPer
+        const int row = (wave * kLoads + i) * kBlockRows + lane / kPer, slot = lane % kPer;
+        return 16 * (KB == 64 ? slot ^ (((row >> 1) ^ (row >> 2)) & 3) : slot ^ (row & 7) ^ ((row >> 3) & 1));
+    };
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int row = (wave * kLoads + i) * kBlockRows + lane / kPer;
+        const bool isw = row < TN;
+        const int64_t at = isw ? n0 + row : m0 + row - TN;
+        dbase[i] = at < (isw ? g.n : g.m) ? (uint32_t)(at * (isw ? kb : g.ld_a) + chunk(i)) : kPast;
+    }
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) {
+        const int blk = wave + i * kWaves, row = blk % (kRows / 64) * 64 + lane, plane = blk / (kRows / 64);
+        const bool isw = row < TN;
+        const int64_t at = isw ? n0 + row : m0 + row - TN;
+        sbase[i] = blk < kScales && at < (isw ? g.n : g.m) ? (uint32_t)(at * (isw ? g.ld_ws : g.ld_as) + 4 * plane) : kPast;
+    }
+    const int nk = (kb + KB - 1) / KB;
+    auto issue = [&](int s, int slot) {
+        uint8_t* const sb = smem + slot * kStage;
+        const int k0 = s * KB, s0 = s * (KB / 16);
+        const bool whole = k0 + KB <= kb;      // else, and past k, each lane's offset is checked
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int blk = wave * kLoads + i;
+            if (whole) dma<16>(blk * kBlockRows < TN ? wrs : ars, sb + blk * 1024, dbase[i], (uint32_t)k0);
+            else dma<16>(blk * kBlockRows < TN ? wrs : ars, sb + blk * 1024, k0 + chunk(i) < kb ? dbase[i] + k0 : kPast, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) {
+            const int blk = wave + i * kWaves, rows64 = blk % (kRows / 64), plane = blk / (kRows / 64);
+            uint8_t* const to = kSpare != 0 && blk >= kScales ? smem + RING * kStage : sb + kCodes + blk * 256;
+            if (whole) dma<4>(rows64 * 64 < TN ? wss : ass, to, sbase[i], (uint32_t)s0);
+            else dma<4>(rows64 * 64 < TN ? wss : ass, to, s0 + 4 * plane < ks ? sbase[i] + s0 : kPast, 0u);
+        }
+    };
+    struct Ops { v4u w[kNI], a[kNJ]; };
+    struct Scales { uint32_t w[kNI], a[kNJ]; };
+    // rows 16 apart have the same slots: addresses are those of the wave's first rows and constants
+    int at[kSteps];
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) at[u] = mx_slot<KB>(r32, q * kSteps + u);
+    const int wrow = wn * (TN / NWN), arow = TN + wm * (TM / NWM);
+    const int sat = kCodes + (kPlanes == 2 ? (q * kRows + r32) * 4 : r32 * 4 + 2 * q);
+    auto read = [&](int slot, int u, Ops& o) {
+        const uint8_t* const p = smem + slot * kStage + at[u];
+#pragma unroll
+        for (int i = 0; i < kNI; ++i) o.w[i] = *reinterpret_cast<const v4u*>(p + (wrow + 32 * i) * KB);
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j) o.a[j] = *reinterpret_cast<const v4u*>(p + (arow + 32 * j) * KB);
+    };
+    auto read_scales = [&](int slot, Scales& o) {
+        const uint8_t* const p = smem + slot * kStage + sat;
+        auto one = [&](int row) {
+            if constexpr (kPlanes == 2) return *reinterpret_cast<const uint32_t*>(p + row * 4);
+            else return (uint32_t)*reinterpret_cast<const uint16_t*>(p + row * 4);
+        };
+#pragma unroll
+        for (int i = 0; i < kNI; ++i) o.w[i] = one(wrow + 32 * i);
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j) o.a[j] = one(arow + 32 * j);
+    };
+    v16f acc[kNI][kNJ];
+#pragma unroll
+    for (int i = 0; i < kNI; ++i)
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    Ops ops[2];
+    Scales sc, sc_next;
+    auto multiply = [&](auto u) {
+        constexpr int U = decltype(u)::value;
+#pragma unroll
+        for (int i = 0; i < kNI; ++i)
+#pragma unroll
+            for (int j = 0; j < kNJ; ++j) acc[i][j] = mfma_mx32<U>(ops[U & 1].w[i], ops[U & 1].a[j], acc[i][j], sc.w[i], sc.a[j]);
+    };
+#pragma unroll
+    for (int s = 0; s < RING - 1; ++s) issue(s, s);
+    wait_vmcnt<(RING - 2) * kAll>();
+    __syncthreads();
+    read(0, 0, ops[0]);
+    read_scales(0, sc);
+    // Of a stage, 64 of k at a time: the next step's operands are read while this one's products run. Ahead of the last
+    // step the next stage has landed (this thread's loads, then everyone's, who are all done with the stage before
+    // this one), and that stage's slot is refilled.
+    int slot = 0;
+    for (int s = 0; s < nk; ++s) {
+        const int next = slot + 1 == RING ? 0 : slot + 1, free = slot == 0 ? RING - 1 : slot - 1;
+        auto inner = [&](auto u) {
+            constexpr int U = decltype(u)::value;
+            if constexpr (U + 1 < kSteps) {
+                read(slot, U + 1, ops[(U + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(u);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        inner(std::integral_constant<int, 0>());
+        inner(std::integral_constant<int, 1>());
+        inner(std::integral_constant<int, 2>());
+        wait_vmcnt<(RING - 3) * kAll>();
+        __syncthreads();
+        issue(s + RING - 1, free);
+        read(next, 0, ops[0]);
+        read_scales(next, sc_next);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(std::integral_constant<int, kSteps - 1>());
+        __builtin_amdgcn_sched_barrier(0);
+        sc = sc_next;
+        slot = next;
+    }
+    wait_vmcnt<0>();                // the stages past k, before the ring is used again
+
+    // acc[i][j] register r: feature 32 i + 8 (r / 4) + 4 q + r % 4 of row 32 j + r32 of the wave's tile
+    if (g.out_f32) {
+#pragma unroll
+        for (int i = 0; i < kNI; ++i)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int64_t nb = n0 + wn * (TN / NWN) + 32 * i + 8 * b + 4 * q;
+#pragma unroll
+                for (int j = 0; j < kNJ; ++j) {
+                    const int64_t row = m0 + wm * (TM / NWM) + 32 * j + r32;
+                    if (row >= g.m) continue;
+                    float* const o = g.out_f32 + row * g.ld_out + nb;
+                    if (g.vec_out && nb + 4 <= g.n) *reinterpret_cast<v4f*>(o) = v4f{acc[i][j][4 * b], acc[i][j][4 * b + 1], acc[i][j][4 * b + 2], acc[i][j][4 * b + 3]};
+                    else
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (nb + r < g.n) o[r] = acc[i][j][4 * b + r];
+                }
+            }
+        return;
+    }
+    // bf16: the tile goes through LDS, so that whole rows are stored. Chunk c of row m at slot c ^ (m % 16), its halves
+    // swapped in every other group of 8 and 16 rows: the 8-byte writes of 32 rows at one feature hit distinct banks.
+    __syncthreads();
+    constexpr int kChunks = TN / 8, kMask = kChunks < 16 ? kChunks - 1 : 15;
+#pragma unroll
+    for (int i = 0; i < kNI; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int c = (wn * (TN / NWN) + 32 * i + 8 * b) / 8;
+#pragma unroll
+            for (int j = 0; j < kNJ; ++j) {
+                const int ml = wm * (TM / NWM) + 32 * j + r32, hs = ((ml >> 3) ^ (ml >> 4)) & 1;
+                *reinterpret_cast<uint2*>(smem + ml * kRowBytes + ((c ^ (ml & kMask)) << 4) + ((q ^ hs) << 3)) =
+                    make_uint2(f32x2_to_bf16x2(acc[i][j][4 * b], acc[i][j][4 * b + 1]), f32x2_to_bf16x2(acc[i][j][4 * b + 2], acc[i][j][4 * b + 3]));
+            }
+        }
+    __syncthreads();
+    const bool vec = (g.ld_out & 7) == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0;
+#pragma unroll 4
+    for (int e = t; e < TM * kChunks; e += 64 * kWaves) {
+        const int ml = e / kChunks, c = e % kChunks;
+        uint4 v = *reinterpret_cast<const uint4*>(smem + ml * kRowBytes + ((c ^ (ml & kMask)) << 4));
+        if (((ml >> 3) ^ (ml >> 4)) & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+        const int64_t row = m0 + ml, nn = n0 + 8 * c;
+        if (row >= g.m) continue;
+        uint16_t* const o = g.out + row * g.ld_out + nn;
+        if (vec && nn + 8 <= g.n) {
+            *reinterpret_cast<uint4*>(o) = v;
+        } else {
+            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (nn + r < g.n) o[r] = (uint16_t)(w4[r >> 1] >> (16 * (r & 1)));
+        }
+    }
+}
+
+// Scale codes with rows padded to whole dwords (k not a multiple of 128).
+__global__ __launch_bounds__(256) void mx_repack_kernel(const uint8_t* src, int64_t rows, int per, uint8_t* dst, int ld) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * ld; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / ld;
+        const int c = (int)(i - row * ld);
+        dst[i] = c < per ? src[row * per + c] : 0;
+    }
+}
+
+static void mx_repack(const uint8_t* src, int64_t rows, int64_t per, uint8_t* dst, int64_t ld, hipStream_t st) {
+    mx_repack_kernel<<<dim3(mx_blocks(rows * ld)), dim3(256), 0, st>>>(src, rows, (int)per, dst, (int)ld);
+}
+
+template <int TN, int TM, int NWN, int NWM, int KB, int RING>
+static void launch_tile(const MxGemmArgs& g, hipStream_t st) {
+    const int64_t tiles = (g.n + TN - 1) / TN * ((g.m + TM - 1) / TM);
+    mx_tile_kernel<TN, TM, NWN, NWM, KB, RING><<<dim3((unsigned)tiles), dim3(64 * NWN * NWM), 0, st>>>(g);
+}
+
+bool mx_tiled(int64_t m) { return m > 64; }
+
+nhm_status launch_mx_gemm(MxGemmArgs g, uint8_t* pad, hipStream_t st) {
+    const unsigned tiles = (unsigned)((g.n + 15) / 16);
+    if (!mx_tiled(g.m)) {
+        const dim3 block(kMxWaves * 64);
+        if (g.m <= 16) mx_rows_kernel<1><<<dim3(tiles), block, 0, st>>>(g);
+        else if (g.m <= 32) mx_rows_kernel<2><<<dim3(tiles), block, 0, st>>>(g);
+        else mx_rows_kernel<4><<<dim3(tiles), block, 0, st>>>(g);
+        count_launch(Kern::kMxRows, g.m);
+        return check_launch("mxfp4 linear");
+    }
+    const int64_t ks = g.k / 32, ld = (int64_t)align_up((size_t)ks, 4);
+    // a dword load takes four scale codes: rows of them start at a multiple of four
+    if (g.ld_ws != ld || reinterpret_cast<uintptr_t>(g.w_scale) % 4 != 0) {
+        mx_repack(g.w_scale, g.n, ks, pad, ld, st);
+        g.w_scale = pad;
+        g.ld_ws = ld;
+        pad += align_up((size_t)g.n * ld, 256);
+    }
+    if (g.ld_as != ld || reinterpret_cast<uintptr_t>(g.a_scale) % 4 != 0) {
+        mx_repack(g.a_scale, g.m, ks, pad, ld, st);
+        g.a_scale = pad;
+        g.ld_as = ld;
+    }
+    auto count = [&](int64_t tn, int64_t tm) { return (g.n + tn - 1) / tn * ((g.m + tm - 1) / tm); };
+    if (count(256, 256) >= 160) launch_tile<256, 256, 2, 4, 64, 4>(g, st);
+    else if (count(128, 128) >= 200) launch_tile<128, 128, 2, 2, 128, 4>(g, st);
+    else launch_tile<64, 64, 2, 2, 128, 4>(g, st);
+    count_launch(Kern::kMxTile, g.m);
     return check_launch("mxfp4 linear");
 }
 

@@ -354,6 +354,7 @@ struct MxQuantArgs {
     int64_t ld_codes;
     uint8_t* scales;               // [rows, ld_scales]
     int64_t ld_scales;
+    int32_t pad = 0;               // scale codes behind a row's that are set to 0
 };
 nhm_status launch_mx_quant(const MxQuantArgs& a, bool f32, hipStream_t st);
 struct MxDequantArgs {
@@ -371,14 +372,17 @@ struct MxGemmArgs {
     const uint8_t* a_scale;        // [m, ld_as]
     int64_t ld_as, m;
     const uint8_t* w;              // codes [n, k / 2]
-    const uint8_t* w_scale;        // [n, k / 32]
-    int64_t n, k;
+    const uint8_t* w_scale;        // [n, ld_ws]
+    int64_t ld_ws, n, k;
     uint16_t* out;                 // bf16 [m, ld_out], or nullptr with out_f32
     float* out_f32;
     int64_t ld_out;
     bool vec_out;                  // rows aligned for stores of four features
 };
-nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st);
+// Whether m rows run on the tile kernels, which take scale codes by dwords: pad is room for copies of the weight's
+// and the activations' with rows of a multiple of 4 bytes, where theirs are not.
+bool mx_tiled(int64_t m);
+nhm_status launch_mx_gemm(MxGemmArgs g, uint8_t* pad, hipStream_t st);
 
 // ---- scoring of tokens (score.hip)
 struct ScoreStrip { double sum, mom; float top; uint32_t count; };

@@ -55,7 +55,8 @@ typedef struct nhm_mxfp4_weight {
     int64_t k;             /* input features, k % 32 == 0                    */
 } nhm_mxfp4_weight;
 
-/* Workspace bytes of nhm_mxfp4_linear (0 for m, n or k <= 0): the codes and scales of a bf16 input. */
+/* Workspace bytes of nhm_mxfp4_linear (0 for m, n or k <= 0): the codes and scales of a bf16 input, and copies of scale codes
+ * whose rows the tile kernels cannot take as they are (k not a multiple of 128, or not 4-byte aligned). */
 NHM_API size_t nhm_mxfp4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, nhm_dtype a_type);
 
 /* out[i, j] = sum_k val(a[i, k]) val(w[j, k]), summed in f32 (within 2^-24 of sum |a w| per 128 products), rounded

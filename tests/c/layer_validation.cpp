@@ -34,7 +34,8 @@ size_t scan_ws_bytes(int64_t dim, int32_t n, int64_t, int64_t seqs) { return (si
 nhm_status launch_scan_prefill(ScanPrefillArgs, void*, hipStream_t) { reached("launch_scan_prefill"); }
 nhm_status launch_mx_quant(const MxQuantArgs&, bool, hipStream_t) { reached("launch_mx_quant"); }
 nhm_status launch_mx_dequant(const MxDequantArgs&, hipStream_t) { reached("launch_mx_dequant"); }
-nhm_status launch_mx_gemm(const MxGemmArgs&, hipStream_t) { reached("launch_mx_gemm"); }
+bool mx_tiled(int64_t m) { return m > 64; }
+nhm_status launch_mx_gemm(MxGemmArgs, uint8_t*, hipStream_t) { reached("launch_mx_gemm"); }
 size_t score_ws_bytes(int64_t rows, int64_t, int32_t) { return (size_t)rows * 16; }
 nhm_status launch_score(ScoreArgs, void*, hipStream_t) { reached("launch_score"); }
 }  // namespace nhm
