@@ -78,7 +78,7 @@ class _StatePool(C.Structure):
 
 
 class _Mxfp4Weight(C.Structure):
-    _fields_ = [("w", C.c_void_p), ("scale", C.c_void_p), ("n", C.c_int64), ("k", C.c_int64)]
+    _fields_ = [("w", C.c_void_p), ("scale", C.c_void_p), ("n", C.c_int64), ("k", C.c_int64), ("packed_scale", C.c_void_p)]
 
 
 class _ScanParams(C.Structure):
@@ -129,6 +129,8 @@ _SIGS = {
     "nhm_mxfp4_quantize": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p]),
     "nhm_mxfp4_dequantize": (C.c_int, [_p, _i64, _p, _i64, _i64, _i64, _p, _i64, _p]),
     "nhm_mxfp4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, C.c_int]),
+    "nhm_mxfp4_packed_scale_bytes": (_sz, [_i64, _i64]),
+    "nhm_mxfp4_pack_scales": (C.c_int, [_p, _i64, _i64, _p, _p]),
     "nhm_mxfp4_linear": (C.c_int, [_p, C.c_int, _p, _i64, _i64, C.POINTER(_Mxfp4Weight), _p, C.c_int, _i64, _p, _sz, _p]),
     "nhm_causal_conv_decode": (C.c_int, [_p, _i64, _p, _p, _i32, _i32, _i32, _i32, _p, _p, _i32, _p, _i64, _p]),
     "nhm_causal_conv_prefill": (C.c_int, [_p, _i64, _i64, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p, _p, _i32, _p, _i64,
@@ -668,15 +670,22 @@ _ctypes_byref = C.byref          # the scans have an argument named C
 
 class Mxfp4Weight:
     """One MXFP4 projection on the device: codes uint8 [n, k / 2] (two a byte, the lower index in the low four bits) and
-    scale codes uint8 [n, k / 32], as mxfp4_quantize makes them."""
+    scale codes uint8 [n, k / 32], as mxfp4_quantize makes them. Calls of more than 64 rows take the scale codes from a copy
+    that is packed here, once: after writing to scale, call pack() again."""
 
-    def __init__(self, w, scale):
+    def __init__(self, w, scale, stream=None):
         import torch
         dev = _device_of(w, "w")
         n, kb = _shape2(w, "w")
         _on(dev, [(w, "w", (torch.uint8,), None), (scale, "scale", (torch.uint8,), (n, kb // 16))])
         self.w, self.scale, self.n, self.k = w, scale, n, 2 * kb
-        self._s = _Mxfp4Weight(w.data_ptr(), scale.data_ptr(), n, 2 * kb)
+        self.packed = _empty((int(lib.nhm_mxfp4_packed_scale_bytes(n, self.k)),), torch.uint8, dev, stream)
+        self._s = _Mxfp4Weight(w.data_ptr(), scale.data_ptr(), n, self.k, self.packed.data_ptr())
+        self.pack(stream)
+
+    def pack(self, stream=None):
+        """The packed copy of the scale codes made anew, on `stream`."""
+        _call(self.w.device, stream, lib.nhm_mxfp4_pack_scales, self.scale.data_ptr(), self.n, self.k, self.packed.data_ptr())
 
     @property
     def struct(self):

@@ -27,7 +27,7 @@ static const char* const kKernNames[(int)Kern::kCount] = {
     "gemm_ring256x128", "gemm_ring256x128_exact", "gemm_ring256x256", "gemm_ring256x256_exact", "gemm_panel64x128",
     "gemm_panel64x128_exact", "gemm_tile128", "gemm_tile128_exact", "gemm_splitk_reduce", "decode_ssm",
     "gnorm_quant", "clear", "conv_fwd", "ssd_state", "ssd_pass", "ssd_out", "lora_down", "lora_rows", "lora_rows_exact", "beam_rows",
-    "beam_pick", "beam_reorder", "batch_plan", "mxfp4_quant", "mxfp4_dequant", "mxfp4_rows", "mxfp4_tile", "conv_prefill",
+    "beam_pick", "beam_reorder", "batch_plan", "mxfp4_quant", "mxfp4_dequant", "mxfp4_pack", "mxfp4_rows", "mxfp4_tile", "conv_prefill",
     "conv_decode", "scan_prefill", "scan_decode", "score_rows", "score_join"};
 static std::atomic<uint64_t> g_launches[(int)Kern::kCount];
 static std::atomic<uint64_t> g_rows[(int)Kern::kCount];

@@ -18,18 +18,17 @@ constexpr int64_t kMaxOperand = int64_t(1) << 31;      // bytes behind a buffer 
 constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxRows = int64_t(1) << 24;
 constexpr int kMaxTop = 64;
 
-// Codes and scales of a bf16 activation (rows of scales a multiple of 4 bytes), and on the tile kernels copies of scale codes
-// with such rows: of the weight's where k is not a multiple of 128 or they are not 4-byte aligned, and of an MXFP4 input's.
-struct MxWs { size_t scales, pad, total; };
+// Codes of a bf16 activation and its scales, as rows or packed for the tile kernels (an MXFP4 input's packed scales
+// alone), and on the tile kernels room for the weight's packed scales where the caller has none.
+struct MxWs { size_t scales, weight, total; };
 MxWs mx_ws(int64_t m, int64_t n, int64_t k, nhm_dtype t) {
     MxWs w{0, 0, 0};
-    const size_t ld = align_up((size_t)k / 32, 4);
-    if (t == NHM_BF16) {
-        w.scales = align_up((size_t)m * (k / 2), 256);
-        w.pad = w.scales + align_up((size_t)m * ld, 256);
-    }
-    w.total = w.pad;
-    if (mx_tiled(m)) w.total += align_up((size_t)n * ld, 256) + (t == NHM_BF16 ? 0 : align_up((size_t)m * ld, 256));
+    const bool tiled = mx_tiled(m);
+    if (t == NHM_BF16) w.scales = align_up((size_t)m * (k / 2), 256);
+    w.weight = w.scales;
+    if (tiled) w.weight += align_up((size_t)mx_packed_words(m, k) * 4, 256);
+    else if (t == NHM_BF16) w.weight += align_up((size_t)m * (k / 32), 256);
+    w.total = w.weight + (tiled ? align_up((size_t)mx_packed_words(n, k) * 4, 256) : 0);
     return w;
 }
 
@@ -157,6 +156,7 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
         return fail(NHM_ERR_SHAPE, "mxfp4: m %lld, n %lld, k %lld (a multiple of 32; ld %lld, %lld) out of range", (long long)m,
                     (long long)w->n, (long long)w->k, (long long)ld_a, (long long)ld_out);
     if (m == 0) return NHM_OK;
+    if (!aligned(w->packed_scale, 4)) return fail(NHM_ERR_ALIGN, "mxfp4: the weight's packed scales must be 4-byte aligned");
     if (!a || !w->w || !w->scale || !out || (!bf16 && !a_scale))
         return fail(NHM_ERR_NULL, "mxfp4: a, a_scale, the weight's codes or scales, or out is NULL");
     if (!rows16(a, ld_a * (bf16 ? 2 : 1)) || !aligned(w->w, 16) || !aligned(out, out_type == NHM_F32 ? 4 : 2))
@@ -179,16 +179,43 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
     g.ld_out = ld_out;
     const size_t four = out_type == NHM_F32 ? 16 : 8;
     g.vec_out = aligned(out, four) && ld_out % 4 == 0;
+    uint8_t* const wsb = static_cast<uint8_t*>(ws);
+    uint32_t* const packed = mx_tiled(m) ? reinterpret_cast<uint32_t*>(wsb + l.scales) : nullptr;
+    nhm_status s = NHM_OK;
     if (bf16) {
-        uint8_t* const codes = static_cast<uint8_t*>(ws);
-        uint8_t* const scales = codes + l.scales;
-        g.ld_as = (int64_t)align_up((size_t)w->k / 32, 4);
-        const nhm_status s = launch_mx_quant(MxQuantArgs{a, m, w->k, ld_a, codes, ld_q, scales, g.ld_as, (int32_t)(g.ld_as - w->k / 32)}, false, st);
-        if (s != NHM_OK) return s;
-        g.a = codes;
-        g.a_scale = scales;
+        MxQuantArgs q{a, m, w->k, ld_a, wsb, ld_q, wsb + l.scales, w->k / 32};
+        q.packed = packed;
+        s = launch_mx_quant(q, false, st);
+        g.a = wsb;
+        g.a_scale = wsb + l.scales;
+    } else if (packed) {
+        s = launch_mx_pack(a_scale, m, w->k, packed, st);
     }
-    return launch_mx_gemm(g, static_cast<uint8_t*>(ws) + l.pad, st);
+    if (s != NHM_OK) return s;
+    g.a_packed = packed;
+    g.w_packed = w->packed_scale;
+    if (packed && !w->packed_scale) {
+        uint32_t* const wp = reinterpret_cast<uint32_t*>(wsb + l.weight);
+        if ((s = launch_mx_pack(w->scale, w->n, w->k, wp, st)) != NHM_OK) return s;
+        g.w_packed = wp;
+    }
+    return launch_mx_gemm(g, st);
+}
+
+size_t nhm_mxfp4_packed_scale_bytes(int64_t n, int64_t k) {
+    if (n <= 0 || k <= 0 || n > INT_MAX || k > INT_MAX || k % 32 != 0) return 0;
+    return (size_t)mx_packed_words(n, k) * 4;
+}
+
+nhm_status nhm_mxfp4_pack_scales(const uint8_t* scale, int64_t n, int64_t k, uint32_t* packed, void* stream) {
+    clear_error();
+    if (n < 0 || k < 0 || n > INT_MAX || k > INT_MAX || k % 32 != 0)
+        return fail(NHM_ERR_SHAPE, "mxfp4: scales of [%lld, %lld] (a multiple of 32) out of range", (long long)n, (long long)k);
+    if (n == 0 || k == 0) return NHM_OK;
+    if (!scale || !packed) return fail(NHM_ERR_NULL, "mxfp4: scale or packed is NULL");
+    if (!aligned(packed, 4)) return fail(NHM_ERR_ALIGN, "mxfp4: packed must be 4-byte aligned");
+    if (mx_packed_words(n, k) >= kMaxOperand / 4) return fail(NHM_ERR_UNSUPPORTED, "mxfp4: scales of 2 GiB or more");
+    return launch_mx_pack(scale, n, k, packed, (hipStream_t)stream);
 }
 
 nhm_status nhm_causal_conv_decode(const uint16_t* x, int64_t ld_x, const uint16_t* w, const uint16_t* b, int32_t dim,

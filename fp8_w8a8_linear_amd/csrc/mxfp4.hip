@@ -69,9 +69,17 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(const MxQuantArgs a) {
         for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
         const uint32_t s = mx_scale(quad_max(m));
         *reinterpret_cast<uint32_t*>(a.codes + row * a.ld_codes + c / 2) = mx_codes(f, s);
-        if ((c & 31) == 0) a.scales[row * a.ld_scales + c / 32] = (uint8_t)s;
-        if (c + 8 == a.cols)
-            for (int p = 0; p < a.pad; ++p) a.scales[row * a.ld_scales + a.cols / 32 + p] = 0;
+        if ((c & 31) == 0) {
+            if (a.packed) {
+                // byte (c / 32) % 4 of dword (c / 128, row); the last block also clears what its dword has left
+                uint8_t* const d = reinterpret_cast<uint8_t*>(a.packed + (int64_t)(c / 128) * a.rows + row);
+                d[c / 32 % 4] = (uint8_t)s;
+                if (c + 32 == a.cols)
+                    for (int p = c / 32 % 4 + 1; p < 4; ++p) d[p] = 0;
+            } else {
+                a.scales[row * a.ld_scales + c / 32] = (uint8_t)s;
+            }
+        }
     }
 }
 
@@ -219,7 +227,8 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs
 // Many rows: a workgroup computes TN features x TM rows, its NWN x NWM waves TN / NWN x TM / NWM each, by the 32x32x64 matrix
 // instruction. Slices of k, KB bytes of codes of every row, stream into a ring of LDS stages by direct loads; the operands of
 // the next stage are read while the current one's products run. The scale codes travel as dwords, four blocks of a row, one
-// dword (KB = 64) or two (KB = 128) to a row and stage, so their rows are 4-byte aligned and padded (MxGemmArgs).
+// dword (KB = 64) or two (KB = 128) to a row and stage, packed so that a load's 64 rows are 256 bytes in a row: from rows of
+// scale codes every dword is a request of its own, and half of all requests to L2 were theirs.
 // A lane's half of a stage's row is KB / 2 bytes, KB / 32 blocks, whose scale codes are adjacent bytes: with 128 byte
 // slices a dword of its own, which the matrix instruction takes bytes of.
 
@@ -264,69 +273,82 @@ __device__ __forceinline__ int mx_slot(int row, int c) {
     else return swz128(row, c);
 }
 
-template <int TN, int TM, int NWN, int NWM, int KB, int RING>
+template <int TN, int TM, int NWN, int NWM, int KB, int RING, bool f32>
 __global__ __launch_bounds__(64 * NWN * NWM) void mx_tile_kernel(const MxGemmArgs g) {
     constexpr int kWaves = NWN * NWM, kRows = TN + TM, kNI = TN / NWN / 32, kNJ = TM / NWM / 32;
     constexpr int kCodes = kRows * KB, kPlanes = KB / 64, kStage = kCodes + kPlanes * kRows * 4;
     constexpr int kBlockRows = 1024 / KB, kBlocks = kRows / kBlockRows, kLoads = kBlocks / kWaves;   // 1 KB a load
     constexpr int kScales = kPlanes * kRows / 64, kScaleLoads = (kScales + kWaves - 1) / kWaves;      // 64 dwords a load
-    constexpr int kAll = kLoads + kScaleLoads, kSteps = KB / 32, kRowBytes = TN * 2;
-    static_assert(kBlocks % kWaves == 0 && TN % kBlockRows == 0 && kRows % 64 == 0 && TN % 64 == 0, "whole loads");
-    static_assert(RING >= 3 && (RING - 2) * kAll < 64, "ring depth and the vmcnt field");
+    constexpr int kAll = kLoads + kScaleLoads, kSteps = KB / 32;
+    static_assert(TN % (kBlockRows * kWaves) == 0 && TM % (kBlockRows * kWaves) == 0 && kBlockRows * kWaves % 16 == 0 &&
+                  TN % 64 == 0 && TM % 64 == 0, "whole loads");
+    static_assert(RING >= 2 && (RING - 2) * kAll + (f32 ? 4 : 2) * kNI * kNJ < 64 && (RING - 1) * kAll < 64, "ring depth and the vmcnt field");
+    // With two waves to a matrix unit the loads go out between the products, ahead of which they hold the units up; with one,
+    // ahead of them.
+    constexpr bool kEarly = kWaves <= 4;
     constexpr int kSpare = kScales % kWaves ? 256 : 0;      // where the waves without a scale load put zeros
-    constexpr int kLds = RING * kStage + kSpare > TM * kRowBytes ? RING * kStage + kSpare : TM * kRowBytes;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[RING * kStage + kSpare];
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wn = wave / NWM, wm = wave % NWM, r32 = lane & 31, q = lane >> 5;
 
-    // blocks go to the 8 XCDs round robin; each takes a contiguous share of the tiles in an order that walks 8 row tiles per
-    // feature tile, so that the tiles it holds at once share operands through its L2
+    // Blocks go to the 8 XCDs round robin; each XCD takes a contiguous share of the tiles, its workgroups tile by tile in
+    // turn, in an order that walks 8 row tiles per feature tile: the tiles it works on at once share operands through its L2.
     const int ntn = (int)((g.n + TN - 1) / TN), ntm = (int)((g.m + TM - 1) / TM), total = ntn * ntm;
-    const int x = blockIdx.x & 7, loc = blockIdx.x >> 3, jt = x * (total >> 3) + min(x, total & 7) + loc;
-    const int grp = jt / (8 * ntn), in_grp = jt - grp * 8 * ntn, gms = min(8, ntm - grp * 8);
-    const int64_t m0 = (int64_t)(grp * 8 + in_grp % gms) * TM, n0 = (int64_t)(in_grp / gms) * TN;
-
-    const int kb = (int)(g.k / 2), ks = (int)(g.k / 32);
-    const i32x4 wrs = mx_desc(g.w, g.n * kb), ars = mx_desc(g.a, g.m * g.ld_a);
-    const i32x4 wss = mx_desc(g.w_scale, g.n * g.ld_ws), ass = mx_desc(g.a_scale, g.m * g.ld_as);
-    // this lane's source offset of each of the wave's loads at k = 0
-    constexpr int kPer = KB / 16;
-    uint32_t dbase[kLoads], sbase[kScaleLoads];
-    auto chunk = [&](int i) {       // byte offset in a row of the chunk that lands at slot lane % kPer
-        const int row = (wave * kLoads + i) * kBlockRows + lane / kPer, slot = lane % kPer;
-        return 16 * (KB == 64 ? slot ^ (((row >> 1) ^ (row >> 2)) & 3) : slot ^ (row & 7) ^ ((row >> 3) & 1));
+    const int xcd = blockIdx.x & 7, share = gridDim.x >> 3;
+    const int tile_end = (xcd + 1) * (total >> 3) + min(xcd + 1, total & 7);
+    int tile = xcd * (total >> 3) + min(xcd, total & 7) + (int)(blockIdx.x >> 3);
+    auto origin = [&](int j, int& m0, int& n0) {
+        const int grp = j / (8 * ntn), in_grp = j - grp * 8 * ntn, gms = min(8, ntm - grp * 8);
+        m0 = (grp * 8 + in_grp % gms) * TM;
+        n0 = in_grp / gms * TN;
     };
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int row = (wave * kLoads + i) * kBlockRows + lane / kPer;
-        const bool isw = row < TN;
-        const int64_t at = isw ? n0 + row : m0 + row - TN;
-        dbase[i] = at < (isw ? g.n : g.m) ? (uint32_t)(at * (isw ? kb : g.ld_a) + chunk(i)) : kPast;
-    }
-#pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) {
-        const int blk = wave + i * kWaves, row = blk % (kRows / 64) * 64 + lane, plane = blk / (kRows / 64);
-        const bool isw = row < TN;
-        const int64_t at = isw ? n0 + row : m0 + row - TN;
-        sbase[i] = blk < kScales && at < (isw ? g.n : g.m) ? (uint32_t)(at * (isw ? g.ld_ws : g.ld_as) + 4 * plane) : kPast;
-    }
-    const int nk = (kb + KB - 1) / KB;
-    auto issue = [&](int s, int slot) {
-        uint8_t* const sb = smem + slot * kStage;
-        const int k0 = s * KB, s0 = s * (KB / 16);
-        const bool whole = k0 + KB <= kb;      // else, and past k, each lane's offset is checked
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int blk = wave * kLoads + i;
-            if (whole) dma<16>(blk * kBlockRows < TN ? wrs : ars, sb + blk * 1024, dbase[i], (uint32_t)k0);
-            else dma<16>(blk * kBlockRows < TN ? wrs : ars, sb + blk * 1024, k0 + chunk(i) < kb ? dbase[i] + k0 : kPast, 0u);
-        }
+
+    const int kb = (int)(g.k / 2), ks4 = (int)((g.k / 32 + 3) / 4), nk = (kb + KB - 1) / KB;
+    const i32x4 wrs = mx_desc(g.w, g.n * kb), ars = mx_desc(g.a, (g.m - 1) * g.ld_a + kb);    // not past the last row's end
+    const i32x4 wss = mx_desc(g.w_packed, g.n * ks4 * 4), ass = mx_desc(g.a_packed, g.m * ks4 * 4);
+    // The loads go ahead of the products, into the next tile too: lt, ls are the tile and stage that they are at. Load i of
+    // a wave is block wave + i kWaves of the stage, so that every wave's are of the weight first, then of the activations, in
+    // rows a multiple of 16 apart, whose chunks have the same slots. No lane needs a check: rows past an operand lie past its
+    // buffer and are zeros, and what a row's last stage takes from behind the row counts nothing, since both operands' scale
+    // codes there are 0 (the products are below 2^-240).
+    constexpr int kPer = KB / 16, kWLoads = TN / kBlockRows / kWaves, kRowStep = kBlockRows * kWaves;
+    const int lrow = wave * kBlockRows + lane / kPer;
+    const int lchunk = 16 * (KB == 64 ? (lane % kPer) ^ (((lrow >> 1) ^ (lrow >> 2)) & 3) : (lane % kPer) ^ (lrow & 7) ^ ((lrow >> 3) & 1));
+    uint32_t wbase, abase, sbase[kScaleLoads];      // this lane's source offsets at k = 0
+    int lt = tile, ls = 0;
+    auto set_bases = [&]() {
+        int m0, n0;
+        origin(min(lt, total - 1), m0, n0);
+        const bool more = lt < tile_end;            // else nothing but zeros
+        wbase = more ? (uint32_t)(n0 + lrow) * (uint32_t)kb + lchunk : kPast;
+        abase = more ? (uint32_t)(m0 + lrow) * (uint32_t)g.ld_a + lchunk : kPast;
 #pragma unroll
         for (int i = 0; i < kScaleLoads; ++i) {
-            const int blk = wave + i * kWaves, rows64 = blk % (kRows / 64), plane = blk / (kRows / 64);
+            const int blk = wave + i * kWaves, row = blk % (kRows / 64) * 64 + lane, plane = blk / (kRows / 64);
+            const bool isw = row < TN;
+            const int at = isw ? n0 + row : m0 + row - TN, rows = (int)(isw ? g.n : g.m);
+            sbase[i] = more && blk < kScales && at < rows ? (uint32_t)(plane * rows + at) * 4 : kPast;
+        }
+    };
+    // the next stage of the loads into a slot: load i of the wave's kAll, and what follows the last
+    auto load = [&](int slot, int i) {
+        uint8_t* const sb = smem + slot * kStage;
+        if (i < kLoads) {
+            uint8_t* const to = sb + (wave + i * kWaves) * 1024;
+            if (i < kWLoads) dma<16>(wrs, to, wbase + (uint32_t)(i * kRowStep * kb), (uint32_t)(ls * KB));
+            else dma<16>(ars, to, abase + (uint32_t)((i - kWLoads) * kRowStep * (int)g.ld_a), (uint32_t)(ls * KB));
+        } else {
+            const int blk = wave + (i - kLoads) * kWaves;
+            const bool isw = blk % (kRows / 64) * 64 < TN;
             uint8_t* const to = kSpare != 0 && blk >= kScales ? smem + RING * kStage : sb + kCodes + blk * 256;
-            if (whole) dma<4>(rows64 * 64 < TN ? wss : ass, to, sbase[i], (uint32_t)s0);
-            else dma<4>(rows64 * 64 < TN ? wss : ass, to, s0 + 4 * plane < ks ? sbase[i] + s0 : kPast, 0u);
+            dma<4>(isw ? wss : ass, to, sbase[i - kLoads] + (uint32_t)(ls * kPlanes * (int)(isw ? g.n : g.m) * 4), 0u);
+        }
+    };
+    auto advance = [&]() {
+        if (++ls == nk) {
+            ls = 0;
+            lt += share;
+            set_bases();
         }
     };
     struct Ops { v4u w[kNI], a[kNJ]; };
@@ -356,164 +378,202 @@ __global__ __launch_bounds__(64 * NWN * NWM) void mx_tile_kernel(const MxGemmArg
         for (int j = 0; j < kNJ; ++j) o.a[j] = one(arow + 32 * j);
     };
     v16f acc[kNI][kNJ];
-#pragma unroll
-    for (int i = 0; i < kNI; ++i)
-#pragma unroll
-        for (int j = 0; j < kNJ; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     Ops ops[2];
     Scales sc, sc_next;
-    auto multiply = [&](auto u) {
+    // then(n) behind the n-th product
+    auto multiply = [&](auto u, auto then) {
         constexpr int U = decltype(u)::value;
 #pragma unroll
         for (int i = 0; i < kNI; ++i)
 #pragma unroll
-            for (int j = 0; j < kNJ; ++j) acc[i][j] = mfma_mx32<U>(ops[U & 1].w[i], ops[U & 1].a[j], acc[i][j], sc.w[i], sc.a[j]);
+            for (int j = 0; j < kNJ; ++j) {
+                acc[i][j] = mfma_mx32<U>(ops[U & 1].w[i], ops[U & 1].a[j], acc[i][j], sc.w[i], sc.a[j]);
+                then(i * kNJ + j);
+            }
     };
+
+    // stores of a finished tile: straight from the registers, so that the ring keeps filling. A fixed number of them, by
+    // offsets in the tile (out of range for rows and features past the output), which the waits below count.
+    // acc[i][j] register r: feature 32 i + 8 (r / 4) + 4 q + r % 4 of row 32 j + r32 of the wave's tile.
+    constexpr int kStores = (f32 ? 4 : 2) * kNI * kNJ;
+    const bool vec = g.vec_tile;
+    auto store = [&](int m0, int n0) {
+        const int nw = n0 + wrow, mw = m0 + arow - TN;
+        if (vec) {
+            const int size = f32 ? 4 : 2;
+            char* const base = (f32 ? reinterpret_cast<char*>(g.out_f32) : reinterpret_cast<char*>(g.out)) + ((int64_t)m0 * g.ld_out + n0) * size;
+            const auto rs = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, 0x7fffffff, 0x00020000);
 #pragma unroll
-    for (int s = 0; s < RING - 1; ++s) issue(s, s);
-    wait_vmcnt<(RING - 2) * kAll>();
+            for (int j = 0; j < kNJ; ++j) {
+                const uint32_t row = (uint32_t)(arow - TN + 32 * j + r32) * (uint32_t)(g.ld_out * size);
+                const bool in = mw + 32 * j + r32 < g.m;
+#pragma unroll
+                for (int i = 0; i < kNI; ++i) {
+                    const v16f& c = acc[i][j];
+                    if constexpr (f32) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int nb = 32 * i + 8 * b + 4 * q;
+                            const v4f v = {c[4 * b], c[4 * b + 1], c[4 * b + 2], c[4 * b + 3]};
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), rs,
+                                                                   in && nw + nb < g.n ? row + (wrow + nb) * 4 : kPast, 0, 0);
+                        }
+                    } else {
+                        // a lane has four consecutive features of a row; two lanes' halves change places for eight
+#pragma unroll
+                        for (int b = 0; b < 4; b += 2) {
+                            const auto lo = __builtin_amdgcn_permlane32_swap(f32x2_to_bf16x2(c[4 * b], c[4 * b + 1]),
+                                                                             f32x2_to_bf16x2(c[4 * b + 4], c[4 * b + 5]), false, false);
+                            const auto hi = __builtin_amdgcn_permlane32_swap(f32x2_to_bf16x2(c[4 * b + 2], c[4 * b + 3]),
+                                                                             f32x2_to_bf16x2(c[4 * b + 6], c[4 * b + 7]), false, false);
+                            const int nb = 32 * i + 8 * (b + q);
+                            __builtin_amdgcn_raw_buffer_store_b128(v4u{lo[0], hi[0], lo[1], hi[1]}, rs,
+                                                                   in && nw + nb < g.n ? row + (wrow + nb) * 2 : kPast, 0, 0);
+                        }
+                    }
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kNI; ++i)
+#pragma unroll
+            for (int j = 0; j < kNJ; ++j) {
+                const int64_t row = mw + 32 * j + r32;
+                if (row >= g.m) continue;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int64_t nn = nw + 32 * i + 8 * (r / 4) + 4 * q + r % 4;
+                    if (nn >= g.n) continue;
+                    if (f32) g.out_f32[row * g.ld_out + nn] = acc[i][j][r];
+                    else g.out[row * g.ld_out + nn] = (uint16_t)f32_to_bf16(acc[i][j][r]);
+                }
+            }
+        wait_vmcnt<0>();
+    };
+
+    set_bases();
+#pragma unroll
+    for (int s = 0; s < RING; ++s) {
+#pragma unroll
+        for (int i = 0; i < kAll; ++i) load(s, i);
+        advance();
+    }
+    wait_vmcnt<(RING - 1) * kAll>();
     __syncthreads();
     read(0, 0, ops[0]);
     read_scales(0, sc);
     // Of a stage, 64 of k at a time: the next step's operands are read while this one's products run. Ahead of the last
-    // step the next stage has landed (this thread's loads, then everyone's, who are all done with the stage before
-    // this one), and that stage's slot is refilled.
-    int slot = 0;
-    for (int s = 0; s < nk; ++s) {
-        const int next = slot + 1 == RING ? 0 : slot + 1, free = slot == 0 ? RING - 1 : slot - 1;
-        auto inner = [&](auto u) {
-            constexpr int U = decltype(u)::value;
-            if constexpr (U + 1 < kSteps) {
-                read(slot, U + 1, ops[(U + 1) & 1]);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply(u);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-        inner(std::integral_constant<int, 0>());
-        inner(std::integral_constant<int, 1>());
-        inner(std::integral_constant<int, 2>());
-        wait_vmcnt<(RING - 3) * kAll>();
-        __syncthreads();
-        issue(s + RING - 1, free);
-        read(next, 0, ops[0]);
-        read_scales(next, sc_next);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(std::integral_constant<int, kSteps - 1>());
-        __builtin_amdgcn_sched_barrier(0);
-        sc = sc_next;
-        slot = next;
-    }
-    wait_vmcnt<0>();                // the stages past k, before the ring is used again
-
-    // acc[i][j] register r: feature 32 i + 8 (r / 4) + 4 q + r % 4 of row 32 j + r32 of the wave's tile
-    if (g.out_f32) {
+    // step's products the next stage has landed (this thread's loads, then everyone's) and everyone has this stage's last
+    // operands in registers: its slot is refilled. Loads and stores return in order: for the first stages behind a tile's
+    // stores these are younger than the stage waited for.
+    int slot = 0, since = RING;
+    for (; tile < tile_end; tile += share) {
+        int m0, n0;
+        origin(tile, m0, n0);
 #pragma unroll
         for (int i = 0; i < kNI; ++i)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int64_t nb = n0 + wn * (TN / NWN) + 32 * i + 8 * b + 4 * q;
+            for (int j = 0; j < kNJ; ++j)
 #pragma unroll
-                for (int j = 0; j < kNJ; ++j) {
-                    const int64_t row = m0 + wm * (TM / NWM) + 32 * j + r32;
-                    if (row >= g.m) continue;
-                    float* const o = g.out_f32 + row * g.ld_out + nb;
-                    if (g.vec_out && nb + 4 <= g.n) *reinterpret_cast<v4f*>(o) = v4f{acc[i][j][4 * b], acc[i][j][4 * b + 1], acc[i][j][4 * b + 2], acc[i][j][4 * b + 3]};
-                    else
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (nb + r < g.n) o[r] = acc[i][j][4 * b + r];
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+        for (int s = 0; s < nk; ++s) {
+            const int next = slot + 1 == RING ? 0 : slot + 1;
+            auto inner = [&](auto u) {
+                constexpr int U = decltype(u)::value;
+                if constexpr (U + 1 < kSteps) {
+                    read(slot, U + 1, ops[(U + 1) & 1]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    multiply(u, [](int) {});
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            }
-        return;
-    }
-    // bf16: the tile goes through LDS, so that whole rows are stored. Chunk c of row m at slot c ^ (m % 16), its halves
-    // swapped in every other group of 8 and 16 rows: the 8-byte writes of 32 rows at one feature hit distinct banks.
-    __syncthreads();
-    constexpr int kChunks = TN / 8, kMask = kChunks < 16 ? kChunks - 1 : 15;
+            };
+            inner(std::integral_constant<int, 0>());
+            inner(std::integral_constant<int, 1>());
+            inner(std::integral_constant<int, 2>());
+            if (since > RING - 2) wait_vmcnt<(RING - 2) * kAll>();
+            else wait_vmcnt<(RING - 2) * kAll + kStores>();
+            ++since;
+            __syncthreads();         // waits for the LDS reads too
+            if constexpr (kEarly)
 #pragma unroll
-    for (int i = 0; i < kNI; ++i)
+                for (int i = 0; i < kAll; ++i) load(slot, i);
+            read(next, 0, ops[0]);
+            read_scales(next, sc_next);
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int kProducts = kNI * kNJ, kEach = (kAll + kProducts - 1) / kProducts;
+            multiply(std::integral_constant<int, kSteps - 1>(), [&](int n) {
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int c = (wn * (TN / NWN) + 32 * i + 8 * b) / 8;
-#pragma unroll
-            for (int j = 0; j < kNJ; ++j) {
-                const int ml = wm * (TM / NWM) + 32 * j + r32, hs = ((ml >> 3) ^ (ml >> 4)) & 1;
-                *reinterpret_cast<uint2*>(smem + ml * kRowBytes + ((c ^ (ml & kMask)) << 4) + ((q ^ hs) << 3)) =
-                    make_uint2(f32x2_to_bf16x2(acc[i][j][4 * b], acc[i][j][4 * b + 1]), f32x2_to_bf16x2(acc[i][j][4 * b + 2], acc[i][j][4 * b + 3]));
-            }
+                for (int i = 0; i < kEach; ++i)
+                    if (!kEarly && n * kEach + i < kAll) load(slot, n * kEach + i);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            advance();
+            sc = sc_next;
+            slot = next;
         }
-    __syncthreads();
-    const bool vec = (g.ld_out & 7) == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0;
-#pragma unroll 4
-    for (int e = t; e < TM * kChunks; e += 64 * kWaves) {
-        const int ml = e / kChunks, c = e % kChunks;
-        uint4 v = *reinterpret_cast<const uint4*>(smem + ml * kRowBytes + ((c ^ (ml & kMask)) << 4));
-        if (((ml >> 3) ^ (ml >> 4)) & 1) v = make_uint4(v.z, v.w, v.x, v.y);
-        const int64_t row = m0 + ml, nn = n0 + 8 * c;
-        if (row >= g.m) continue;
-        uint16_t* const o = g.out + row * g.ld_out + nn;
-        if (vec && nn + 8 <= g.n) {
-            *reinterpret_cast<uint4*>(o) = v;
-        } else {
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+        store(m0, n0);
+        since = vec ? 0 : RING;
+    }
+    wait_vmcnt<0>();                // the loads past the last tile
+}
+
+__global__ __launch_bounds__(256) void mx_pack_kernel(const uint8_t* scales, int rows, int ks, uint32_t* packed) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int row = (int)(i % rows), j = (int)(i / rows);
+    if (4 * j >= ks) return;
+    uint32_t v = 0;
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (nn + r < g.n) o[r] = (uint16_t)(w4[r >> 1] >> (16 * (r & 1)));
-        }
-    }
+    for (int p = 0; p < 4; ++p)
+        if (4 * j + p < ks) v |= (uint32_t)scales[(int64_t)row * ks + 4 * j + p] << (8 * p);
+    packed[i] = v;
 }
 
-// Scale codes with rows padded to whole dwords (k not a multiple of 128).
-__global__ __launch_bounds__(256) void mx_repack_kernel(const uint8_t* src, int64_t rows, int per, uint8_t* dst, int ld) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * ld; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / ld;
-        const int c = (int)(i - row * ld);
-        dst[i] = c < per ? src[row * per + c] : 0;
-    }
+nhm_status launch_mx_pack(const uint8_t* scales, int64_t rows, int64_t k, uint32_t* packed, hipStream_t st) {
+    const int64_t words = mx_packed_words(rows, k);
+    mx_pack_kernel<<<dim3((unsigned)((words + 255) / 256)), dim3(256), 0, st>>>(scales, (int)rows, (int)(k / 32), packed);
+    count_launch(Kern::kMxPack, rows);
+    return check_launch("mxfp4 scales");
 }
 
-static void mx_repack(const uint8_t* src, int64_t rows, int64_t per, uint8_t* dst, int64_t ld, hipStream_t st) {
-    mx_repack_kernel<<<dim3(mx_blocks(rows * ld)), dim3(256), 0, st>>>(src, rows, (int)per, dst, (int)ld);
-}
-
-template <int TN, int TM, int NWN, int NWM, int KB, int RING>
-static void launch_tile(const MxGemmArgs& g, hipStream_t st) {
-    const int64_t tiles = (g.n + TN - 1) / TN * ((g.m + TM - 1) / TM);
-    mx_tile_kernel<TN, TM, NWN, NWM, KB, RING><<<dim3((unsigned)tiles), dim3(64 * NWN * NWM), 0, st>>>(g);
+// PER_CU: workgroups that a CU holds at once; more tiles than that follow one another in the same workgroups, whose loads
+// then run ahead into the next tile.
+template <int TN, int TM, int NWN, int NWM, int KB, int RING, int PER_CU>
+static void launch_tile(MxGemmArgs g, hipStream_t st) {
+    const int64_t tiles = (g.n + TN - 1) / TN * ((g.m + TM - 1) / TM), most = 256 * PER_CU;
+    const int64_t blocks = tiles < most ? (tiles + 7) / 8 * 8 : most;
+    // stores of 16 bytes at 32-bit offsets within a tile
+    const int64_t size = g.out_f32 ? 4 : 2;
+    const uintptr_t out = g.out_f32 ? reinterpret_cast<uintptr_t>(g.out_f32) : reinterpret_cast<uintptr_t>(g.out);
+    g.vec_tile = out % 16 == 0 && g.ld_out * size % 16 == 0 && g.n * size % 16 == 0 && g.ld_out * size * TM < (int64_t(1) << 31);
+    if (TN * TM < 256 * 256 && g.out_f32) mx_tile_kernel<TN, TM, NWN, NWM, KB, RING, TN * TM < 256 * 256><<<dim3((unsigned)blocks), dim3(64 * NWN * NWM), 0, st>>>(g);
+    else mx_tile_kernel<TN, TM, NWN, NWM, KB, RING, false><<<dim3((unsigned)blocks), dim3(64 * NWN * NWM), 0, st>>>(g);
 }
 
 bool mx_tiled(int64_t m) { return m > 64; }
 
-nhm_status launch_mx_gemm(MxGemmArgs g, uint8_t* pad, hipStream_t st) {
-    const unsigned tiles = (unsigned)((g.n + 15) / 16);
+nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st) {
     if (!mx_tiled(g.m)) {
-        const dim3 block(kMxWaves * 64);
-        if (g.m <= 16) mx_rows_kernel<1><<<dim3(tiles), block, 0, st>>>(g);
-        else if (g.m <= 32) mx_rows_kernel<2><<<dim3(tiles), block, 0, st>>>(g);
-        else mx_rows_kernel<4><<<dim3(tiles), block, 0, st>>>(g);
+        const dim3 grid((unsigned)((g.n + 15) / 16)), block(kMxWaves * 64);
+        if (g.m <= 16) mx_rows_kernel<1><<<grid, block, 0, st>>>(g);
+        else if (g.m <= 32) mx_rows_kernel<2><<<grid, block, 0, st>>>(g);
+        else mx_rows_kernel<4><<<grid, block, 0, st>>>(g);
         count_launch(Kern::kMxRows, g.m);
         return check_launch("mxfp4 linear");
     }
-    const int64_t ks = g.k / 32, ld = (int64_t)align_up((size_t)ks, 4);
-    // a dword load takes four scale codes: rows of them start at a multiple of four
-    if (g.ld_ws != ld || reinterpret_cast<uintptr_t>(g.w_scale) % 4 != 0) {
-        mx_repack(g.w_scale, g.n, ks, pad, ld, st);
-        g.w_scale = pad;
-        g.ld_ws = ld;
-        pad += align_up((size_t)g.n * ld, 256);
-    }
-    if (g.ld_as != ld || reinterpret_cast<uintptr_t>(g.a_scale) % 4 != 0) {
-        mx_repack(g.a_scale, g.m, ks, pad, ld, st);
-        g.a_scale = pad;
-        g.ld_as = ld;
-    }
+    // Tiles by rounds over the chip, us at 15,360 x 10,304 x 2,688 | 15,360 x 2,688 x 4,096 | 2,048 x 10,304 x 2,688: 256 x 256, one to a
+    // CU, 280 | 110 | 49.6 (10, 3 and 2 rounds), 128 x 128, two to a CU, 305 | 104 | 47.7 (19, 5 and 3): a round of the small ones
+    // takes 0.57 of one of the large. While the 128 x 128 tiles do not fill the chip, smaller ones: 477 x 10,304 x 2,688 17.5 with 128 x 128
+    // (324 tiles), 19.3 with 128 x 64, 19.9 with 64 x 64; 1,024 x 4,096 x 4,096 17.4 (256), 16.8, 18.5; 477 x 2,688 x 4,096 14.8 (84), 10.9
+    // (168), 10.1 (336).
     auto count = [&](int64_t tn, int64_t tm) { return (g.n + tn - 1) / tn * ((g.m + tm - 1) / tm); };
-    if (count(256, 256) >= 160) launch_tile<256, 256, 2, 4, 64, 4>(g, st);
-    else if (count(128, 128) >= 200) launch_tile<128, 128, 2, 2, 128, 4>(g, st);
-    else launch_tile<64, 64, 2, 2, 128, 4>(g, st);
+    const int64_t rounds256 = (count(256, 256) + 255) / 256, rounds128 = (count(128, 128) + 511) / 512;
+    // (f32 outputs of a 256 x 256 tile do not fit the registers beside its sums: 405 us.)
+    if (!g.out_f32 && count(256, 256) > 256 && rounds256 * 100 < rounds128 * 57) launch_tile<256, 256, 2, 4, 64, 4, 1>(g, st);
+    else if (count(128, 128) >= 300) launch_tile<128, 128, 2, 2, 128, 2, 2>(g, st);
+    else if (count(128, 64) >= 400) launch_tile<128, 64, 2, 2, 128, 2, 3>(g, st);
+    else launch_tile<64, 64, 2, 2, 128, 2, 4>(g, st);
     count_launch(Kern::kMxTile, g.m);
     return check_launch("mxfp4 linear");
 }

@@ -30,7 +30,7 @@ enum class Kern : int {
     kRing256x128Exact, kRing256x256, kRing256x256Exact, kPanel64x128, kPanel64x128Exact, kTile128,
     kTile128Exact, kSplitkReduce, kDecodeSsm, kGnormQuant, kClear, kConvFwd, kSsdState, kSsdPass, kSsdOut,
     kLoraDown, kLoraRows, kLoraRowsExact, kBeamRows, kBeamPick, kBeamReorder, kBatchPlan,
-    kMxQuant, kMxDequant, kMxRows, kMxTile, kConvPrefill, kConvDecode, kScanPrefill, kScanDecode, kScoreRows,
+    kMxQuant, kMxDequant, kMxPack, kMxRows, kMxTile, kConvPrefill, kConvDecode, kScanPrefill, kScanDecode, kScoreRows,
     kScoreJoin, kCount
 };
 void count_launch(Kern k, int64_t rows);
@@ -354,7 +354,8 @@ struct MxQuantArgs {
     int64_t ld_codes;
     uint8_t* scales;               // [rows, ld_scales]
     int64_t ld_scales;
-    int32_t pad = 0;               // scale codes behind a row's that are set to 0
+    // non-null: the scale codes in the tile kernels' layout (launch_mx_pack) instead of scales
+    uint32_t* packed = nullptr;
 };
 nhm_status launch_mx_quant(const MxQuantArgs& a, bool f32, hipStream_t st);
 struct MxDequantArgs {
@@ -374,15 +375,20 @@ struct MxGemmArgs {
     const uint8_t* w;              // codes [n, k / 2]
     const uint8_t* w_scale;        // [n, ld_ws]
     int64_t ld_ws, n, k;
+    const uint32_t* a_packed;      // the tile kernels': scale codes as launch_mx_pack lays them out
+    const uint32_t* w_packed;
     uint16_t* out;                 // bf16 [m, ld_out], or nullptr with out_f32
     float* out_f32;
     int64_t ld_out;
     bool vec_out;                  // rows aligned for stores of four features
+    bool vec_tile = false;         // rows and features in whole 16 bytes (the tile kernels' launch sets it)
 };
-// Whether m rows run on the tile kernels, which take scale codes by dwords: pad is room for copies of the weight's
-// and the activations' with rows of a multiple of 4 bytes, where theirs are not.
+// Whether m rows run on the tile kernels, which take scale codes packed: dword (j, row) at [j * rows + row] holds those of
+// the row's blocks 4 j .. 4 j + 3 (zeros past the row), mx_packed_words(rows, k) in all.
 bool mx_tiled(int64_t m);
-nhm_status launch_mx_gemm(MxGemmArgs g, uint8_t* pad, hipStream_t st);
+inline int64_t mx_packed_words(int64_t rows, int64_t k) { return rows * ((k / 32 + 3) / 4); }
+nhm_status launch_mx_pack(const uint8_t* scales, int64_t rows, int64_t k, uint32_t* packed, hipStream_t st);
+nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st);
 
 // ---- scoring of tokens (score.hip)
 struct ScoreStrip { double sum, mom; float top; uint32_t count; };

@@ -53,10 +53,19 @@ typedef struct nhm_mxfp4_weight {
     const uint8_t* scale;  /* (device) scale codes [n, k / 32]               */
     int64_t n;             /* output features                                */
     int64_t k;             /* input features, k % 32 == 0                    */
+    const uint32_t* packed_scale; /* (device) nhm_mxfp4_pack_scales of scale, or NULL: packed
+                              in the workspace by every call of more than 64 rows   */
 } nhm_mxfp4_weight;
 
-/* Workspace bytes of nhm_mxfp4_linear (0 for m, n or k <= 0): the codes and scales of a bf16 input, and copies of scale codes
- * whose rows the tile kernels cannot take as they are (k not a multiple of 128, or not 4-byte aligned). */
+/* A weight's scale codes in the order in which the kernels for many rows take them, made once where the weight is
+ * loaded: dword [j, row] of packed [ceil(k / 128), n] holds the codes of the row's blocks 4 j .. 4 j + 3, the first in the
+ * low byte, 0 past the row. packed: (device, 4-byte aligned) nhm_mxfp4_packed_scale_bytes(n, k) bytes.
+ * Errors: NHM_ERR_NULL, NHM_ERR_SHAPE, NHM_ERR_ALIGN, NHM_ERR_UNSUPPORTED (2 GiB or more), NHM_ERR_HIP. */
+NHM_API size_t nhm_mxfp4_packed_scale_bytes(int64_t n, int64_t k);
+NHM_API nhm_status nhm_mxfp4_pack_scales(const uint8_t* scale, int64_t n, int64_t k, uint32_t* packed, void* stream);
+
+/* Workspace bytes of nhm_mxfp4_linear (0 for m, n or k <= 0): the codes and scales of a bf16 input, and past 64 rows the
+ * packed scales of both operands. */
 NHM_API size_t nhm_mxfp4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, nhm_dtype a_type);
 
 /* out[i, j] = sum_k val(a[i, k]) val(w[j, k]), summed in f32 (within 2^-24 of sum |a w| per 128 products), rounded

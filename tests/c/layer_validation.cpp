@@ -35,7 +35,8 @@ nhm_status launch_scan_prefill(ScanPrefillArgs, void*, hipStream_t) { reached("l
 nhm_status launch_mx_quant(const MxQuantArgs&, bool, hipStream_t) { reached("launch_mx_quant"); }
 nhm_status launch_mx_dequant(const MxDequantArgs&, hipStream_t) { reached("launch_mx_dequant"); }
 bool mx_tiled(int64_t m) { return m > 64; }
-nhm_status launch_mx_gemm(MxGemmArgs, uint8_t*, hipStream_t) { reached("launch_mx_gemm"); }
+nhm_status launch_mx_pack(const uint8_t*, int64_t, int64_t, uint32_t*, hipStream_t) { reached("launch_mx_pack"); }
+nhm_status launch_mx_gemm(const MxGemmArgs&, hipStream_t) { reached("launch_mx_gemm"); }
 size_t score_ws_bytes(int64_t rows, int64_t, int32_t) { return (size_t)rows * 16; }
 nhm_status launch_score(ScoreArgs, void*, hipStream_t) { reached("launch_score"); }
 }  // namespace nhm
@@ -67,15 +68,18 @@ int main() {
         EXPECT(nhm_mxfp4_quantize(H, NHM_BF16, 4, v, INT64_MAX, Q, INT64_MAX, Q, INT64_MAX, nullptr), NHM_ERR_SHAPE);
         EXPECT(nhm_mxfp4_dequantize(Q, 32, Q, 2, v, 64, H, 64, nullptr), NHM_ERR_SHAPE);
         if (v > 0) EXPECT(nhm_mxfp4_quantize(H, NHM_BF16, 4, 64, v, Q, 32, Q, 2, nullptr), NHM_ERR_SHAPE);
-        nhm_mxfp4_weight w = {Q, Q, v, 64};
+        nhm_mxfp4_weight w = {Q, Q, v, 64, nullptr};
         EXPECT(nhm_mxfp4_linear(H, NHM_BF16, nullptr, 4, 64, &w, H, NHM_BF16, INT64_MAX, WS, SIZE_MAX, nullptr), NHM_ERR_SHAPE);
-        w = nhm_mxfp4_weight{Q, Q, 64, v};
+        w = nhm_mxfp4_weight{Q, Q, 64, v, nullptr};
         EXPECT(nhm_mxfp4_linear(H, NHM_BF16, nullptr, 4, INT64_MAX, &w, H, NHM_BF16, 64, WS, SIZE_MAX, nullptr), NHM_ERR_SHAPE);
-        w = nhm_mxfp4_weight{Q, Q, 64, 64};
+        w = nhm_mxfp4_weight{Q, Q, 64, 64, nullptr};
         EXPECT(nhm_mxfp4_linear(H, NHM_BF16, nullptr, v, 64, &w, H, NHM_BF16, 64, WS, SIZE_MAX, nullptr), NHM_ERR_SHAPE);
         nhm_mxfp4_linear_workspace_bytes(v, v, v, NHM_BF16);
+        EXPECT(nhm_mxfp4_pack_scales(Q, v, 64, P<uint32_t>(0x60000), nullptr), NHM_ERR_SHAPE);
+        EXPECT(nhm_mxfp4_pack_scales(Q, 64, v, P<uint32_t>(0x60000), nullptr), NHM_ERR_SHAPE);
+        EXPECT(nhm_mxfp4_packed_scale_bytes(v, 64), 0);
     }
-    const nhm_mxfp4_weight w = {Q, Q, 64, 64};
+    const nhm_mxfp4_weight w = {Q, Q, 64, 64, nullptr};
     EXPECT(nhm_mxfp4_linear(H, (nhm_dtype)INT_MIN, nullptr, 4, 64, &w, H, NHM_BF16, 64, WS, SIZE_MAX, nullptr), NHM_ERR_UNSUPPORTED);
     EXPECT(nhm_mxfp4_linear(H, NHM_BF16, nullptr, 4, 64, &w, H, (nhm_dtype)77, 64, WS, SIZE_MAX, nullptr), NHM_ERR_UNSUPPORTED);
     EXPECT(nhm_mxfp4_linear(H, NHM_BF16, nullptr, INT_MAX, 64, &w, H, NHM_BF16, 64, WS, SIZE_MAX, nullptr), NHM_ERR_UNSUPPORTED);

@@ -28,7 +28,7 @@ def check(nhm, call, cases):
 def test_every_declared_symbol_is_exported(nhm):
     txt = open(os.path.join(ROOT, "include", "nhm_layer.h")).read()
     names = sorted(set(re.findall(r"NHM_API\s+[\w\s\*]+?\b(nhm_\w+)\s*\(", txt)))
-    assert len(names) == 11 and all(n in nhm._SIGS and hasattr(nhm.lib, n) for n in names), names
+    assert len(names) == 13 and all(n in nhm._SIGS and hasattr(nhm.lib, n) for n in names), names
 
 
 def test_mxfp4_refusals(nhm):
@@ -58,8 +58,8 @@ def test_mxfp4_linear_refusals(nhm):
     assert nhm.mxfp4_linear_workspace_bytes(32, 64, 128, nhm.NHM_MXFP4) % 256 == 0
     assert nhm.mxfp4_linear_workspace_bytes(0, 64, 128, nhm.NHM_BF16) == 0
 
-    def call(a=A, t=nhm.NHM_BF16, sa=None, m=32, lda=128, w=W, s=S, n=64, k=128, o=O, ot=nhm.NHM_BF16, ldo=64, ws=WS, wsb=need):
-        wt = nhm._Mxfp4Weight(w, s, n, k)
+    def call(a=A, t=nhm.NHM_BF16, sa=None, m=32, lda=128, w=W, s=S, n=64, k=128, o=O, ot=nhm.NHM_BF16, ldo=64, ws=WS, wsb=need, p=None):
+        wt = nhm._Mxfp4Weight(w, s, n, k, p)
         return nhm.lib.nhm_mxfp4_linear(a, t, sa, m, lda, C.byref(wt), o, ot, ldo, ws, wsb, None)
 
     assert call(m=0) == 0 and call(m=0, a=None, o=None, ws=None, wsb=0) == 0
@@ -68,10 +68,19 @@ def test_mxfp4_linear_refusals(nhm):
                       (dict(t=1), 4), (dict(t=2), 4), (dict(ot=1), 4), (dict(ot=3), 4), (dict(m=-1), 2), (dict(n=0), 2), (dict(k=0), 2),
                       (dict(k=112), 2), (dict(lda=120), 2), (dict(codes, lda=63), 2), (dict(ldo=63), 2), (dict(a=A + 8), 3),
                       (dict(lda=132), 3), (dict(codes, lda=72), 3), (dict(w=W + 8), 3), (dict(o=O + 1), 3),
-                      (dict(ot=nhm.NHM_F32, o=O + 2), 3), (dict(ws=WS + 16), 3), (dict(ws=None), 5), (dict(wsb=need - 1), 5),
+                      (dict(ot=nhm.NHM_F32, o=O + 2), 3), (dict(ws=WS + 16), 3), (dict(ws=None), 5), (dict(wsb=need - 1), 5), (dict(p=S + 2), 3),
                       (dict(n=1 << 20, k=4096, lda=4096, ldo=1 << 20, wsb=1 << 60), 4),
                       (dict(codes, m=1 << 20, lda=4096, wsb=1 << 60), 4)])
     assert nhm.lib.nhm_mxfp4_linear(A, 0, None, 4, 64, None, O, 0, 64, WS, need, None) == 1
+    size = nhm.lib.nhm_mxfp4_packed_scale_bytes
+    assert size(10, 128) == 40 and size(10, 160) == 80 and size(10, 100) == 0 and size(0, 128) == 0
+
+    def pack(s=S, n=10, k=160, p=W):
+        return nhm.lib.nhm_mxfp4_pack_scales(s, n, k, p, None)
+
+    assert pack(n=0, s=None, p=None) == 0
+    check(nhm, pack, [(dict(s=None), 1), (dict(p=None), 1), (dict(n=-1), 2), (dict(k=100), 2), (dict(p=W + 2), 3),
+                      (dict(n=1 << 30, k=128), 4)])
 
 
 def test_conv_refusals(nhm):
