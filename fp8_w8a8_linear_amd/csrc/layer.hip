@@ -15,6 +15,7 @@ bool rows16(const void* p, int64_t ld_bytes) { return aligned(p, 16) && ld_bytes
 constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
 constexpr int64_t kMaxLd = int64_t(1) << 40;           // row strides: offsets stay within 63 bits
 constexpr int64_t kMaxOperand = int64_t(1) << 31;      // bytes behind a buffer descriptor
+constexpr int64_t kMaxScanLd = int64_t(1) << 23;       // 80 rows of bf16 within 31 bits
 constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxRows = int64_t(1) << 24;
 constexpr int kMaxTop = 64;
 
@@ -76,6 +77,8 @@ nhm_status scan_args(ScanDecodeArgs& a, const nhm_scan_params* p, const uint16_t
     for (int i = 0; i < 6; ++i)
         if (lds[i] < (i == 2 || i == 3 ? p->d_state : p->dim) || lds[i] > kMaxLd)
             return fail(NHM_ERR_SHAPE, "scan: a leading dimension of %lld is out of range", (long long)lds[i]);
+    for (int i = 0; i < 6; ++i)
+        if (lds[i] > kMaxScanLd) return fail(NHM_ERR_UNSUPPORTED, "scan: a leading dimension of more than 2^23");
     if (!p->A_log || !pool || !slot_idx || (rows > 0 && (!u || !dt || !B || !C || !out)))
         return fail(NHM_ERR_NULL, "scan: A_log, u, dt, B, C, slot_idx, ssm_pool or out is NULL");
     if (!aligned(p->A_log, 16) || !aligned(pool, 16) || !aligned(p->D, 4) || !aligned(p->dt_bias, 4) || !aligned(slot_idx, 4) ||

@@ -35,46 +35,50 @@ __device__ __forceinline__ bool has_slot(int slot, int n_slots) { return slot >=
 
 // ---------------------------------------------------------------- scan of prompts
 //
-// A lane holds one state of one channel (R of them where d_state > 16): 16 lanes, a row of the wave, are a
-// channel, a wave is four, a workgroup of four waves 16. What a token needs of its channel, dt and dt u, is formed
-// once per 16 tokens by the row's lanes, a token each, and handed to the row by lane moves that the
-// multiplications take in. A token then costs mul, exp2, mul, fma, mul per state, and the sum over the row: the
-// 16 tokens' products are summed together, each step keeping half of the tokens in half of the lanes, so that
-// lane l ends with token l's sum, beside the u and z of that token that it loaded. B and C of 16 to 64 tokens
-// are in LDS as f32, transposed, for the whole workgroup; loads are one such block ahead.
+// A lane holds one state of one channel (R of them where d_state > 16): 16 lanes are a channel, a wave is four, a
+// workgroup of four waves 16. What a token needs of its channel, dt and dt u, is formed once per 16 tokens by the
+// channel's lanes, a token each, and read back from LDS by all of them, as are B and C, staged as f32, transposed, for
+// the whole workgroup, 16 to 64 tokens at a time; loads are one such block ahead. (Lane moves inside the multiplications
+// halve their rate: 8.4 cycles against 4.5.) A token then costs mul, exp2, mul, fma, mul per state, and the sum over the
+// channel's lanes: the 16 tokens' products are summed together, each step keeping half of the tokens in half of the
+// lanes, so that the lane of state n ends with token n's sum, beside the u and z of that token that it loaded. The lanes of
+// a channel are those of equal bits 2 and 3: the steps over bits 5 and 4 are swaps of two registers' halves and an add.
 
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true));
 }
-template <int T>
-__device__ __forceinline__ float row_token(float v) { return dpp<0x150 + T>(v); }    // row_newbcast: lane T of the row
+__device__ __forceinline__ int lane_state(int lane) { return (lane >> 4) * 4 + (lane & 3); }
+__device__ __forceinline__ int lane_channel(int lane) { return (lane >> 2) & 3; }
 
-// Lane l of each row: the sum over the row of p[l].
-__device__ __forceinline__ float row_sums(const float (&p)[16], int lane) {
-    const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+// The sums over a channel's lanes of two registers, the first's in the lanes with a clear bit 5 (or 4), the second's in the others.
+__device__ __forceinline__ float swap32_sum(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap16_sum(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// The lane of state n: the sum over its channel of p[n].
+__device__ __forceinline__ float channel_sums(const float (&p)[16], int lane) {
+    const bool b1 = lane & 2, b0 = lane & 1;
     float a[8], b[4], c[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = (b3 ? p[i + 8] : p[i]) + dpp<0x128>(b3 ? p[i] : p[i + 8]);   // row_ror:8
+    for (int i = 0; i < 8; ++i) a[i] = swap32_sum(p[i], p[i + 8]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = (b2 ? a[i + 4] : a[i]) + dpp<0x141>(b2 ? a[i] : a[i + 4]);   // row_half_mirror
+    for (int i = 0; i < 4; ++i) b[i] = swap16_sum(a[i], a[i + 4]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) c[i] = (b1 ? b[i + 2] : b[i]) + dpp<0x4E>(b1 ? b[i] : b[i + 2]);    // xor 2
     return (b0 ? c[1] : c[0]) + dpp<0xB1>(b0 ? c[0] : c[1]);                                        // xor 1
 }
 
-template <int T, int R, bool kOut, typename F>
-__device__ __forceinline__ void scan_tokens(float (&h)[R], const float (&A2)[R], float dt, float du, const F& bc,
-                                            float (&p)[16]) {
-    float sum = 0.f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float e = __builtin_amdgcn_exp2f(row_token<T>(dt) * A2[r]);
-        h[r] = fmaf(e, h[r], row_token<T>(du) * bc(0, r, T));
-        if constexpr (kOut) sum = r == 0 ? h[r] * bc(1, r, T) : fmaf(h[r], bc(1, r, T), sum);
-    }
-    if constexpr (kOut) p[T] = sum;
-    if constexpr (T + 1 < 16) scan_tokens<T + 1, R, kOut>(h, A2, dt, du, bc, p);
+// Rows t0 .. end - 1 of a bf16 tensor of row stride ld behind a buffer descriptor: offsets from row t0, rows past the end read
+// as zeros and are not written. Offsets of up to 80 rows stay within 31 bits for ld <= kMaxScanLd.
+constexpr uint32_t kPastRow = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const uint16_t* p, int64_t ld, int64_t t0, int64_t end) {
+    const int64_t bytes = (end - t0) * ld * 2;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p + t0 * ld), (short)0, (int)min(bytes, (int64_t)0x7fffffff), 0x00020000);
 }
 
 constexpr int kScanWaves = 4, kScanChannels = 4 * kScanWaves;   // channels of a workgroup
@@ -88,7 +92,8 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
     constexpr int kTiles = kBlock / 16, kRowsN = 16 * R, kStep = kScanWaves * 64 / kRowsN;
     constexpr bool kOut = kMode != 1;
     __shared__ __attribute__((aligned(16))) float s_bc[2][2][kRowsN][kBlock + 4];   // odd multiples of 16 bytes a row
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, l16 = lane & 15;
+    __shared__ __attribute__((aligned(16))) float s_dt[kScanWaves][2][4][16 + 4];   // a tile's dt and dt u of a wave
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, l16 = lane_state(lane), chan = lane_channel(lane);
     // Units of four workgroups, whose channels share 128-byte lines, follow one another on one XCD (block b runs
     // on XCD b % 8): the lines come from memory once. The last units, past the sequences, zero the rows behind them.
     const int lines = (a.dim + 4 * kScanChannels - 1) / (4 * kScanChannels);
@@ -99,7 +104,7 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
     const int seq = (int)(sc / chunks), chunk = (int)(sc % chunks);
     const int ch0 = ((int)(unit % lines) * 4 + (int)(j & 3)) * kScanChannels;
     if (seq > a.n_seqs || ch0 >= a.dim) return;
-    const int ch = ch0 + wave * 4 + (lane >> 4);
+    const int ch = ch0 + wave * 4 + chan;
     const bool on = ch < a.dim;
     const int chc = on ? ch : a.dim - 1;
     if (seq == a.n_seqs) {
@@ -151,34 +156,42 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
     const float bias = a.dt_bias ? a.dt_bias[chc] : 0.f;
     const float Dc = a.D ? a.D[chc] : 0.f;
 
-    // a block's loads: u, dt, z of this lane's token of each tile, and this thread's share of B and C
-    uint16_t ru[kTiles], rdt[kTiles], rz[kTiles], rb[4], rc[4];
+    // A block's loads: u, dt, z of this lane's token of each tile, and this thread's share of B and C, at offsets from the
+    // block's first token that stay the same; its rows end where the sequence does (zeros past that).
+    const uint32_t uoff = on ? (uint32_t)(l16 * (int)a.ld_u + ch) * 2 : kPastRow, dtoff = on ? (uint32_t)(l16 * (int)a.ld_dt + ch) * 2 : kPastRow,
+                   zoff = on ? (uint32_t)(l16 * (int)a.ld_z + ch) * 2 : kPastRow, ooff = on ? (uint32_t)(l16 * (int)a.ld_out + ch) * 2 : kPastRow;
     const int nb = t % kRowsN, tb = t / kRowsN;
-    const bool nin = nb < a.d_state;
+    const uint32_t boff = nb < a.d_state ? (uint32_t)(tb * (int)a.ld_b + nb) * 2 : kPastRow, coff = nb < a.d_state ? (uint32_t)(tb * (int)a.ld_c + nb) * 2 : kPastRow;
+    uint16_t ru[kTiles], rdt[kTiles], rz[kTiles], rb[4], rc[4];
     auto load = [&](int64_t t0) {
+        const auto rsu = rows_from(a.u, a.ld_u, t0, end), rsd = rows_from(a.dt, a.ld_dt, t0, end), rsb = rows_from(a.B, a.ld_b, t0, end);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-            const int64_t tok = min(t0 + 16 * i + l16, end - 1);
-            ru[i] = a.u[tok * a.ld_u + chc];
-            rdt[i] = a.dt[tok * a.ld_dt + chc];
-            if (kOut && a.z) rz[i] = a.z[tok * a.ld_z + chc];
+            ru[i] = __builtin_amdgcn_raw_buffer_load_b16(rsu, uoff + (uint32_t)(i * 32 * (int)a.ld_u), 0, 0);
+            rdt[i] = __builtin_amdgcn_raw_buffer_load_b16(rsd, dtoff + (uint32_t)(i * 32 * (int)a.ld_dt), 0, 0);
+        }
+        if (kOut && a.z) {
+            const auto rsz = rows_from(a.z, a.ld_z, t0, end);
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) rz[i] = __builtin_amdgcn_raw_buffer_load_b16(rsz, zoff + (uint32_t)(i * 32 * (int)a.ld_z), 0, 0);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t tok = min(t0 + tb + kStep * k, end - 1);
-            rb[k] = a.B[tok * a.ld_b + (nin ? nb : 0)];
-            if (kOut) rc[k] = a.C[tok * a.ld_c + (nin ? nb : 0)];
+        for (int k = 0; k < 4; ++k) rb[k] = __builtin_amdgcn_raw_buffer_load_b16(rsb, boff + (uint32_t)(k * kStep * 2 * (int)a.ld_b), 0, 0);
+        if constexpr (kOut) {
+            const auto rsc = rows_from(a.C, a.ld_c, t0, end);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rc[k] = __builtin_amdgcn_raw_buffer_load_b16(rsc, coff + (uint32_t)(k * kStep * 2 * (int)a.ld_c), 0, 0);
         }
     };
     float dt_sum = 0.f;
     if (beg < end) load(beg);
     int buf = 0;
     for (int64_t t0 = beg; t0 < end; t0 += kBlock) {
-        // past the sequence's end (and d_state) B is zero and dt too: the state stays, whatever is held there
+        // past the sequence's end (and d_state) B is zero and dt too: the state stays
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            s_bc[buf][0][nb][tb + kStep * k] = nin && t0 + tb + kStep * k < end ? bf16_to_f32(rb[k]) : 0.f;
-            if (kOut) s_bc[buf][1][nb][tb + kStep * k] = nin ? bf16_to_f32(rc[k]) : 0.f;
+            s_bc[buf][0][nb][tb + kStep * k] = bf16_to_f32(rb[k]);
+            if (kOut) s_bc[buf][1][nb][tb + kStep * k] = bf16_to_f32(rc[k]);
         }
         float u[kTiles], dt[kTiles], z[kTiles];
 #pragma unroll
@@ -189,13 +202,22 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
         }
         __syncthreads();     // this block is in LDS, and everyone has read the one before the last
         if (t0 + kBlock < end) load(t0 + kBlock);
+        const int left = (int)min(end - t0, (int64_t)kBlock);
+        const auto rso = rows_from(a.out, a.ld_out, t0, end);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-            if (t0 + 16 * i >= end) break;
-            const bool live = t0 + 16 * i + l16 < end;
-            const float d = live ? softplus_series(dt[i] + bias) : 0.f;
-            const float du = live ? d * u[i] : 0.f;
+            if (16 * i >= left) break;
+            const float d = 16 * i + l16 < left ? softplus_series(dt[i] + bias) : 0.f;
             if (kMode == 1) dt_sum += d;
+            s_dt[wave][0][chan][l16] = d;
+            s_dt[wave][1][chan][l16] = d * u[i];
+            wave_lds_order();
+            v4f dts[2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dts[m][k] = *reinterpret_cast<const v4f*>(&s_dt[wave][m][chan][4 * k]);
+            wave_lds_order();
             v4f bc[kOut ? 2 : 1][R][4];
 #pragma unroll
             for (int m = 0; m < (kOut ? 2 : 1); ++m)
@@ -205,11 +227,19 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
                     for (int k = 0; k < 4; ++k)
                         bc[m][r][k] = *reinterpret_cast<const v4f*>(&s_bc[buf][m][l16 + 16 * r][16 * i + 4 * k]);
             float p[16];
-            scan_tokens<0, R, kOut>(h, A2, d, du, [&](int m, int r, int k) { return bc[kOut ? m : 0][r][k >> 2][k & 3]; }, p);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float e = __builtin_amdgcn_exp2f(dts[0][k >> 2][k & 3] * A2[r]);
+                    h[r] = fmaf(e, h[r], dts[1][k >> 2][k & 3] * bc[0][r][k >> 2][k & 3]);
+                    if constexpr (kOut) p[k] = r == 0 ? h[r] * bc[1][r][k >> 2][k & 3] : fmaf(h[r], bc[1][r][k >> 2][k & 3], p[k]);
+                }
+            }
             if constexpr (kOut) {
-                float y = fmaf(Dc, u[i], row_sums(p, lane));
+                float y = fmaf(Dc, u[i], channel_sums(p, lane));
                 if (a.z) y *= silu(z[i]);
-                if (live && on) a.out[(t0 + 16 * i + l16) * a.ld_out + ch] = (uint16_t)f32_to_bf16(y);
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f32_to_bf16(y), rso, ooff + (uint32_t)(i * 32 * (int)a.ld_out), 0, 0);
             }
         }
         buf ^= 1;
@@ -219,8 +249,8 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (l16 + 16 * r < a.d_state) ws_state(chunk + 1)[l16 + 16 * r] = h[r];
-            dt_sum += dpp<0x128>(dt_sum);
-            dt_sum += dpp<0x141>(dt_sum);
+            dt_sum = swap32_sum(dt_sum, dt_sum);
+            dt_sum = swap16_sum(dt_sum, dt_sum);
             dt_sum += dpp<0x4E>(dt_sum);
             dt_sum += dpp<0xB1>(dt_sum);
             if (l16 == 0) a.ws_dt[((int64_t)seq * a.n_chunks + chunk) * a.dim + ch] = dt_sum;

@@ -123,7 +123,7 @@ typedef struct nhm_scan_params {
  *   out_t[c] = (sum_n C_t[n] h_t[c, n] + D[c] u_t[c]) silu(z_t[c])      (without silu(z) where z is NULL)
  * in f32, out rounded once; a bf16 pool's states are widened when read and rounded when written, as the mixer's.
  *   u, dt, z, out (device) bf16 [n_tokens or batch, ld_*], dim columns; 2-byte aligned: slices of wider
- *                 rows (a projection's output) are taken as they are
+ *                 rows (a projection's output) are taken as they are; row strides of at most 2^23
  *   B, C          (device) bf16 [.., ld_*], d_state columns, shared by the channels; likewise
  *   ssm_pool      (device) f32 or bf16 (ssm_type) [n_slots, dim, d_state], 16-byte aligned; updated in place
  *   ws            (device, 256-byte aligned) nhm_selective_scan_prefill_workspace_bytes(...) bytes (may be 0: NULL)

@@ -135,7 +135,7 @@ def test_scan_refusals(nhm):
     both = [(dict(a=None), 1), (dict(u=None), 1), (dict(dt=None), 1), (dict(b=None), 1), (dict(c=None), 1), (dict(sl=None), 1),
             (dict(sp=None), 1), (dict(o=None), 1), (dict(dim=0), 2), (dict(n=0), 2), (dict(slots=0), 2), (dict(ldu=63), 2),
             (dict(lddt=63), 2), (dict(ldb=15), 2), (dict(ldc=15), 2), (dict(ldz=63), 2), (dict(ldo=63), 2), (dict(dim=60), 4),
-            (dict(n=6), 4), (dict(n=68, ldb=68, ldc=68), 4), (dict(t=1), 4), (dict(t=9), 4), (dict(a=A + 4), 3), (dict(sp=SP + 8), 3),
+            (dict(n=6), 4), (dict(n=68, ldb=68, ldc=68), 4), (dict(ldu=(1 << 23) + 1), 4), (dict(t=1), 4), (dict(t=9), 4), (dict(a=A + 4), 3), (dict(sp=SP + 8), 3),
             (dict(d=D + 2), 3), (dict(bi=BI + 1), 3), (dict(u=U + 1), 3), (dict(z=Z + 1), 3), (dict(sl=SL + 2), 3), (dict(o=O + 1), 3)]
     check(nhm, dec, both + [(dict(batch=-1), 2)])
     check(nhm, pre, both + [(dict(T=-1), 2), (dict(ns=-1), 2), (dict(cu=None), 1), (dict(hi=None), 1), (dict(cu=CU + 2), 3)])
