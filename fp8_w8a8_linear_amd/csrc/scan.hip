@@ -89,10 +89,12 @@ constexpr int kScanWaves = 4, kScanChannels = 4 * kScanWaves;   // channels of a
 template <int R, int kMode>
 __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const ScanPrefillArgs a) {
     constexpr int kBlock = R == 1 ? 64 : R == 2 ? 32 : 16;      // tokens staged at a time
-    constexpr int kTiles = kBlock / 16, kRowsN = 16 * R, kStep = kScanWaves * 64 / kRowsN;
+    constexpr int kTiles = kBlock / 16, kRowsN = 16 * R;
     constexpr bool kOut = kMode != 1;
     __shared__ __attribute__((aligned(16))) float s_bc[2][2][kRowsN][kBlock + 4];   // odd multiples of 16 bytes a row
-    __shared__ __attribute__((aligned(16))) float s_dt[kScanWaves][2][4][16 + 4];   // a tile's dt and dt u of a wave
+    __shared__ __attribute__((aligned(16))) float s_dt[2][2][kScanChannels][kBlock + 4];   // dt and dt u
+    __shared__ uint32_t s_uz[kOut ? 2 : 1][kScanChannels][kBlock + 4];                      // u and z
+    __shared__ __attribute__((aligned(8))) uint16_t s_y[kOut ? 2 : 1][kBlock][kScanChannels + 4];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, l16 = lane_state(lane), chan = lane_channel(lane);
     // Units of four workgroups, whose channels share 128-byte lines, follow one another on one XCD (block b runs
     // on XCD b % 8): the lines come from memory once. The last units, past the sequences, zero the rows behind them.
@@ -153,79 +155,72 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
             }
         }
     }
-    const float bias = a.dt_bias ? a.dt_bias[chc] : 0.f;
     const float Dc = a.D ? a.D[chc] : 0.f;
 
-    // A block's loads: u, dt, z of this lane's token of each tile, and this thread's share of B and C, at offsets from the
-    // block's first token that stay the same; its rows end where the sequence does (zeros past that).
-    const uint32_t uoff = on ? (uint32_t)(l16 * (int)a.ld_u + ch) * 2 : kPastRow, dtoff = on ? (uint32_t)(l16 * (int)a.ld_dt + ch) * 2 : kPastRow,
-                   zoff = on ? (uint32_t)(l16 * (int)a.ld_z + ch) * 2 : kPastRow, ooff = on ? (uint32_t)(l16 * (int)a.ld_out + ch) * 2 : kPastRow;
-    const int nb = t % kRowsN, tb = t / kRowsN;
-    const uint32_t boff = nb < a.d_state ? (uint32_t)(tb * (int)a.ld_b + nb) * 2 : kPastRow, coff = nb < a.d_state ? (uint32_t)(tb * (int)a.ld_c + nb) * 2 : kPastRow;
-    uint16_t ru[kTiles], rdt[kTiles], rz[kTiles], rb[4], rc[4];
+    // A block's loads: thread (token lt, quad lq) takes four channels' u, dt and z of a token, 8 bytes of a row of which the
+    // workgroup takes 32, and four states' B and C of token tb, at offsets from the block's first token that stay the same; a
+    // block's rows end where the sequence does (zeros past that).
+    constexpr int kQuads = kRowsN / 4;
+    const int lt = t >> 2, lq = t & 3, tb = t / kQuads, qb = t % kQuads;
+    const bool in = ch0 + 4 * lq < a.dim && lt < kBlock, bin = 4 * qb < a.d_state;
+    auto offset = [](bool v, int row, int64_t ld, int col) { return v ? (uint32_t)(row * (int)ld + col) * 2 : kPastRow; };
+    const uint32_t uoff = offset(in, lt, a.ld_u, ch0 + 4 * lq), doff = offset(in, lt, a.ld_dt, ch0 + 4 * lq), zoff = offset(in, lt, a.ld_z, ch0 + 4 * lq),
+                   ooff = offset(in, lt, a.ld_out, ch0 + 4 * lq), boff = offset(bin, tb, a.ld_b, 4 * qb), coff = offset(bin, tb, a.ld_c, 4 * qb);
+    float bias[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) bias[c] = a.dt_bias && in ? a.dt_bias[ch0 + 4 * lq + c] : 0.f;
+    typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+    v2u ru{}, rd{}, rz{}, rb{}, rc{};
     auto load = [&](int64_t t0) {
-        const auto rsu = rows_from(a.u, a.ld_u, t0, end), rsd = rows_from(a.dt, a.ld_dt, t0, end), rsb = rows_from(a.B, a.ld_b, t0, end);
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            ru[i] = __builtin_amdgcn_raw_buffer_load_b16(rsu, uoff + (uint32_t)(i * 32 * (int)a.ld_u), 0, 0);
-            rdt[i] = __builtin_amdgcn_raw_buffer_load_b16(rsd, dtoff + (uint32_t)(i * 32 * (int)a.ld_dt), 0, 0);
-        }
-        if (kOut && a.z) {
-            const auto rsz = rows_from(a.z, a.ld_z, t0, end);
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) rz[i] = __builtin_amdgcn_raw_buffer_load_b16(rsz, zoff + (uint32_t)(i * 32 * (int)a.ld_z), 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) rb[k] = __builtin_amdgcn_raw_buffer_load_b16(rsb, boff + (uint32_t)(k * kStep * 2 * (int)a.ld_b), 0, 0);
+        ru = __builtin_amdgcn_raw_buffer_load_b64(rows_from(a.u, a.ld_u, t0, end), uoff, 0, 0);
+        rd = __builtin_amdgcn_raw_buffer_load_b64(rows_from(a.dt, a.ld_dt, t0, end), doff, 0, 0);
+        rb = __builtin_amdgcn_raw_buffer_load_b64(rows_from(a.B, a.ld_b, t0, end), boff, 0, 0);
         if constexpr (kOut) {
-            const auto rsc = rows_from(a.C, a.ld_c, t0, end);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) rc[k] = __builtin_amdgcn_raw_buffer_load_b16(rsc, coff + (uint32_t)(k * kStep * 2 * (int)a.ld_c), 0, 0);
+            rc = __builtin_amdgcn_raw_buffer_load_b64(rows_from(a.C, a.ld_c, t0, end), coff, 0, 0);
+            if (a.z) rz = __builtin_amdgcn_raw_buffer_load_b64(rows_from(a.z, a.ld_z, t0, end), zoff, 0, 0);
         }
     };
-    float dt_sum = 0.f;
+    auto half = [](const v2u& v, int c) { return c & 1 ? v[c >> 1] >> 16 : v[c >> 1] & 0xffffu; };
+    // a block's outputs, whole rows of the workgroup, once everyone has passed the barrier behind it
+    auto store = [&](int64_t t0, int buf) {
+        if (lt < kBlock)
+            __builtin_amdgcn_raw_buffer_store_b64(*reinterpret_cast<const v2u*>(&s_y[buf][lt][4 * lq]), rows_from(a.out, a.ld_out, t0, end), ooff, 0, 0);
+    };
+    float dt_sum[4] = {0.f, 0.f, 0.f, 0.f};
     if (beg < end) load(beg);
     int buf = 0;
     for (int64_t t0 = beg; t0 < end; t0 += kBlock) {
-        // past the sequence's end (and d_state) B is zero and dt too: the state stays
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            s_bc[buf][0][nb][tb + kStep * k] = bf16_to_f32(rb[k]);
-            if (kOut) s_bc[buf][1][nb][tb + kStep * k] = bf16_to_f32(rc[k]);
-        }
-        float u[kTiles], dt[kTiles], z[kTiles];
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            u[i] = bf16_to_f32(ru[i]);
-            dt[i] = bf16_to_f32(rdt[i]);
-            z[i] = kOut && a.z ? bf16_to_f32(rz[i]) : 0.f;
-        }
-        __syncthreads();     // this block is in LDS, and everyone has read the one before the last
-        if (t0 + kBlock < end) load(t0 + kBlock);
+        // Past the sequence's end (and d_state) B is zero and dt too: the state stays.
         const int left = (int)min(end - t0, (int64_t)kBlock);
-        const auto rso = rows_from(a.out, a.ld_out, t0, end);
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            if (16 * i >= left) break;
-            const float d = 16 * i + l16 < left ? softplus_series(dt[i] + bias) : 0.f;
-            if (kMode == 1) dt_sum += d;
-            s_dt[wave][0][chan][l16] = d;
-            s_dt[wave][1][chan][l16] = d * u[i];
-            wave_lds_order();
-            v4f dts[2][4];
+        for (int j = 0; j < 4; ++j) {
+            s_bc[buf][0][4 * qb + j][tb] = bf16_to_f32(half(rb, j));
+            if (kOut) s_bc[buf][1][4 * qb + j][tb] = bf16_to_f32(half(rc, j));
+        }
+        if (lt < kBlock)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int c = 0; c < 4; ++c) {
+                const float d = lt < left ? softplus_series(bf16_to_f32(half(rd, c)) + bias[c]) : 0.f;
+                s_dt[buf][0][4 * lq + c][lt] = d;
+                s_dt[buf][1][4 * lq + c][lt] = d * bf16_to_f32(half(ru, c));
+                if (kOut) s_uz[buf][4 * lq + c][lt] = half(ru, c) | half(rz, c) << 16;
+                if (kMode == 1) dt_sum[c] += d;
+            }
+        __syncthreads();     // this block is in LDS, and everyone is done with the one before the last
+        if (t0 + kBlock < end) load(t0 + kBlock);
+        if (kOut && t0 > beg) store(t0 - kBlock, buf ^ 1);
+        auto tile = [&](int i) {
+            v4f dts[2][4], bc[kOut ? 2 : 1][R][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) dts[m][k] = *reinterpret_cast<const v4f*>(&s_dt[wave][m][chan][4 * k]);
-            wave_lds_order();
-            v4f bc[kOut ? 2 : 1][R][4];
+            for (int k = 0; k < 4; ++k) {
 #pragma unroll
-            for (int m = 0; m < (kOut ? 2 : 1); ++m)
+                for (int m = 0; m < 2; ++m) dts[m][k] = *reinterpret_cast<const v4f*>(&s_dt[buf][m][4 * wave + chan][16 * i + 4 * k]);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int m = 0; m < (kOut ? 2 : 1); ++m)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int r = 0; r < R; ++r)
                         bc[m][r][k] = *reinterpret_cast<const v4f*>(&s_bc[buf][m][l16 + 16 * r][16 * i + 4 * k]);
+            }
             float p[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -237,23 +232,45 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
                 }
             }
             if constexpr (kOut) {
-                float y = fmaf(Dc, u[i], channel_sums(p, lane));
-                if (a.z) y *= silu(z[i]);
-                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f32_to_bf16(y), rso, ooff + (uint32_t)(i * 32 * (int)a.ld_out), 0, 0);
+                const uint32_t uz = s_uz[buf][4 * wave + chan][16 * i + l16];
+                float y = fmaf(Dc, bf16_to_f32(uz & 0xffffu), channel_sums(p, lane));
+                if (a.z) y *= silu(bf16_to_f32(uz >> 16));
+                s_y[buf][16 * i + l16][4 * wave + chan] = (uint16_t)f32_to_bf16(y);
             }
+        };
+        if (left == kBlock) {        // no branch between the tiles: their latencies overlap
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) tile(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+                if (16 * i < left) tile(i);
         }
         buf ^= 1;
+    }
+    if (kOut && beg < end) {
+        __syncthreads();
+        store(beg + (end - 1 - beg) / kBlock * kBlock, buf ^ 1);
     }
     if constexpr (kMode == 1) {
         if (beg < end && on) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (l16 + 16 * r < a.d_state) ws_state(chunk + 1)[l16 + 16 * r] = h[r];
-            dt_sum = swap32_sum(dt_sum, dt_sum);
-            dt_sum = swap16_sum(dt_sum, dt_sum);
-            dt_sum += dpp<0x4E>(dt_sum);
-            dt_sum += dpp<0xB1>(dt_sum);
-            if (l16 == 0) a.ws_dt[((int64_t)seq * a.n_chunks + chunk) * a.dim + ch] = dt_sum;
+        }
+        if (beg < end) {         // the chunk's sum of dt of each channel: over the tokens' threads of the workgroup
+            __syncthreads();     // everyone is done with the last block
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (lt < kBlock) s_dt[0][0][4 * lq + c][lt] = dt_sum[c];
+            __syncthreads();
+            float sum = 0.f;
+            for (int i = l16; i < kBlock; i += 16) sum += s_dt[0][0][4 * wave + chan][i];
+            sum = swap32_sum(sum, sum);
+            sum = swap16_sum(sum, sum);
+            sum += dpp<0x4E>(sum);
+            sum += dpp<0xB1>(sum);
+            if (l16 == 0 && on) a.ws_dt[((int64_t)seq * a.n_chunks + chunk) * a.dim + ch] = sum;
         }
     } else {
         if (end == last && held && on)      // the sequence's last chunk (an empty sequence's only one)
