@@ -144,15 +144,25 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
                 if (l16 + 16 * r < a.d_state) ws_state(0)[l16 + 16 * r] = h[r];
     }
     if constexpr (kMode == 2) {
-        for (int c = 0; c <= chunk; ++c) {
-            // entry 1 holds the state behind the first chunk, the later ones what their chunk adds
-            const float keep = c < 2 ? 0.f : a.ws_dt[((int64_t)seq * a.n_chunks + c - 1) * a.dim + chc];
+        // entry 1 holds the state behind the first chunk, the later ones what their chunk adds; eight at a time, so that the
+        // loads do not wait for each other
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int n = l16 + 16 * r;
-                const float s = n < a.d_state ? ws_state(c)[n] : 0.f;
-                h[r] = c < 2 ? s : fmaf(__builtin_amdgcn_exp2f(keep * A2[r]), h[r], s);
+        for (int r = 0; r < R; ++r)
+            if (l16 + 16 * r < a.d_state) h[r] = ws_state(min(chunk, 1))[l16 + 16 * r];
+        for (int c0 = 2; c0 <= chunk; c0 += 8) {
+            float keep[8], add[R][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = min(c0 + i, chunk);
+                keep[i] = a.ws_dt[((int64_t)seq * a.n_chunks + c - 1) * a.dim + chc];
+#pragma unroll
+                for (int r = 0; r < R; ++r) add[r][i] = l16 + 16 * r < a.d_state ? ws_state(c)[l16 + 16 * r] : 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + i <= chunk)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) h[r] = fmaf(__builtin_amdgcn_exp2f(keep[i] * A2[r]), h[r], add[r][i]);
         }
     }
     const float Dc = a.D ? a.D[chc] : 0.f;
@@ -296,10 +306,19 @@ static void launch_scan_r(const ScanPrefillArgs& a, hipStream_t st) {
     scan_prefill_kernel<R, 2><<<grid(a.n_chunks), dim3(kScanWaves * 64), 0, st>>>(a);
 }
 
-// The chunks that sequences are cut into where there are too few of them to fill the chip.
+// Where sequences x channels do not fill the chip, sequences are cut into chunks of at least 128 tokens, up to 64 of them, for
+// about 1,024 workgroups, at the price of forming the decays twice. us, whole and cut: 4,096 tokens x 4,096 channels (4
+// chunks) 155 and 166, x 2,048 (8) 151 and 88, x 1,024 152 and 50, x 64 149 and 18; 15,360 x 512 547 and 94; 256 x 256
+// (2 of 128 tokens) 13.5 and 14.4, 1,024 x 1,024 41 and 19.
 ScanSplit scan_split(int64_t dim, int64_t n_tokens, int64_t n_seqs) {
-    ScanSplit s{1, n_tokens > 0 ? n_tokens : 1};
-    return s;
+    const ScanSplit whole{1, n_tokens > 0 ? n_tokens : 1};
+    const int64_t groups = (n_seqs > 0 ? n_seqs : 1) * ((dim + 15) / 16);
+    const int64_t s = 1024 / groups < 64 ? 1024 / groups : 64;
+    if (s < 6) return whole;
+    int64_t chunk = ((n_tokens + s - 1) / s + 63) / 64 * 64;
+    chunk = chunk < 128 ? 128 : chunk;
+    const int64_t n = (n_tokens + chunk - 1) / chunk;
+    return n < 4 ? whole : ScanSplit{n, chunk};
 }
 
 size_t scan_ws_bytes(int64_t dim, int32_t d_state, int64_t n_tokens, int64_t n_seqs) {
