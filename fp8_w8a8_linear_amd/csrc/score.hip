@@ -132,59 +132,63 @@ __global__ __launch_bounds__(kScoreWaves * 64, F32 ? 3 : 4) void score_strip_ker
     if (lane == 0) g.strips[id] = ScoreStrip{sum, mom, all, count};
 }
 
-// One workgroup per row (of one wave where the strips are few): wave w joins every w-th strip's list.
-constexpr int kJoinWaves = 8;
+// One workgroup per row: of one wave where the strips are few, else wave 0 forms the sums while the others merge
+// the strips' lists (a row of 131,072 with 20 alternatives: 15.8 us, with eight waves that all did both 18.8).
+constexpr int kJoinWaves = 16;
 
 __global__ __launch_bounds__(kJoinWaves * 64) void score_join_kernel(const ScoreArgs g) {
     __shared__ StripKey s_list[kJoinWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int64_t row = blockIdx.x;
     const int S = g.n_strips;
-    const ScoreStrip* const st = g.strips + row * S;
-    float top = -INFINITY;
-    for (int s = lane; s < S; s += 64) top = fmaxf(top, st[s].top);
-    top = wave_max(top);
-    double sum = 0.0, mom = 0.0;
-    uint32_t count = 0;
-    for (int s = lane; s < S; s += 64) {
-        const ScoreStrip v = st[s];
-        count += v.count;
-        if (v.top == top) {
-            sum += v.sum;
-            mom += v.mom;
-        } else if (v.top > -INFINITY && top < INFINITY) {
-            const double d = (double)v.top - (double)top, keep = exp(d);
-            sum += keep * v.sum;
-            mom += keep * (v.mom + d * (1.0 / kLn2) * v.sum);
-        }
-    }
-    sum = wave_sum_f64(sum);
-    mom = wave_sum_f64(mom);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) count += __shfl_xor(count, o);
-    const bool none = top == -INFINITY;                   // nothing is possible
-    const double lse = none ? 0.0 : log(sum);             // beside top
-    if (wave == 0 && lane == 0) {
+    StripKey list{0};
+    double top = 0.0, lse = 0.0;         // wave 0: the row's largest logit, and log of the sum beside it
+    if (wave == 0) {
+        const ScoreStrip* const st = g.strips + row * S;
         const int64_t token = g.tokens ? g.tokens[row] : -1;
-        if (token >= 0 && token < g.vocab) {
-            const float x = clean_logit(g.f32 ? static_cast<const float*>(g.logits)[row * g.ld + token]
-                                              : bf16_to_f32(static_cast<const uint16_t*>(g.logits)[row * g.ld + token]));
-            if (g.logprobs) g.logprobs[row] = x == -INFINITY ? -INFINITY : (float)((x == top ? 0.0 : (double)x - (double)top) - lse);
-            // all the entries ahead of a token at -inf come before it
-            if (g.ranks) g.ranks[row] = (int32_t)(count + 1 + (x == -INFINITY ? (uint32_t)token : 0u));
-        } else {
-            if (g.logprobs) g.logprobs[row] = 0.f;
-            if (g.ranks) g.ranks[row] = 0;
+        const bool asked = token >= 0 && token < g.vocab;
+        const int64_t at = row * g.ld + (asked ? token : 0);
+        const float x = clean_logit(g.f32 ? static_cast<const float*>(g.logits)[at] : bf16_to_f32(static_cast<const uint16_t*>(g.logits)[at]));
+        float topf = -INFINITY;
+        for (int s = lane; s < S; s += 64) topf = fmaxf(topf, st[s].top);
+        topf = wave_max(topf);
+        top = topf;
+        double sum = 0.0, mom = 0.0;
+        uint32_t count = 0;
+        for (int s = lane; s < S; s += 64) {
+            const ScoreStrip v = st[s];
+            count += v.count;
+            if (v.top == topf) {
+                sum += v.sum;
+                mom += v.mom;
+            } else if (v.top > -INFINITY && topf < INFINITY) {
+                const double d = (double)v.top - top, keep = exp(d);
+                sum += keep * v.sum;
+                mom += keep * (v.mom + d * (1.0 / kLn2) * v.sum);
+            }
         }
-        if (g.entropy) g.entropy[row] = none ? 0.f : (float)(lse - kLn2 * (mom / sum));
+        sum = wave_sum_f64(sum);
+        mom = wave_sum_f64(mom);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) count += __shfl_xor(count, o);
+        const bool none = topf == -INFINITY;              // nothing is possible
+        lse = none ? 0.0 : log(sum);
+        if (lane == 0) {
+            if (g.logprobs) g.logprobs[row] = !asked ? 0.f : x == -INFINITY ? -INFINITY : (float)((x == topf ? 0.0 : (double)x - top) - lse);
+            // all the entries ahead of a token at -inf come before it
+            if (g.ranks) g.ranks[row] = asked ? (int32_t)(count + 1 + (x == -INFINITY ? (uint32_t)token : 0u)) : 0;
+            if (g.entropy) g.entropy[row] = none ? 0.f : (float)(lse - kLn2 * (mom / sum));
+        }
     }
     if (g.n_top == 0) return;
-    StripKey list{0};
     const uint64_t* const keys = g.strip_keys + row * S * g.n_top;
-    for (int s = wave; s < S; s += waves) {
-        const StripKey k{lane < g.n_top ? keys[(int64_t)s * g.n_top + lane] : 0};
-        merge64(list, k, lane);
-    }
+    const int step = waves > 1 ? waves - 1 : 1, s0 = waves > 1 ? wave - 1 : 0;
+    if (s0 >= 0)
+        for (int s = s0; s < S; s += step) {
+            const StripKey k{lane < g.n_top ? keys[(int64_t)s * g.n_top + lane] : 0};
+            if (s == s0) list = k;
+            else merge64(list, k, lane);
+        }
     for (int half = waves / 2; half > 0; half >>= 1) {
         if (wave >= half && wave < 2 * half) s_list[wave][lane] = list;
         __syncthreads();
@@ -194,7 +198,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void score_join_kernel(const Score
         const int64_t o = row * g.n_top + lane;
         const float x = unordered((uint32_t)(list.v >> 32));
         // beside +inf entries the finite ones have no probability
-        const double lp = list.v == 0 ? -INFINITY : (x == top ? 0.0 : (double)x - (double)top) - lse;
+        const double lp = list.v == 0 ? -INFINITY : ((double)x == top ? 0.0 : (double)x - top) - lse;
         g.top_tokens[o] = lp > -INFINITY ? (int32_t)~(uint32_t)list.v : -1;
         g.top_logprobs[o] = (float)lp;
     }

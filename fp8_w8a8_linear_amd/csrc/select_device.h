@@ -208,7 +208,8 @@ struct StripBest {
         StripKey k{lane < count ? lds->fresh[pending + lane].v : 0};
         wave_lds_order();
         sort64(k, lane);
-        merge64(list, k, lane);
+        if (__ballot(list.v != 0) == 0) list = k;     // the first ones
+        else merge64(list, k, lane);
         const uint64_t t = (uint64_t)take((uint32_t)(list.v >> 32), n - 1) << 32 | take((uint32_t)list.v, n - 1);
         if (t != 0) {
             last = unordered((uint32_t)(t >> 32));
