@@ -20,11 +20,13 @@ constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxRows = int64_t(1) << 24;
 constexpr int kMaxTop = 64;
 
 // Codes of a bf16 activation and its scales, as rows or packed for the tile kernels (an MXFP4 input's packed scales
-// alone), and on the tile kernels room for the weight's packed scales where the caller has none.
+// alone), and on the tile kernels room for the weight's packed scales where the caller has none. Nothing where the rows
+// kernel quantises the activation itself.
 struct MxWs { size_t scales, weight, total; };
 MxWs mx_ws(int64_t m, int64_t n, int64_t k, nhm_dtype t) {
     MxWs w{0, 0, 0};
     const bool tiled = mx_tiled(m);
+    if (t == NHM_BF16 && mx_rows_quantise(m, k)) return w;
     if (t == NHM_BF16) w.scales = align_up((size_t)m * (k / 2), 256);
     w.weight = w.scales;
     if (tiled) w.weight += align_up((size_t)mx_packed_words(m, k) * 4, 256);
@@ -185,7 +187,10 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
     uint8_t* const wsb = static_cast<uint8_t*>(ws);
     uint32_t* const packed = mx_tiled(m) ? reinterpret_cast<uint32_t*>(wsb + l.scales) : nullptr;
     nhm_status s = NHM_OK;
-    if (bf16) {
+    if (bf16 && mx_rows_quantise(m, w->k)) {
+        g.a_bf16 = static_cast<const uint16_t*>(a);
+        g.ld_bf16 = ld_a;
+    } else if (bf16) {
         MxQuantArgs q{a, m, w->k, ld_a, wsb, ld_q, wsb + l.scales, w->k / 32};
         q.packed = packed;
         s = launch_mx_quant(q, false, st);

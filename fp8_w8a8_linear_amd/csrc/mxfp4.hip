@@ -150,19 +150,23 @@ __device__ __forceinline__ v4f mfma_mx16(const v4u& a, const v4u& b, const v4f& 
 
 // Few rows: a workgroup of eight waves takes 16 features, each wave a share of k, in steps of 256: lane (r, q) holds the 32 bytes
 // of row r that start 32 q into the step's 128-byte line, two blocks, and their two scale codes. The waves' sums are added in LDS
-// in wave order. TM: 16-row tiles of the activations.
+// in wave order. TM: 16-row tiles of the activations. kQuant: the activations are bf16, and every workgroup quantises them
+// into LDS, behind its first loads of the weight. Bound by latency and the weight's bytes: 1 row x 10,304 x 2,688 5.0 us (14.7 MB,
+// 2.9 TB/s), 61 rows 12.5. (Loading a step or two ahead of the products: 7.5 and 18.)
 constexpr int kMxWaves = 8;
 
-template <int TM>
+template <int TM, bool kQuant>
 __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs g) {
     __shared__ v4f s_sum[kMxWaves][TM][64];
+    extern __shared__ __attribute__((aligned(16))) uint8_t s_a[];      // kQuant: codes [m, 128 steps], behind them scale codes [m, 8 steps]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, q = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t kb = g.k / 2, ks = g.k / 32;       // bytes of codes and of scales in a weight row
+    const int steps = (int)((g.k + 255) / 256);
     const auto wrs = mx_buffer(g.w, g.n * kb), wss = mx_buffer(g.w_scale, g.n * g.ld_ws);
-    const auto ars = mx_buffer(g.a, g.m * g.ld_a), ass = mx_buffer(g.a_scale, g.m * g.ld_as);
     const int64_t wr = n0 + r16;
     const uint32_t woff = wr < g.n ? (uint32_t)(wr * kb) : kPast, wsoff = wr < g.n ? (uint32_t)(wr * g.ld_ws) : kPast;
+    const auto ars = mx_buffer(g.a, kQuant ? 0 : g.m * g.ld_a), ass = mx_buffer(g.a_scale, kQuant ? 0 : g.m * g.ld_as);
     uint32_t aoff[TM], asoff[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
@@ -178,22 +182,61 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs
         const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b8(rs, at + 1 < ks ? off + at + 1 : kPast, 0, 0);
         return lo | hi << 8;
     };
+    struct Step { v4u w0, w1, a0[TM], a1[TM]; uint32_t ws, as[TM]; };
+    auto load = [&](Step& x, int s) {                // a step past the last is all zeros
+        const uint32_t cb = (uint32_t)s * 128 + 32 * q, sb = (uint32_t)s * 8 + 2 * q;
+        x.w0 = load16(wrs, woff, cb);
+        x.w1 = load16(wrs, woff, cb + 16);
+        x.ws = load2(wss, wsoff, sb);
+        if constexpr (!kQuant)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                x.a0[j] = load16(ars, aoff[j], cb);
+                x.a1[j] = load16(ars, aoff[j], cb + 16);
+                x.as[j] = load2(ass, asoff[j], sb);
+            }
+    };
+    Step x;
+    if constexpr (kQuant) {
+        load(x, wave);
+        // as mx_quant_kernel, zeros up to whole steps
+        for (int i = threadIdx.x; i < (int)g.m * steps * 32; i += kMxWaves * 64) {
+            const int row = i / (steps * 32), c = i % (steps * 32) * 8;
+            uint32_t s = 0, codes = 0;
+            if (c < g.k) {
+                float f[8];
+                load8<false>(reinterpret_cast<const char*>(g.a_bf16 + row * g.ld_bf16 + c), f);
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+                s = mx_scale(quad_max(m));
+                codes = mx_codes(f, s);
+            }
+            *reinterpret_cast<uint32_t*>(s_a + row * (steps * 128) + c / 2) = codes;
+            if ((c & 31) == 0) s_a[(int)g.m * (steps * 128) + row * (steps * 8) + c / 32] = (uint8_t)s;
+        }
+        __syncthreads();
+    }
     v4f acc[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int steps = (int)((g.k + 255) / 256);
-#pragma unroll 2
-    for (int s = wave; s < steps; s += kMxWaves) {
-        const uint32_t cb = (uint32_t)s * 128 + 32 * q, sb = (uint32_t)s * 8 + 2 * q;
-        const v4u w0 = load16(wrs, woff, cb), w1 = load16(wrs, woff, cb + 16);
-        const uint32_t ws = load2(wss, wsoff, sb);
+    auto use = [&](Step& x, int s) {
+        if constexpr (kQuant) {
+            const int row = min(r16, (int)g.m - 1);         // (rows past the last are not stored)
+            const uint8_t* const c = s_a + row * (steps * 128) + s * 128 + 32 * q;
+            x.a0[0] = *reinterpret_cast<const v4u*>(c);
+            x.a1[0] = *reinterpret_cast<const v4u*>(c + 16);
+            x.as[0] = *reinterpret_cast<const uint16_t*>(s_a + (int)g.m * (steps * 128) + row * (steps * 8) + s * 8 + 2 * q);
+        }
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-            const v4u a0 = load16(ars, aoff[j], cb), a1 = load16(ars, aoff[j], cb + 16);
-            const uint32_t as = load2(ass, asoff[j], sb);
-            acc[j] = mfma_mx16<0>(w0, a0, acc[j], ws, as);
-            acc[j] = mfma_mx16<1>(w1, a1, acc[j], ws, as);
+            acc[j] = mfma_mx16<0>(x.w0, x.a0[j], acc[j], x.ws, x.as[j]);
+            acc[j] = mfma_mx16<1>(x.w1, x.a1[j], acc[j], x.ws, x.as[j]);
         }
+    };
+    for (int s = wave; s < steps; s += kMxWaves) {
+        if (!kQuant || s != wave) load(x, s);
+        use(x, s);
     }
 #pragma unroll
     for (int j = 0; j < TM; ++j) s_sum[wave][j][lane] = acc[j];
@@ -553,12 +596,18 @@ static void launch_tile(MxGemmArgs g, hipStream_t st) {
 
 bool mx_tiled(int64_t m) { return m > 64; }
 
+// Where the rows kernel takes bf16 values and quantises them itself, once a workgroup, rather than after a launch of the
+// quantisation, us: 1 row x 10,304 x 2,688 4.9 and 7.3, 4 rows 6.4 and 7.4, 8 rows 8.6 and 7.6; 4 x 2,688 x 4,096 5.8 and 6.8, 8 rows 7.5
+// and 7.2. The codes have to fit LDS.
+bool mx_rows_quantise(int64_t m, int64_t k) { return m <= 4 && m * ((k + 255) / 256) * 136 <= 32768; }
+
 nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st) {
     if (!mx_tiled(g.m)) {
         const dim3 grid((unsigned)((g.n + 15) / 16)), block(kMxWaves * 64);
-        if (g.m <= 16) mx_rows_kernel<1><<<grid, block, 0, st>>>(g);
-        else if (g.m <= 32) mx_rows_kernel<2><<<grid, block, 0, st>>>(g);
-        else mx_rows_kernel<4><<<grid, block, 0, st>>>(g);
+        if (g.a_bf16) mx_rows_kernel<1, true><<<grid, block, (size_t)g.m * ((g.k + 255) / 256) * 136, st>>>(g);
+        else if (g.m <= 16) mx_rows_kernel<1, false><<<grid, block, 0, st>>>(g);
+        else if (g.m <= 32) mx_rows_kernel<2, false><<<grid, block, 0, st>>>(g);
+        else mx_rows_kernel<4, false><<<grid, block, 0, st>>>(g);
         count_launch(Kern::kMxRows, g.m);
         return check_launch("mxfp4 linear");
     }

@@ -375,6 +375,8 @@ struct MxGemmArgs {
     const uint8_t* w;              // codes [n, k / 2]
     const uint8_t* w_scale;        // [n, ld_ws]
     int64_t ld_ws, n, k;
+    const uint16_t* a_bf16 = nullptr;   // or the values [m, ld_bf16] in place of a, which the kernel quantises (mx_rows_quantise)
+    int64_t ld_bf16 = 0;
     const uint32_t* a_packed;      // the tile kernels': scale codes as launch_mx_pack lays them out
     const uint32_t* w_packed;
     uint16_t* out;                 // bf16 [m, ld_out], or nullptr with out_f32
@@ -386,6 +388,7 @@ struct MxGemmArgs {
 // Whether m rows run on the tile kernels, which take scale codes packed: dword (j, row) at [j * rows + row] holds those of
 // the row's blocks 4 j .. 4 j + 3 (zeros past the row), mx_packed_words(rows, k) in all.
 bool mx_tiled(int64_t m);
+bool mx_rows_quantise(int64_t m, int64_t k);
 inline int64_t mx_packed_words(int64_t rows, int64_t k) { return rows * ((k / 32 + 3) / 4); }
 nhm_status launch_mx_pack(const uint8_t* scales, int64_t rows, int64_t k, uint32_t* packed, hipStream_t st);
 nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st);

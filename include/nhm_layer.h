@@ -74,7 +74,7 @@ NHM_API size_t nhm_mxfp4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k,
  *            a_type NHM_MXFP4: (device) codes [m, ld_a] bytes, ld_a >= k / 2, 16-byte aligned rows
  *   a_scale  (device) scale codes [m, k / 32] of an MXFP4 input (NULL with bf16)
  *   out      (device) [m, ld_out] of out_type NHM_BF16 or NHM_F32, ld_out >= n, aligned to its element size
- *   ws       (device, 256-byte aligned) nhm_mxfp4_linear_workspace_bytes(...) bytes
+ *   ws       (device, 256-byte aligned) nhm_mxfp4_linear_workspace_bytes(...) bytes (may be 0: NULL)
  * m == 0 is a valid no-op. The result of a row does not depend on the other rows' values.
  * Operands of 2 GiB or more (of codes) are NHM_ERR_UNSUPPORTED.
  * Errors: NHM_ERR_NULL, NHM_ERR_SHAPE, NHM_ERR_ALIGN, NHM_ERR_UNSUPPORTED, NHM_ERR_WORKSPACE, NHM_ERR_HIP. */

@@ -192,6 +192,48 @@ def test_mxfp4_linear_rows_alone(nhm):
     assert nhm.mxfp4_linear(x[:0], weight, a_scale=xs[:0]).shape == (0, 200)
 
 
+@pytest.mark.parametrize("k", [32, 288, 4096, 15360, 15616, 40960])
+def test_mxfp4_linear_quantises_alike(nhm, k):
+    """bf16 rows and their codes give the same bits, whether or not the quantisation is a launch of its own (up to four rows
+    whose codes fit LDS are quantised beside the product); infinities and NaN, and rows of a wider tensor, among them."""
+    r = np.random.default_rng(k)
+    w = nhm.Mxfp4Weight(u8(r.integers(0, 256, (50, k // 2))), u8(r.integers(118, 130, (50, k // 32))))
+    for m in (1, 2, 3, 4, 5, 70):
+        x = r.normal(size=(m, k)) * np.exp2(r.integers(-140, 100, (m, 1)).astype(float))
+        x[m - 1, k - 1] = np.nan if m % 2 else np.inf
+        x = wider(bf16(x), 8, 16)
+        codes, scales = nhm.mxfp4_quantize(x)
+        for t in (nhm.NHM_F32, nhm.NHM_BF16):
+            want, got = nhm.mxfp4_linear(codes, w, a_scale=scales, out_type=t), nhm.mxfp4_linear(x, w, out_type=t)
+            bits = torch.int32 if t == nhm.NHM_F32 else torch.int16
+            assert torch.equal(got.view(bits), want.view(bits)), (m, t)
+            assert bool(torch.isnan(got.view(torch.float32 if t == nhm.NHM_F32 else torch.bfloat16)[m - 1]).all())
+
+
+def test_mxfp4_linear_packed_scales(nhm):
+    """A weight without packed scale codes gives the same bits; with them, new scale codes count from pack() on."""
+    import ctypes as C
+    r = np.random.default_rng(8)
+    m, n, k = 100, 70, 416
+    weight = nhm.Mxfp4Weight(u8(r.integers(0, 256, (n, k // 2))), u8(r.integers(118, 130, (n, k // 32))))
+    x = bf16(r.normal(size=(m, k)))
+    codes, scales = nhm.mxfp4_quantize(x)
+
+    def bare(a, t, s):
+        wt = nhm._Mxfp4Weight(weight.w.data_ptr(), weight.scale.data_ptr(), n, k, None)
+        size = nhm.mxfp4_linear_workspace_bytes(m, n, k, t)
+        ws, out = torch.empty(size, dtype=torch.uint8, device="cuda"), torch.empty(m, n, dtype=torch.float32, device="cuda")
+        st = torch.cuda.current_stream().cuda_stream
+        assert nhm.lib.nhm_mxfp4_linear(a.data_ptr(), t, s, m, a.shape[1], C.byref(wt), out.data_ptr(), nhm.NHM_F32, n, ws.data_ptr(), size, st) == 0
+        return out
+
+    for _ in range(2):
+        want = nhm.mxfp4_linear(x, weight, out_type=nhm.NHM_F32)
+        assert torch.equal(bare(x, nhm.NHM_BF16, None), want) and torch.equal(bare(codes, nhm.NHM_MXFP4, scales.data_ptr()), want)
+        weight.scale.copy_(u8(r.integers(118, 130, (n, k // 32))))
+        weight.pack()
+
+
 # ---------------------------------------------------------------- batches
 
 BATCHES = [[1], [2, 3], [0], [5, 130, 1, 0, 260, 128], [0, 0, 7, 0], [8, 8, 8], [1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1], [64, 16, 63, 65],
@@ -614,6 +656,6 @@ def test_binding_refusals_on_the_gpu(nhm):
             f()
             print("not refused:", i)
     for f in [lambda: nhm.token_logprobs(x, sl, n_top=65), lambda: nhm.mxfp4_quantize(x[:, :16]),
-              lambda: nhm.mxfp4_linear(x, w, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))]:
+              lambda: nhm.mxfp4_linear(x.repeat(2, 1), w, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))]:
         with pytest.raises(nhm.NhmError):
             f()
