@@ -596,11 +596,6 @@ static void launch_tile(MxGemmArgs g, hipStream_t st) {
 
 bool mx_tiled(int64_t m) { return m > 64; }
 
-// Where the rows kernel takes bf16 values and quantises them itself, once a workgroup, rather than after a launch of the
-// quantisation, us: 1 row x 10,304 x 2,688 4.9 and 7.3, 4 rows 6.4 and 7.4, 8 rows 8.6 and 7.6; 4 x 2,688 x 4,096 5.8 and 6.8, 8 rows 7.5
-// and 7.2. The codes have to fit LDS.
-bool mx_rows_quantise(int64_t m, int64_t k) { return m <= 4 && m * ((k + 255) / 256) * 136 <= 32768; }
-
 nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st) {
     if (!mx_tiled(g.m)) {
         const dim3 grid((unsigned)((g.n + 15) / 16)), block(kMxWaves * 64);
