@@ -151,8 +151,8 @@ __device__ __forceinline__ v4f mfma_mx16(const v4u& a, const v4u& b, const v4f& 
 // Few rows: a workgroup of eight waves takes 16 features, each wave a share of k, in steps of 256: lane (r, q) holds the 32 bytes
 // of row r that start 32 q into the step's 128-byte line, two blocks, and their two scale codes. The waves' sums are added in LDS
 // in wave order. TM: 16-row tiles of the activations. kQuant: the activations are bf16, and every workgroup quantises them
-// into LDS, behind its first loads of the weight. Bound by latency and the weight's bytes: 1 row x 10,304 x 2,688 5.0 us (14.7 MB,
-// 2.9 TB/s), 61 rows 12.5. (Loading a step or two ahead of the products: 7.5 and 18.)
+// into LDS, behind its first loads of the weight. Bound by latency and the weight's bytes: 1 row x 10,304 x 2,688 4.4 us (14.7 MB,
+// 3.3 TB/s), 61 rows 9.9. (Loading a step or two ahead of the products made the call up to half again as long.)
 constexpr int kMxWaves = 8;
 
 template <int TM, bool kQuant>
@@ -177,7 +177,11 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs
     auto load16 = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t off, uint32_t at) {
         return __builtin_amdgcn_raw_buffer_load_b128(rs, at < kb ? off + at : kPast, 0, 0);
     };
-    auto load2 = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t off, uint32_t at) {      // past the row: scale 2^-127 of zeros
+    // two scale codes; past the row 2^-127, of zeros. In one load where every row's pairs are whole (half the requests: 64 x 2,688 x
+    // 4,096 9.0 us, with two 11.0)
+    const bool pairs = ks % 2 == 0 && ((reinterpret_cast<uintptr_t>(g.w_scale) | reinterpret_cast<uintptr_t>(g.a_scale)) & 1) == 0;
+    auto load2 = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t off, uint32_t at) -> uint32_t {
+        if (pairs) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at < ks ? off + at : kPast, 0, 0);
         const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b8(rs, at < ks ? off + at : kPast, 0, 0);
         const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b8(rs, at + 1 < ks ? off + at + 1 : kPast, 0, 0);
         return lo | hi << 8;

@@ -388,9 +388,9 @@ struct MxGemmArgs {
 // Whether m rows run on the tile kernels, which take scale codes packed: dword (j, row) at [j * rows + row] holds those of
 // the row's blocks 4 j .. 4 j + 3 (zeros past the row), mx_packed_words(rows, k) in all.
 bool mx_tiled(int64_t m);
-// Where the rows kernel takes bf16 values and quantises them itself, once a workgroup, rather than after a launch of the
-// quantisation, us: 1 row x 10,304 x 2,688 4.9 and 7.3, 4 rows 6.4 and 7.4, 8 rows 8.6 and 7.6; 4 x 2,688 x 4,096 5.8 and 6.8, 8 rows 7.5
-// and 7.2. The codes have to fit LDS.
+// Where the rows kernel takes bf16 values and quantises them itself, in every workgroup, rather than after a launch of the
+// quantisation, us: 10,304 x 2,688: 1 row 4.4, 4 rows 6.2, 8 rows 8.6, and after a launch 5 rows 6.7, 8 rows 6.8; 2,688 x 4,096: 4 rows 5.4,
+// 8 rows 7.5, and after a launch 6.3 and 6.5. The codes have to fit LDS.
 inline bool mx_rows_quantise(int64_t m, int64_t k) { return m <= 4 && m * ((k + 255) / 256) * 136 <= 32768; }
 inline int64_t mx_packed_words(int64_t rows, int64_t k) { return rows * ((k / 32 + 3) / 4); }
 nhm_status launch_mx_pack(const uint8_t* scales, int64_t rows, int64_t k, uint32_t* packed, hipStream_t st);
