@@ -167,7 +167,7 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
     if (!rows16(a, ld_a * (bf16 ? 2 : 1)) || !aligned(w->w, 16) || !aligned(out, out_type == NHM_F32 ? 4 : 2))
         return fail(NHM_ERR_ALIGN, "mxfp4: rows of a and the weight's codes must be 16-byte aligned, out to its element size");
     const int64_t ld_q = bf16 ? w->k / 2 : ld_a;
-    if (w->n >= kMaxOperand / (w->k / 2) || m >= kMaxOperand / ld_q)
+    if (w->n > (kMaxOperand - 1) / (w->k / 2) || m > (kMaxOperand - 1) / ld_q)
         return fail(NHM_ERR_UNSUPPORTED, "mxfp4: an operand of 2 GiB or more");
     const MxWs l = mx_ws(m, w->n, w->k, a_type);
     if (l.total > 0 && (!ws || ws_bytes < l.total))

@@ -382,13 +382,13 @@ __global__ __launch_bounds__(64 * NWN * NWM) void mx_tile_kernel(const MxGemmArg
         uint8_t* const sb = smem + slot * kStage;
         if (i < kLoads) {
             uint8_t* const to = sb + (wave + i * kWaves) * 1024;
-            if (i < kWLoads) dma<16>(wrs, to, wbase + (uint32_t)(i * kRowStep * kb), (uint32_t)(ls * KB));
-            else dma<16>(ars, to, abase + (uint32_t)((i - kWLoads) * kRowStep * (int)g.ld_a), (uint32_t)(ls * KB));
+            if (i < kWLoads) dma<16>(wrs, to, wbase + (uint32_t)(i * kRowStep) * (uint32_t)kb, (uint32_t)(ls * KB));
+            else dma<16>(ars, to, abase + (uint32_t)((i - kWLoads) * kRowStep) * (uint32_t)g.ld_a, (uint32_t)(ls * KB));
         } else {
             const int blk = wave + (i - kLoads) * kWaves;
             const bool isw = blk % (kRows / 64) * 64 < TN;
             uint8_t* const to = kSpare != 0 && blk >= kScales ? smem + RING * kStage : sb + kCodes + blk * 256;
-            dma<4>(isw ? wss : ass, to, sbase[i - kLoads] + (uint32_t)(ls * kPlanes * (int)(isw ? g.n : g.m) * 4), 0u);
+            dma<4>(isw ? wss : ass, to, sbase[i - kLoads] + (uint32_t)(ls * kPlanes) * (uint32_t)(isw ? g.n : g.m) * 4u, 0u);
         }
     };
     auto advance = [&]() {

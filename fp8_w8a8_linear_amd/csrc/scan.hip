@@ -31,6 +31,12 @@ __device__ __forceinline__ float softplus_series(float x) {
     return fmaxf(x, 0.0f) + 2.0f * s * p;
 }
 
+// A log2(e) of a state, finite where A is not, so that a step of 0 (as past a sequence's end) keeps any state.
+__device__ __forceinline__ float decay_rate(float A_log) {
+    const float r = -expf(A_log) * kLog2e;
+    return r < -3.402823466e38f ? -3.402823466e38f : r;
+}
+
 __device__ __forceinline__ bool has_slot(int slot, int n_slots) { return slot >= 0 && slot < n_slots; }
 
 // ---------------------------------------------------------------- scan of prompts
@@ -130,7 +136,7 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
     for (int r = 0; r < R; ++r) {
         const int n = l16 + 16 * r;
         const bool in = n < a.d_state;
-        A2[r] = in ? -expf(a.A_log[(int64_t)chc * a.d_state + n]) * kLog2e : 0.f;
+        A2[r] = in ? decay_rate(a.A_log[(int64_t)chc * a.d_state + n]) : 0.f;
         h[r] = 0.f;
         if (in && (kMode == 0 || (kMode == 1 && chunk == 0)) && held && a.has_initial[seq] != 0)
             h[r] = a.pool_bf16 ? bf16_to_f32(a.pool_bf16[state0 + n]) : a.pool[state0 + n];
@@ -379,7 +385,7 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(const ScanDecodeArgs a
     float y = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        h[k] = fmaf(__builtin_amdgcn_exp2f(dt * (-expf(al[k]) * kLog2e)), h[k], dt * u * B[k]);
+        h[k] = fmaf(__builtin_amdgcn_exp2f(dt * decay_rate(al[k])), h[k], dt * u * B[k]);
         y = fmaf(h[k], C[k], y);
     }
     if (in) {

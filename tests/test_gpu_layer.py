@@ -210,6 +210,19 @@ def test_mxfp4_linear_quantises_alike(nhm, k):
             assert bool(torch.isnan(got.view(torch.float32 if t == nhm.NHM_F32 else torch.bfloat16)[m - 1]).all())
 
 
+@pytest.mark.parametrize("m", [3, 20, 70])
+def test_mxfp4_linear_rows_far_apart(nhm, m):
+    """Rows of codes so far apart that the operand fills its 2 GiB."""
+    r = np.random.default_rng(14)
+    n, k = 130, 544
+    ld = ((1 << 31) // m - 64) // 16 * 16
+    x = torch.empty(m * ld, dtype=torch.uint8, device="cuda").as_strided((m, k // 2), (ld, 1))
+    x.copy_(u8(r.integers(0, 256, (m, k // 2))))
+    s = u8(r.integers(118, 130, (m, k // 32)))
+    w = nhm.Mxfp4Weight(u8(r.integers(0, 256, (n, k // 2))), u8(r.integers(118, 130, (n, k // 32))))
+    assert torch.equal(nhm.mxfp4_linear(x, w, a_scale=s), nhm.mxfp4_linear(x.contiguous(), w, a_scale=s))
+
+
 def test_mxfp4_linear_packed_scales(nhm):
     """A weight without packed scale codes gives the same bits; with them, new scale codes count from pack() on."""
     import ctypes as C
@@ -437,6 +450,31 @@ def test_scan_extremes(nhm):
         keep = ~bad[e]
         within(np.where(keep, got[e], 0), np.where(keep, ref, 0), tol * (1 + 2.0 ** -8) + lo.half_step(ref, True), "finite channels")
     assert np.isnan(got[50:, 3]).all() and not np.isfinite(got[45:, 9]).any()
+
+
+def test_scan_infinite_decay(nhm):
+    """A = -inf (A_log past 88.7) forgets a state within a step and leaves it alone where there is none: past a sequence's end,
+    whether it ends inside a block of tokens or its last chunk, and as a single token."""
+    r = np.random.default_rng(13)
+    dim, n = 16, 16
+    for lengths in ([5, 40], [1500]):
+        lay = Layer(nhm, r, dim, n)
+        lay.params.A_log[:, 3], lay.params.A_log[2] = 100.0, float("inf")
+        t, S = sum(lengths), len(lengths)
+        u, dt, B, C, z = scan_inputs(r, t, dim, n, True)
+        pool = torch.from_numpy(r.normal(size=(S, dim, n)).astype(np.float32)).cuda()
+        cu = np.concatenate([[0], np.cumsum(lengths)])
+        out = nhm.selective_scan_prefill(lay.params, u, dt, B, C, i32(cu), i32(np.arange(S)), i32(np.ones(S)), pool, z=z)
+        last = cu[1:] - 1
+        gone = f64(lay.params.A_log) > 88.7
+        delta = lo.softplus(f64(dt)[last] + f64(lay.params.dt_bias))
+        want = (delta * f64(u)[last])[:, :, None] * f64(B)[last][:, None, :]
+        assert np.isfinite(f64(out.view(torch.bfloat16))).all() and np.isfinite(f64(pool)).all()
+        within(f64(pool)[:, gone], want[:, gone], np.abs(want[:, gone]) * 20 * lo.U, "states forgotten")   # softplus 16 U and two products
+        one = nhm.selective_scan_decode(lay.params, u[:S], dt[:S], B[:S], C[:S], i32(np.arange(S)), pool, z=z[:S])
+        want = (lo.softplus(f64(dt)[:S] + f64(lay.params.dt_bias)) * f64(u)[:S])[:, :, None] * f64(B)[:S][:, None, :]
+        assert np.isfinite(f64(one.view(torch.bfloat16))).all()
+        within(f64(pool)[:, gone], want[:, gone], np.abs(want[:, gone]) * 20 * lo.U, "states forgotten in a step")
 
 
 def test_decode_is_a_prefill_of_one(nhm):
