@@ -4,7 +4,9 @@
 // With top = max x, S = sum exp(x - top), M = sum exp(x - top) (x - top) (no term of which is positive):
 //   log p(v) = (x_v - top) - log S,  H = log S - M / S,  rank = 1 + #{v before the token, by logit, then index}
 // One pass over the logits: a wave walks a strip of a row and keeps the running top, S, M, the count and
-// the strip's best logits (as the beam selection does); a second kernel joins a row's strips. Bound by bytes.
+// the strip's best logits (as the beam selection does); a second kernel joins a row's strips. Bound by bytes where rows are
+// many (1,021 x 131,072 bf16, 268 MB: 55 us without alternatives, 4.9 TB/s, 71 with five, for the cells read again and their sorting); one row
+// takes 7.2 us without and 15.8 with 20 alternatives, two launches of latency chains.
 #include <math.h>
 
 #include "nhm_internal.h"
