@@ -42,17 +42,18 @@ __device__ __forceinline__ bool has_slot(int slot, int n_slots) { return slot >=
 // ---------------------------------------------------------------- scan of prompts
 //
 // A lane holds one state of one channel (R of them where d_state > 16): 16 lanes are a channel, a wave is four, a
-// workgroup of four waves 16. What a token needs of its channel, dt and dt u, is formed once per 16 tokens by the
-// channel's lanes, a token each, and read back from LDS by all of them, as are B and C, staged as f32, transposed, for
-// the whole workgroup, 16 to 64 tokens at a time; loads are one such block ahead. (Lane moves inside the multiplications
-// halve their rate: 8.4 cycles against 4.5.) A token then costs mul, exp2, mul, fma, mul per state, and the sum over the
-// channel's lanes: the 16 tokens' products are summed together, each step keeping half of the tokens in half of the
-// lanes, so that the lane of state n ends with token n's sum, beside the u and z of that token that it loaded. The lanes of
+// workgroup of four waves 16. Tokens are staged 16 to 64 at a time, loads one such block ahead: a thread takes four
+// channels of a token, forms dt and dt u, and leaves them, u and z in LDS by channel, as it does B and C by state, widened to f32;
+// the lanes read four tokens of theirs at once. (Lane moves inside the multiplications halve their rate: 8.4 cycles
+// against 4.5.) A token then costs mul, exp2, mul, fma, mul per state, and the sum over the channel's lanes: 16 tokens' products
+// are summed together, each step keeping half of the tokens in half of the lanes, so that the lane of state n ends with
+// token n's sum, which it finishes and leaves in LDS, from where the workgroup stores 32 bytes of a row at a time. The lanes of
 // a channel are those of equal bits 2 and 3: the steps over bits 5 and 4 are swaps of two registers' halves and an add.
 //
 // Bound by the vector units: 15,360 tokens in 4 sequences x 4,096 channels x 16 states 380 us (508 MB, 1.3 TB/s), 9.7
-// instructions for a token in a wave, the units busy 89 % of the time; 524 tokens in 9 sequences x 2,688 22 us, where the longest
-// sequence's own chain counts (45 ns a token, 24 us for 512 tokens). Eight lanes to a channel of two states each save a sixth of
+// instructions for a token in a wave, the units busy 89 % of the time. Few tokens take the longest sequence's own chain (512 x
+// 4,096 24 us, 4,096 153), and a start of 5 us again where the workgroups, three to a CU by their LDS, do not all fit at once
+// (524 tokens in 6 sequences x 2,688, 260 the longest, 22 us). Eight lanes to a channel of two states each save a sixth of
 // the instructions and take 320 us in place of 356 for 16 sequences of 960, but 646 in place of 432 for 4 of 8,192 to 1,024 (both
 // as first written), whose few waves then wait for each other's results.
 
