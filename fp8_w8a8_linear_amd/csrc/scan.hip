@@ -16,19 +16,16 @@ namespace nhm {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], and log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by
-// its series: relative to log1p the first term left out is s^16 / 17 < 2^-29.
-__device__ __forceinline__ float softplus_series(float x) {
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], and log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3. atanh(s) / s =
+// 1 + s^2 / 3 + s^4 / 5 ... by the polynomial in s^2 <= 1/9 that meets it at the five Chebyshev nodes, within 2^-26.9 of the value.
+__device__ __forceinline__ float softplus_poly(float x) {
     const float e = __builtin_amdgcn_exp2f(-fabsf(x) * kLog2e);
     const float s = e * __builtin_amdgcn_rcpf(2.0f + e), q = s * s;
-    float p = fmaf(q, 1.0f / 15, 1.0f / 13);
-    p = fmaf(q, p, 1.0f / 11);
-    p = fmaf(q, p, 1.0f / 9);
-    p = fmaf(q, p, 1.0f / 7);
-    p = fmaf(q, p, 1.0f / 5);
-    p = fmaf(q, p, 1.0f / 3);
-    p = fmaf(q, p, 1.0f);
-    return fmaxf(x, 0.0f) + 2.0f * s * p;
+    float p = fmaf(q, 2 * 0.1407889f, 2 * 0.13982579f);
+    p = fmaf(q, p, 2 * 0.20012298f);
+    p = fmaf(q, p, 2 * 0.3333316f);
+    p = fmaf(q, p, 2.0f);
+    return fmaf(s, p, fmaxf(x, 0.0f));
 }
 
 // A log2(e) of a state, finite where A is not, so that a step of 0 (as past a sequence's end) keeps any state.
@@ -48,11 +45,12 @@ __device__ __forceinline__ bool has_slot(int slot, int n_slots) { return slot >=
 // against 4.5.) A token then costs mul, exp2, mul, fma, mul per state, and the sum over the channel's lanes: 16 tokens' products
 // are summed together, each step keeping half of the tokens in half of the lanes, so that the lane of state n ends with
 // token n's sum, which it finishes and leaves in LDS, from where the workgroup stores 32 bytes of a row at a time. The lanes of
-// a channel are those of equal bits 2 and 3: the steps over bits 5 and 4 are swaps of two registers' halves and an add.
+// a channel are those of equal bits 2 and 3: the steps over bits 5 and 4 are swaps of two registers' halves and an add; where a
+// lane has one state the states are swapped ahead of the first step, whose products then are its sum (378 us without that).
 //
-// Bound by the vector units: 15,360 tokens in 4 sequences x 4,096 channels x 16 states 380 us (508 MB, 1.3 TB/s), 9.7
-// instructions for a token in a wave, the units busy 89 % of the time. Few tokens take the longest sequence's own chain (512 x
-// 4,096 24 us, 4,096 153), and a start of 5 us again where the workgroups, three to a CU by their LDS, do not all fit at once
+// Bound by the vector units: 15,360 tokens in 4 sequences x 4,096 channels x 16 states 355 us (508 MB, 1.4 TB/s), 9.1
+// instructions for a token in a wave, the units busy 87 % of the time. Few tokens take the longest sequence's own chain (512 x
+// 4,096 24 us, 4,096 147), and a start of 5 us again where the workgroups, three to a CU by their LDS, do not all fit at once
 // (524 tokens in 6 sequences x 2,688, 260 the longest, 22 us). Eight lanes to a channel of two states each save a sixth of
 // the instructions and take 320 us in place of 356 for 16 sequences of 960, but 646 in place of 432 for 4 of 8,192 to 1,024 (both
 // as first written), whose few waves then wait for each other's results.
@@ -73,12 +71,11 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// The lane of state n: the sum over its channel of p[n].
-__device__ __forceinline__ float channel_sums(const float (&p)[16], int lane) {
+// The lane of state n: the sum over its channel of token n's products, from a[i]: the products' sums over bit 5, of token i in
+// the lanes with a clear bit 5, of token i + 8 in the others.
+__device__ __forceinline__ float channel_sums(const float (&a)[8], int lane) {
     const bool b1 = lane & 2, b0 = lane & 1;
-    float a[8], b[4], c[2];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = swap32_sum(p[i], p[i + 8]);
+    float b[4], c[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = swap16_sum(a[i], a[i + 4]);
 #pragma unroll
@@ -223,7 +220,7 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
         if (lt < kBlock)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float d = lt < left ? softplus_series(bf16_to_f32(half(rd, c)) + bias[c]) : 0.f;
+                const float d = lt < left ? softplus_poly(bf16_to_f32(half(rd, c)) + bias[c]) : 0.f;
                 s_dt[buf][0][4 * lq + c][lt] = d;
                 s_dt[buf][1][4 * lq + c][lt] = d * bf16_to_f32(half(ru, c));
                 if (kOut) s_uz[buf][4 * lq + c][lt] = half(ru, c) | half(rz, c) << 16;
@@ -233,17 +230,23 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
         if (t0 + kBlock < end) load(t0 + kBlock);
         if (kOut && t0 > beg) store(t0 - kBlock, buf ^ 1);
         auto tile = [&](int i) {
-            v4f dts[2][4], bc[kOut ? 2 : 1][R][4];
+            v4f dts[2][4], bc[kOut ? 2 : 1][R][4], cs[2][2];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
 #pragma unroll
                 for (int m = 0; m < 2; ++m) dts[m][k] = *reinterpret_cast<const v4f*>(&s_dt[buf][m][4 * wave + chan][16 * i + 4 * k]);
 #pragma unroll
-                for (int m = 0; m < (kOut ? 2 : 1); ++m)
+                for (int m = 0; m < (kOut && R > 1 ? 2 : 1); ++m)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
                         bc[m][r][k] = *reinterpret_cast<const v4f*>(&s_bc[buf][m][l16 + 16 * r][16 * i + 4 * k]);
             }
+            if constexpr (kOut && R == 1)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        cs[m][k] = *reinterpret_cast<const v4f*>(&s_bc[buf][1][(l16 & 7) + 8 * m][16 * i + (lane & 32) / 4 + 4 * k]);
             float p[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -251,12 +254,24 @@ __global__ __launch_bounds__(kScanWaves * 64) void scan_prefill_kernel(const Sca
                 for (int r = 0; r < R; ++r) {
                     const float e = __builtin_amdgcn_exp2f(dts[0][k >> 2][k & 3] * A2[r]);
                     h[r] = fmaf(e, h[r], dts[1][k >> 2][k & 3] * bc[0][r][k >> 2][k & 3]);
-                    if constexpr (kOut) p[k] = r == 0 ? h[r] * bc[1][r][k >> 2][k & 3] : fmaf(h[r], bc[1][r][k >> 2][k & 3], p[k]);
+                    if constexpr (kOut && R == 1) p[k] = h[0];
+                    else if constexpr (kOut) p[k] = r == 0 ? h[r] * bc[1][r][k >> 2][k & 3] : fmaf(h[r], bc[1][r][k >> 2][k & 3], p[k]);
                 }
             }
             if constexpr (kOut) {
+                float a8[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (R == 1) {
+                        // the states change lanes before their products, C read as they lie then: 24 instructions in place of 32
+                        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(p[k]), __float_as_uint(p[k + 8]), false, false);
+                        a8[k] = fmaf(__uint_as_float(x[1]), cs[1][k >> 2][k & 3], __uint_as_float(x[0]) * cs[0][k >> 2][k & 3]);
+                    } else {
+                        a8[k] = swap32_sum(p[k], p[k + 8]);
+                    }
+                }
                 const uint32_t uz = s_uz[buf][4 * wave + chan][16 * i + l16];
-                float y = fmaf(Dc, bf16_to_f32(uz & 0xffffu), channel_sums(p, lane));
+                float y = fmaf(Dc, bf16_to_f32(uz & 0xffffu), channel_sums(a8, lane));
                 if (a.z) y *= silu(bf16_to_f32(uz >> 16));
                 s_y[buf][16 * i + l16][4 * wave + chan] = (uint16_t)f32_to_bf16(y);
             }
@@ -388,7 +403,7 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(const ScanDecodeArgs a
         C[k] = bf16_to_f32(a.C[row * a.ld_c + (in ? s4 + k : 0)]);
     }
     const float u = bf16_to_f32(a.u[row * a.ld_u + ch]);
-    const float dt = softplus_series(bf16_to_f32(a.dt[row * a.ld_dt + ch]) + (a.dt_bias ? a.dt_bias[ch] : 0.f));
+    const float dt = softplus_poly(bf16_to_f32(a.dt[row * a.ld_dt + ch]) + (a.dt_bias ? a.dt_bias[ch] : 0.f));
     float y = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
