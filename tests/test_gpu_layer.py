@@ -587,6 +587,54 @@ def test_logprobs_row_past_two_gib(nhm):
     within(f64(lp)[-1], -np.log1p(np.exp(-1.0)), 2.0 ** -19, "log probability")
 
 
+# ---------------------------------------------------------------- offsets past 32 bits
+
+def far(t, ld, at=0):
+    """The same rows ld elements apart, in memory that is not initialised."""
+    v = torch.empty(t.shape[0] * ld, dtype=t.dtype, device="cuda").as_strided(t.shape, (ld, 1), at)
+    v.copy_(t)
+    return v
+
+
+def test_rows_far_apart(nhm):
+    """Rows of which the last lie more than 2^32 bytes, and 2^31 elements, from the first: the same bits as close together."""
+    r = np.random.default_rng(15)
+    t, ld, dim, n = 36000, 65536, 64, 16
+    x, dt, z, B, C = (bf16(r.normal(size=(t, c))) for c in (dim, dim, dim, n, n))
+    fx, fz = far(x, ld, 8), far(z, ld, 3)
+    assert all(torch.equal(a, b) for a, b in zip(nhm.mxfp4_quantize(fx), nhm.mxfp4_quantize(x)))
+    where = (i32([0, 20000, t - 5]), i32([1, 0]), i32([1, 0]))
+    w, b, lay = bf16(r.normal(size=(dim, 4))), bf16(r.normal(size=dim)), Layer(nhm, r, dim, n)
+    windows = bf16(r.normal(size=(2, 3, dim)))
+    cp = [windows.clone() for _ in range(2)]
+    out = far(torch.full_like(x, 3.0), ld, 16)
+    nhm.causal_conv_prefill(fx, w, b, *where, cp[0], out=out)
+    assert torch.equal(out.view(torch.int16), nhm.causal_conv_prefill(x, w, b, *where, cp[1])) and torch.equal(*cp)
+    states = torch.from_numpy(r.normal(size=(2, dim, n)).astype(np.float32)).cuda()
+    sp = [states.clone() for _ in range(2)]
+    out = far(torch.full_like(x, 3.0), ld, 5)
+    nhm.selective_scan_prefill(lay.params, fx, far(dt, ld, 1), far(B, ld), far(C, ld, 7), *where, sp[0], z=fz, out=out)
+    want = nhm.selective_scan_prefill(lay.params, x, dt, B, C, *where, sp[1], z=z)
+    assert torch.equal(out.view(torch.int16), want) and torch.equal(*sp)
+    slots = i32(np.where(np.arange(t) == t - 1, 0, -1))
+    for fs in (nhm.causal_conv_decode(fx, w, b, slots, cp[0]), nhm.causal_conv_decode(x, w, b, slots, cp[1])), (
+            nhm.selective_scan_decode(lay.params, fx, dt, B, C, slots, sp[0], z=fz),
+            nhm.selective_scan_decode(lay.params, x, dt, B, C, slots, sp[1], z=z)):
+        assert torch.equal(*fs) and bool(fs[0][-1].any()) and not fs[0][:-1].any()
+    assert torch.equal(*cp) and torch.equal(*sp)
+
+
+@pytest.mark.parametrize("m,ld", [(3, 1 << 30), (40, 1 << 26), (70, 1 << 25), (300, 1 << 23), (300, (1 << 23) + 1)])
+def test_mxfp4_linear_outputs_far_apart(nhm, m, ld):
+    r = np.random.default_rng(m)
+    n, k = 136, 256
+    w = nhm.Mxfp4Weight(u8(r.integers(0, 256, (n, k // 2))), u8(r.integers(118, 130, (n, k // 32))))
+    x = bf16(r.normal(size=(m, k)))
+    out = torch.empty(m * ld, dtype=torch.float32, device="cuda").as_strided((m, n), (ld, 1))
+    nhm.mxfp4_linear(x, w, out=out)
+    assert torch.equal(out, nhm.mxfp4_linear(x, w, out_type=nhm.NHM_F32))
+
+
 # ---------------------------------------------------------------- streams and graphs
 
 def everything(nhm, s, stream=None):
