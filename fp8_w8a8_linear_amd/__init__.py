@@ -631,14 +631,18 @@ def batch_plan(lengths, plan: BatchPlan, past=None, adapters=None, stream=None):
 
 def _row_view(t, name, dev, dtypes, rows, cols):
     """Checks a [rows, cols] tensor whose rows may be slices of wider ones; its row stride in elements."""
-    import torch
-    if isinstance(t, torch.Tensor) and t.get_device() == dev.index and t.dtype in dtypes and t.shape == (rows, cols):
+    try:
+        fits = t.get_device() == dev.index and t.dtype in dtypes and t.shape == (rows, cols)
+    except AttributeError:      # not a tensor
+        fits = False
+    if fits:
         ld, step = t.stride()
         if rows == 0 or (rows == 1 and step == 1):
             return cols
         if step == 1 and ld >= cols:
             return ld
         raise ValueError(f"{name} of strides {t.stride()}: expected rows of consecutive elements")
+    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
     if t.get_device() != dev.index:
@@ -819,14 +823,13 @@ def _scan(params, u, dt, B, C_, z, slot_idx, ssm_pool, out, stream, n_seqs, inde
     dev = _device_of(u, "u")
     rows, dim, n = _shape2(u, "u")[0], params.dim, params.d_state
     bf, i32 = _bf16_types(), (torch.int32,)
-    args = []
-    for t, name, cols in ((u, "u", dim), (dt, "dt", dim), (B, "B", n), (C_, "C", n), (z, "z", dim)):
-        args += [None, 0] if t is None and name == "z" else [t, _row_view(t, name, dev, bf, rows, cols)]
+    lds = [_row_view(u, "u", dev, bf, rows, dim), _row_view(dt, "dt", dev, bf, rows, dim), _row_view(B, "B", dev, bf, rows, n),
+           _row_view(C_, "C", dev, bf, rows, n), 0 if z is None else _row_view(z, "z", dev, bf, rows, dim)]
     if ssm_pool.dim() != 3:
         raise ValueError(f"ssm_pool of shape {tuple(ssm_pool.shape)}: expected [slots, dim, d_state]")
     _on(dev, [(params.A_log, "params", (torch.float32,), None), (slot_idx, "slot_idx", i32, (n_seqs,)),
               (ssm_pool, "ssm_pool", bf + (torch.float32,), (ssm_pool.shape[0], dim, n))] + [(t, m, i32, s) for t, m, s in index])
-    args = [_addr(a) if isinstance(a, torch.Tensor) else a for a in args]
+    args = (u.data_ptr(), lds[0], dt.data_ptr(), lds[1], B.data_ptr(), lds[2], C_.data_ptr(), lds[3], _addr(z), lds[4])
     if out is None:
         return dev, rows, args, _empty((rows, dim), torch.int16, dev, stream), dim
     return dev, rows, args, out, _row_view(out, "out", dev, bf, rows, dim)
