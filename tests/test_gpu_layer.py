@@ -477,6 +477,28 @@ def test_scan_infinite_decay(nhm):
         within(f64(pool)[:, gone], want[:, gone], np.abs(want[:, gone]) * 20 * lo.U, "states forgotten in a step")
 
 
+@pytest.mark.parametrize("n", [4, 8, 16, 20, 64])
+def test_scan_values_that_are_not_finite(nhm, n):
+    """Infinities and NaN stay in their channel and sequence, also beside the lanes of no state; the others' bits stay."""
+    r = np.random.default_rng(n)
+    dim, t = 40, 150
+    lay = Layer(nhm, r, dim, n)
+    u, dt, B, C, z = scan_inputs(r, t, dim, n, True)
+    where = (i32([0, 100, t]), i32([0, 1]), i32([0, 0]))
+    run = lambda u, dt, p: f64(nhm.selective_scan_prefill(lay.params, u, dt, B, C, *where, p, z=z).view(torch.bfloat16))  # noqa: E731
+    pools = torch.zeros(2, dim, n, device="cuda"), torch.zeros(2, dim, n, device="cuda")
+    clean = run(u, dt, pools[0])
+    bu, bdt = u.clone(), dt.clone()
+    bu[20, 5], bu[90, 9], bdt[33, 13], bdt[110, 17] = float("inf"), float("nan"), float("nan"), float("inf")
+    got = run(bu, bdt, pools[1])
+    bad = np.zeros((t, dim), bool)
+    bad[20:100, 5] = bad[90:100, 9] = bad[33:100, 13] = bad[110:, 17] = True
+    assert np.array_equal(got[~bad], clean[~bad]) and not np.isfinite(got[bad]).any()
+    kept = np.ones((2, dim), bool)
+    kept[0, [5, 9, 13]] = kept[1, 17] = False
+    assert np.array_equal(f64(pools[1])[kept], f64(pools[0])[kept])
+
+
 def test_decode_is_a_prefill_of_one(nhm):
     """Prompts, then tokens one by one, against the whole as one prompt: the same recurrence, within its roundings."""
     r = np.random.default_rng(10)
