@@ -62,8 +62,9 @@ __global__ __launch_bounds__(kScoreWaves * 64, F32 ? 3 : 4) void score_strip_ker
             for (int i = 0; i < 32; ++i) asm volatile("" : "+v"(x[i]));
             if (p + kPiece < p_end) cur.load(base, p + kPiece, g.vocab, lane);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) mx = max3(mx, x[i], x[i + 1]);
-            if (__ballot(mx != mx)) {                        // a signalling NaN: max3 passes it on
+            for (int i = 0; i < 32; i += 2) mx = maximum3(mx, x[i], x[i + 1]);
+            // A piece with a NaN is cleaned and its maxima taken again. (The terms below do not show one: their bound takes it to 0.)
+            if (__ballot(mx != mx)) {
                 mx = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {

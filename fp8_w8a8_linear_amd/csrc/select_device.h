@@ -48,10 +48,17 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 __device__ __forceinline__ uint32_t take(uint32_t v, int src) { return (uint32_t)__builtin_amdgcn_readlane((int)v, src); }
 
-// max3: quiet NaN passed over; a signalling one comes out as NaN.
+// max3: quiet NaN passed over; a signalling one comes out as a quiet one, which the next max3 passes over together with
+// what was in front of it, so that a chain of them does not show it.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+// maximum3: NaN where any of the three is one, quiet or signalling, so that a chain of them ends as NaN.
+__device__ __forceinline__ float maximum3(float a, float b, float c) {
+    float r;
+    asm("v_maximum3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
     return r;
 }
 __device__ __forceinline__ double wave_sum_f64(double v) {
