@@ -127,8 +127,9 @@ typedef struct nhm_scan_params {
  *   B, C          (device) bf16 [.., ld_*], d_state columns, shared by the channels; likewise
  *   ssm_pool      (device) f32 or bf16 (ssm_type) [n_slots, dim, d_state], 16-byte aligned; updated in place
  *   ws            (device, 256-byte aligned) nhm_selective_scan_prefill_workspace_bytes(...) bytes (may be 0: NULL)
- * From a token on whose u or dt is not finite, its channel's outputs of that sequence are infinite or NaN (which of them may
- * differ between the two forms); other channels and sequences do not depend on it.
+ * From a token on whose u is not finite, or whose dt_raw + dt_bias is NaN or +inf, its channel's outputs of that sequence are
+ * infinite or NaN (which of them may differ between the two forms); other channels and sequences do not depend on it.
+ * A dt_raw + dt_bias of -inf is a step of 0, as softplus has it: with a finite u the state stays as it is.
  * Slots, cu_seqlens, has_initial, padding and the rows behind the last sequence: as for the convolution above.
  * Errors: NHM_ERR_NULL, NHM_ERR_SHAPE, NHM_ERR_ALIGN, NHM_ERR_UNSUPPORTED, NHM_ERR_WORKSPACE, NHM_ERR_HIP. */
 NHM_API nhm_status nhm_selective_scan_decode(const nhm_scan_params* p, const uint16_t* u, int64_t ld_u,

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_layer import bf16, check_scores, nhm  # noqa: E402,F401
+from tests.test_gpu_layer import Layer, bf16, check_scores, check_state, f64, i32, nhm, scan_inputs, within  # noqa: E402,F401
 
 
 # ---------------------------------------------------------------- scoring of tokens
@@ -51,3 +51,69 @@ def test_logprobs_signalling_nan_behind(nhm, dtype, kind):
         put_signalling_nan(t, row, nan)
     check_scores(nhm, t, tokens, 5)
     check_scores(nhm, t, tokens, 0)
+
+
+# ---------------------------------------------------------------- scan: values that are not finite
+
+@pytest.mark.parametrize("n", [4, 16, 20, 64])
+@pytest.mark.parametrize("first", [150, 2600])
+def test_scan_not_finite_in_every_form(nhm, n, first):
+    """u of infinity or NaN and dt of NaN or +inf keep to their channel and sequence, in the sequence's first tokens, its middle and its
+    last ones, whether it is scanned whole or in chunks; dt of -inf, once or at every token, is a step of 0."""
+    r = np.random.default_rng(n + first)
+    dim, t = 40, first + 200
+    assert (nhm.selective_scan_prefill_workspace_bytes(dim, n, t, 2) > 0) == (first > 1000)
+    lay = Layer(nhm, r, dim, n)
+    u, dt, B, C, z = scan_inputs(r, t, dim, n, True)
+    states = torch.from_numpy(r.normal(size=(2, dim, n)).astype(np.float32)).cuda()
+    where = (i32([0, first, t]), i32([0, 1]), i32([1, 1]))
+    run = lambda u, dt, p: f64(nhm.selective_scan_prefill(lay.params, u, dt, B, C, *where, p, z=z).view(torch.bfloat16))  # noqa: E731
+    pools = states.clone(), states.clone()
+    clean = run(u, dt, pools[0])
+    bu, bdt, bad = u.clone(), dt.clone(), np.zeros((t, dim), bool)
+    inf, nan, mid, last = float("inf"), float("nan"), first // 2, first - 3
+    for x, at, ch, v in [(bu, 20, 5, inf), (bu, 0, 6, nan), (bdt, 3, 7, inf), (bdt, mid, 13, nan), (bdt, mid + 1, 14, inf), (bu, mid + 2, 15, -inf),
+                         (bu, last, 9, nan), (bdt, last, 10, inf), (bu, last + 2, 11, inf), (bdt, first + 10, 17, inf), (bu, first, 18, nan)]:
+        x[at, ch] = v
+        bad[at:first if at < first else t, ch] = True
+    still = [21, 25, 39]
+    bdt[mid, 21], bdt[:, 25], bdt[[0, last, first, t - 1], 39] = -inf, -inf, -inf
+    got = run(bu, bdt, pools[1])
+    same = ~bad
+    same[:, still] = False
+    assert np.array_equal(got[same], clean[same]) and not np.isfinite(got[bad]).any()
+    kept = np.ones((2, dim), bool)
+    kept[0, [5, 6, 7, 13, 14, 15, 9, 10, 11]] = kept[1, [17, 18]] = kept[:, still] = False
+    assert np.array_equal(f64(pools[1])[kept], f64(pools[0])[kept])
+    for i, e in enumerate((slice(0, first), slice(first, t))):
+        ref, tol, h, err = lay.ref(f64(u)[e], f64(bdt)[e], f64(B)[e], f64(C)[e], f64(states)[i], f64(z)[e])
+        within(got[e][:, still], ref[:, still], (tol * (1 + 2.0 ** -8) + lo.half_step(ref, True))[:, still], "steps of 0")
+        check_state(f64(pools[1])[i, still], h[still], err[still], False)
+    assert torch.equal(pools[1][:, 25], states[:, 25])
+
+
+@pytest.mark.parametrize("n", [4, 16, 20, 64])
+def test_scan_decode_not_finite(nhm, n):
+    """The same for single tokens: a step of 0 leaves the state's bits alone."""
+    r = np.random.default_rng(n)
+    dim = 40
+    lay = Layer(nhm, r, dim, n)
+    u, dt, B, C, z = scan_inputs(r, 3, dim, n, True)
+    states = torch.from_numpy(r.normal(size=(3, dim, n)).astype(np.float32)).cuda()
+    run = lambda u, dt, p: f64(nhm.selective_scan_decode(lay.params, u, dt, B, C, i32([2, 0, 1]), p, z=z).view(torch.bfloat16))  # noqa: E731
+    pools = states.clone(), states.clone()
+    clean = run(u, dt, pools[0])
+    inf, nan = float("inf"), float("nan")
+    bu, bdt, bad = u.clone(), dt.clone(), np.zeros((3, dim), bool)
+    for x, at, ch, v in [(bu, 0, 0, inf), (bu, 1, 5, nan), (bdt, 2, 7, inf), (bdt, 0, 39, nan)]:
+        x[at, ch] = v
+        bad[at, ch] = True
+    bdt[:, 21] = -inf
+    got = run(bu, bdt, pools[1])
+    same = ~bad
+    same[:, 21] = False
+    assert np.array_equal(got[same], clean[same]) and not np.isfinite(got[bad]).any()
+    assert torch.equal(pools[1][:, 21], states[:, 21])
+    for i, s in enumerate([2, 0, 1]):
+        ref, tol, _, _ = lay.ref(f64(u)[i:i + 1], f64(bdt)[i:i + 1], f64(B)[i:i + 1], f64(C)[i:i + 1], f64(states)[s], f64(z)[i:i + 1])
+        within(got[i, 21], ref[0, 21], (tol * (1 + 2.0 ** -8) + lo.half_step(ref, True))[0, 21], "a step of 0")
