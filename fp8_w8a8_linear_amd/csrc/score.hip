@@ -240,23 +240,10 @@ nhm_status launch_score(ScoreArgs g, void* ws, hipStream_t st) {
     count_launch(Kern::kScoreRows, g.rows);
     const nhm_status s = check_launch("token scores");
     if (s != NHM_OK) return s;
-    // a launch holds fewer than 2^32 threads: rows < 2^24 of at most 512 do not fit one
-    constexpr int64_t kJoinRows = int64_t(1) << 22;
+    // one launch: fewer than 2^24 rows of one wave are fewer than 2^30 threads (more than 8 strips, for which a row takes 16
+    // waves, have only calls of at most 511 rows)
     const int waves = g.n_top > 0 && g.n_strips > 8 ? kJoinWaves : 1;
-    for (int64_t r0 = 0; r0 < g.rows; r0 += kJoinRows) {
-        ScoreArgs p = g;
-        p.rows = g.rows - r0 < kJoinRows ? g.rows - r0 : kJoinRows;
-        p.logits = static_cast<const char*>(g.logits) + r0 * g.ld * (g.f32 ? 4 : 2);
-        if (p.tokens) p.tokens += r0;
-        if (p.logprobs) p.logprobs += r0;
-        if (p.ranks) p.ranks += r0;
-        if (p.entropy) p.entropy += r0;
-        if (p.top_logprobs) p.top_logprobs += r0 * g.n_top;
-        if (p.top_tokens) p.top_tokens += r0 * g.n_top;
-        p.strips += r0 * g.n_strips;
-        p.strip_keys += r0 * g.n_strips * g.n_top;
-        score_join_kernel<<<dim3((unsigned)p.rows), dim3(waves * 64), 0, st>>>(p);
-    }
+    score_join_kernel<<<dim3((unsigned)g.rows), dim3(waves * 64), 0, st>>>(g);
     count_launch(Kern::kScoreJoin, g.rows);
     return check_launch("token scores' join");
 }

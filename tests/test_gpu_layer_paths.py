@@ -53,6 +53,26 @@ def test_logprobs_signalling_nan_behind(nhm, dtype, kind):
     check_scores(nhm, t, tokens, 0)
 
 
+def test_logprobs_of_many_rows(nhm):
+    """More than 2^22 rows, the last of them among them, against torch's log softmax in 64 bits."""
+    rows, V = (1 << 22) + 5, 7
+    g = torch.Generator(device="cuda")
+    g.manual_seed(22)
+    x = (torch.randn(rows, V, generator=g, device="cuda") * 2).to(torch.bfloat16)
+    tokens = torch.randint(-1, V, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    lp, rank, ent, tl, tt = nhm.token_logprobs(x, tokens, n_top=2)
+    want, t = torch.log_softmax(x.double(), dim=1), tokens.long().clamp(min=0)[:, None]
+    none = tokens < 0
+    own, at = x.gather(1, t), torch.arange(V, device="cuda")
+    place = 1 + ((x > own) | ((x == own) & (at < t))).sum(dim=1)
+    tol = 2.0 ** -19 + 2.0 ** -24 * 64          # as the oracle's; no log probability is below -64
+    assert bool(((lp - want.gather(1, t)[:, 0]).abs() <= tol)[~none].all()) and not lp[none].any()
+    assert torch.equal(rank.long(), torch.where(none, 0, place))
+    assert bool(((ent + (want.exp() * want).sum(dim=1)).abs() <= 2 * tol).all())
+    order = torch.sort(x.float(), dim=1, descending=True, stable=True)[1][:, :2]
+    assert torch.equal(tt.long(), order) and bool(((tl - want.gather(1, order)).abs() <= tol).all())
+
+
 # ---------------------------------------------------------------- scan: values that are not finite
 
 @pytest.mark.parametrize("n", [4, 16, 20, 64])
