@@ -73,6 +73,78 @@ def test_logprobs_of_many_rows(nhm):
     assert torch.equal(tt.long(), order) and bool(((tl - want.gather(1, order)).abs() <= tol).all())
 
 
+def strip_tolerance(x, pieces):
+    """(of the log of the sum, of the entropy) of a row that waves walk in strips of up to `pieces` pieces. D: an entry's distance from
+    the row's largest logit in log2, p its probability. A term and its rescalings, at most `pieces` of them, each an exp2 (2 U) of an
+    argument of three roundings: 2 U (1 + pieces) + 3 ln2 U D; seven sums in f32 to a piece's term. The moment's terms are D times that,
+    with D's own three roundings and 32 sums."""
+    x = np.where(np.isnan(x), -np.inf, x)
+    if not np.isfinite(x.max()):
+        return 2.0 ** -23, 2.0 ** -23           # counts, exact, and a logarithm
+    D = (x.max() - x) / np.log(2)
+    p = np.exp2(-D) / np.exp2(-D).sum()
+    D, p = D[p > 0], p[p > 0]
+    each = 2 * (1 + pieces) + 2.1 * D
+    s = lo.U * (p * (each + 7)).sum()
+    return s, s + np.log(2) * (lo.U * (p * D * (each + 35)).sum() + (p * D).sum() * s)
+
+
+@pytest.mark.parametrize("rows,V,pieces", [(1400, 40000, 7), (4100, 20001, 10)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logprobs_over_many_pieces(nhm, rows, V, pieces, dtype):
+    """Strips of several pieces and of more than one span of eight: maxima that rise and fall along the row, infinities, NaN and masked
+    runs in its later pieces, tokens and alternatives anywhere."""
+    strips = -(-(-(-V // 2048)) // pieces)
+    assert nhm.token_logprobs_workspace_bytes(rows, V, 0) == -(-rows * strips * 24 // 256) * 256, "other strips: choose other sizes"
+    r = np.random.default_rng(V)
+    special = r.normal(size=(18, V)) * 3
+    special[0] = np.sort(special[0] * 2)
+    special[1] = np.sort(special[1] * 2)[::-1]
+    special[2, V - 3] = 120.0
+    special[3, :V * 3 // 5] = -np.inf
+    special[4, 6 * 2048 + lane_place(7, 33, dtype)] = np.inf
+    special[5, V // 2:][r.random(V - V // 2) < 0.3] = np.nan
+    special[6] += np.arange(V) // 2048 * 8.0
+    special[7] = -np.inf
+    special[7, V - 1] = -3.0
+    special[8] = -np.inf
+    special[9] = 1.25
+    special[10] = np.round(special[10] / 3)
+    special[11, V - 100:] += 30.0
+    special[12, 17::2048] = 40.0
+    special[13, [3, V - 2]] = np.inf
+    special[14] -= np.arange(V) // 2048 * 8.0
+    special[15, 8 * 2048 + lane_place(20, 5, dtype)] = 150.0
+    special[16, :2048] = np.nan
+    special[16, 9 * 2048:] = -np.inf
+    special[17] = np.where(np.arange(V) < V - 4096, -1e30, special[17])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    t = (torch.randn(rows, V, generator=g, device="cuda") * 3).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    at = np.r_[r.permutation(np.arange(1, rows - 1))[:17], rows - 1]
+    t[torch.from_numpy(at).cuda()] = to_logits(special, dtype)
+    put_signalling_nan(t, int(at[4]), 6 * 2048 + lane_place(8, 33, dtype))
+    put_signalling_nan(t, int(at[15]), 8 * 2048 + lane_place(21, 5, dtype))
+    look = np.r_[at, 0, r.integers(0, rows, 6)]
+    X = f64(t[torch.from_numpy(look).cuda()])
+    tolerance = [strip_tolerance(x, pieces) for x in X]
+    for call, n_top in enumerate((20, 64, 0)):
+        tokens = r.integers(0, V, rows)
+        tokens[look] = r.integers([0, V // 3, V - 2048][call], [2048, V * 2 // 3, V][call], len(look))
+        if call == 1:
+            tokens[look] = np.nanargmax(np.where(np.isnan(X), -np.inf, X), axis=1)
+        lp, rank, ent, tl, tt = nhm.token_logprobs(t, i32(tokens), n_top=n_top)
+        lp, ent, tl = f64(lp), f64(ent), f64(tl)
+        for i, x, (tol, tol_h) in zip(look, X, tolerance):
+            w_lp, w_rank, w_ent, w_tl, w_tt = lo.token_logprobs(x, tokens[i], n_top)
+            what = f"row {i}, place {np.flatnonzero(look == i)}, call {call}"
+            within(lp[i], w_lp, tol + lo.half_step(np.nan_to_num(w_lp, neginf=0), False), what + ": log probability")
+            assert int(rank[i]) == w_rank, f"{what}: rank {int(rank[i])} for {w_rank}"
+            within(ent[i], w_ent, tol_h + lo.half_step(w_ent, False), what + ": entropy")
+            assert tt[i].tolist() == w_tt.tolist(), what + ": alternatives"
+            within(tl[i], w_tl, tol + lo.half_step(np.nan_to_num(w_tl, neginf=0), False), what + ": alternatives' log probabilities")
+
+
 # ---------------------------------------------------------------- scan: values that are not finite
 
 @pytest.mark.parametrize("n", [4, 16, 20, 64])
