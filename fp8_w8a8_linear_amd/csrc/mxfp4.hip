@@ -591,11 +591,11 @@ nhm_status launch_mx_pack(const uint8_t* scales, int64_t rows, int64_t k, uint32
     return check_launch("mxfp4 scales");
 }
 
-// PER_CU: workgroups that a CU holds at once; more tiles than that follow one another in the same workgroups, whose loads
-// then run ahead into the next tile.
-template <int TN, int TM, int NWN, int NWM, int KB, int RING, int PER_CU>
-static void launch_tile(MxGemmArgs g, hipStream_t st) {
-    const int64_t tiles = (g.n + TN - 1) / TN * ((g.m + TM - 1) / TM), most = 256 * PER_CU;
+// More tiles than the chip holds workgroups of follow one another in the same workgroups, whose loads then run ahead into the
+// next tile.
+template <int TN, int TM, int NWN, int NWM, int KB, int RING>
+static void launch_tile(MxGemmArgs g, const MxTile& t, hipStream_t st) {
+    const int64_t tiles = (g.n + TN - 1) / TN * ((g.m + TM - 1) / TM), most = 256 * t.per_cu;
     const int64_t blocks = tiles < most ? (tiles + 7) / 8 * 8 : most;
     // stores of 16 bytes at 32-bit offsets within a tile
     const int64_t size = g.out_f32 ? 4 : 2;
@@ -617,18 +617,11 @@ nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st) {
         count_launch(Kern::kMxRows, g.m);
         return check_launch("mxfp4 linear");
     }
-    // Tiles by rounds over the chip, us at 15,360 x 10,304 x 2,688 | 15,360 x 2,688 x 4,096 | 2,048 x 10,304 x 2,688: 256 x 256, one to a
-    // CU, 280 | 110 | 49.6 (10, 3 and 2 rounds), 128 x 128, two to a CU, 305 | 104 | 47.7 (19, 5 and 3): a round of the small ones
-    // takes 0.57 of one of the large. While the 128 x 128 tiles do not fill the chip, smaller ones: 477 x 10,304 x 2,688 17.5 with 128 x 128
-    // (324 tiles), 19.3 with 128 x 64, 19.9 with 64 x 64; 1,024 x 4,096 x 4,096 17.4 (256), 16.8, 18.5; 477 x 2,688 x 4,096 14.8 (84), 10.9
-    // (168), 10.1 (336).
-    auto count = [&](int64_t tn, int64_t tm) { return (g.n + tn - 1) / tn * ((g.m + tm - 1) / tm); };
-    const int64_t rounds256 = (count(256, 256) + 255) / 256, rounds128 = (count(128, 128) + 511) / 512;
-    // (f32 outputs of a 256 x 256 tile do not fit the registers beside its sums: 405 us.)
-    if (!g.out_f32 && count(256, 256) > 256 && rounds256 * 100 < rounds128 * 57) launch_tile<256, 256, 2, 4, 64, 4, 1>(g, st);
-    else if (count(128, 128) >= 300) launch_tile<128, 128, 2, 2, 128, 2, 2>(g, st);
-    else if (count(128, 64) >= 400) launch_tile<128, 64, 2, 2, 128, 2, 3>(g, st);
-    else launch_tile<64, 64, 2, 2, 128, 2, 4>(g, st);
+    const MxTile t = mx_tile(g.m, g.n, g.out_f32 != nullptr);
+    if (t.tn == 256) launch_tile<256, 256, 2, 4, 64, 4>(g, t, st);
+    else if (t.tm == 128) launch_tile<128, 128, 2, 2, 128, 2>(g, t, st);
+    else if (t.tn == 128) launch_tile<128, 64, 2, 2, 128, 2>(g, t, st);
+    else launch_tile<64, 64, 2, 2, 128, 2>(g, t, st);
     count_launch(Kern::kMxTile, g.m);
     return check_launch("mxfp4 linear");
 }

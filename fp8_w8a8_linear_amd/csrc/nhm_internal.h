@@ -393,6 +393,23 @@ bool mx_tiled(int64_t m);
 // 8 rows 7.5, and after a launch 6.3 and 6.5. The codes have to fit LDS.
 inline bool mx_rows_quantise(int64_t m, int64_t k) { return m <= 4 && m * ((k + 255) / 256) * 136 <= 32768; }
 inline int64_t mx_packed_words(int64_t rows, int64_t k) { return rows * ((k / 32 + 3) / 4); }
+// The tile of a product of more than 64 rows: its features and rows, and the workgroups of it that a CU holds at once (256 of
+// those take the tiles in turn).
+struct MxTile { int tn, tm, per_cu; };
+// By rounds over the chip, us at 15,360 x 10,304 x 2,688 | 15,360 x 2,688 x 4,096 | 2,048 x 10,304 x 2,688: 256 x 256, one to a
+// CU, 280 | 110 | 49.6 (10, 3 and 2 rounds), 128 x 128, two to a CU, 305 | 104 | 47.7 (19, 5 and 3): a round of the small ones
+// takes 0.57 of one of the large. While the 128 x 128 tiles do not fill the chip, smaller ones: 477 x 10,304 x 2,688 17.5 with 128 x 128
+// (324 tiles), 19.3 with 128 x 64, 19.9 with 64 x 64; 1,024 x 4,096 x 4,096 17.4 (256), 16.8, 18.5; 477 x 2,688 x 4,096 14.8 (84), 10.9
+// (168), 10.1 (336).
+inline MxTile mx_tile(int64_t m, int64_t n, bool f32) {
+    auto count = [&](int64_t tn, int64_t tm) { return (n + tn - 1) / tn * ((m + tm - 1) / tm); };
+    const int64_t rounds256 = (count(256, 256) + 255) / 256, rounds128 = (count(128, 128) + 511) / 512;
+    // (f32 outputs of a 256 x 256 tile do not fit the registers beside its sums: 405 us.)
+    if (!f32 && count(256, 256) > 256 && rounds256 * 100 < rounds128 * 57) return MxTile{256, 256, 1};
+    if (count(128, 128) >= 300) return MxTile{128, 128, 2};
+    if (count(128, 64) >= 400) return MxTile{128, 64, 3};
+    return MxTile{64, 64, 4};
+}
 nhm_status launch_mx_pack(const uint8_t* scales, int64_t rows, int64_t k, uint32_t* packed, hipStream_t st);
 nhm_status launch_mx_gemm(const MxGemmArgs& g, hipStream_t st);
 

@@ -9,7 +9,36 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_layer import Layer, bf16, check_scores, check_state, f64, i32, nhm, scan_inputs, within  # noqa: E402,F401
+from tests.test_gpu_layer import Layer, bf16, check_scores, check_state, f64, i32, nhm, scan_inputs, u8, within  # noqa: E402,F401
+from tests.test_layer_tiles import TILE_CASES  # noqa: E402
+
+
+# ---------------------------------------------------------------- MXFP4 projection: the tiles of many rows
+
+@pytest.mark.parametrize("m,n,k,codes,f32,tn,tm,turns", TILE_CASES)
+def test_mxfp4_linear_tiles(nhm, m, n, k, codes, f32, tn, tm, turns):
+    """Every tile, one and several in turn of a workgroup, stores of whole 16 bytes and single ones, ragged edges on both sides; whole
+    outputs against products in 64 bits, and nothing stored beside them."""
+    print(m, n, k, tn, tm, turns, flush=True)
+    r = np.random.default_rng(m + n + k)
+    w, ws = r.integers(0, 16, (n, k)).astype(np.uint8), r.integers(110, 135, (n, k // 32)).astype(np.uint8)
+    weight = nhm.Mxfp4Weight(u8(lo.mxfp4_pack(w)), u8(ws))
+    if codes:
+        a, s = r.integers(0, 16, (m, k)).astype(np.uint8), r.integers(110, 135, (m, k // 32)).astype(np.uint8)
+        x, xs = u8(lo.mxfp4_pack(a)), u8(s)
+    else:
+        x, xs = bf16(r.normal(size=(m, k)) * np.exp2(r.integers(-8, 8, (m, 1)).astype(float))), None
+        a, s = lo.mxfp4_quantize(f64(x))
+    right = 0 if n % 8 == 0 else 5               # rows of whole 16 bytes behind their like, odd ones behind odd ones
+    out = torch.full((m + 2, n + right), 7.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    nhm.mxfp4_linear(x, weight, a_scale=xs, out=out[1:m + 1, :n])
+    av, wv = (torch.from_numpy(v).cuda() for v in (lo.mxfp4_values(a, s), lo.mxfp4_values(w, ws).T.copy()))
+    ref, tol = av @ wv, lo.U * (k / 128 + 18) * (av.abs() @ wv.abs())          # as the oracle's
+    tol = tol * (1 + 2.0 ** -8) + ref.abs() * (lo.U if f32 else 2.0 ** -8)
+    wrong = ~((out[1:m + 1, :n].double() - ref).abs() <= tol)
+    assert not bool(wrong.any()), f"{int(wrong.sum())} outside, first at {wrong.nonzero()[0].tolist()}"
+    out[1:m + 1, :n] = 7.0
+    assert bool((out == 7.0).all()), "stores outside the output"
 
 
 # ---------------------------------------------------------------- scoring of tokens
