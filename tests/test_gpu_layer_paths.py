@@ -238,3 +238,32 @@ def test_scan_decode_not_finite(nhm, n):
     for i, s in enumerate([2, 0, 1]):
         ref, tol, _, _ = lay.ref(f64(u)[i:i + 1], f64(bdt)[i:i + 1], f64(B)[i:i + 1], f64(C)[i:i + 1], f64(states)[s], f64(z)[i:i + 1])
         within(got[i, 21], ref[0, 21], (tol * (1 + 2.0 ** -8) + lo.half_step(ref, True))[0, 21], "a step of 0")
+
+
+# ---------------------------------------------------------------- single tokens of many sequences
+
+def test_decode_of_many_rows(nhm):
+    """More rows than a launch's y extent, of more than 2^32 threads together: the rows with a slot as in a call of their own, padding zero."""
+    rows, dim, n = 65535 + 5, 4104, 64
+    r = np.random.default_rng(24)
+    lay = Layer(nhm, r, dim, n)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(24)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    u, dt, B, C, z = rand(rows, dim), rand(rows, dim), rand(rows, n), rand(rows, n), rand(rows, dim)
+    w, b = bf16(r.normal(size=(dim, 4))), bf16(r.normal(size=dim))
+    at = torch.tensor([0, 65534, 65535, rows - 1], device="cuda")
+    slots = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    slots[at] = i32([3, 0, 2, 1])
+    states, windows = torch.randn(4, dim, n, generator=g, device="cuda"), rand(4, 3, dim)
+    pools = states.clone(), states.clone()
+    out = nhm.selective_scan_decode(lay.params, u, dt, B, C, slots, pools[0], z=z)
+    want = nhm.selective_scan_decode(lay.params, u[at], dt[at], B[at], C[at], i32([3, 0, 2, 1]), pools[1], z=z[at])
+    assert torch.equal(out[at], want) and torch.equal(*pools) and not torch.equal(pools[0], states)
+    out[at] = 0
+    assert not out.any()
+    pools = windows.clone(), windows.clone()
+    out = nhm.causal_conv_decode(u, w, b, slots, pools[0])
+    assert torch.equal(out[at], nhm.causal_conv_decode(u[at], w, b, i32([3, 0, 2, 1]), pools[1])) and torch.equal(*pools)
+    out[at] = 0
+    assert not out.any()
