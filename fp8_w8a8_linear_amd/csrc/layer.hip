@@ -169,6 +169,9 @@ nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_sc
     const int64_t ld_q = bf16 ? w->k / 2 : ld_a;
     if (w->n > (kMaxOperand - 1) / (w->k / 2) || m > (kMaxOperand - 1) / ld_q)
         return fail(NHM_ERR_UNSUPPORTED, "mxfp4: an operand of 2 GiB or more");
+    // up to 64 rows: workgroups of 512 threads take 16 features each
+    if (!mx_tiled(m) && (w->n + 15) / 16 > kMaxThreads / 512)
+        return fail(NHM_ERR_UNSUPPORTED, "mxfp4: %lld features are more than a launch holds", (long long)w->n);
     const MxWs l = mx_ws(m, w->n, w->k, a_type);
     if (l.total > 0 && (!ws || ws_bytes < l.total))
         return fail(NHM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", l.total, ws ? ws_bytes : (size_t)0);

@@ -76,7 +76,8 @@ NHM_API size_t nhm_mxfp4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k,
  *   out      (device) [m, ld_out] of out_type NHM_BF16 or NHM_F32, ld_out >= n, aligned to its element size
  *   ws       (device, 256-byte aligned) nhm_mxfp4_linear_workspace_bytes(...) bytes (may be 0: NULL)
  * m == 0 is a valid no-op. The result of a row does not depend on the other rows' values.
- * Operands of 2 GiB or more (of codes) are NHM_ERR_UNSUPPORTED.
+ * Operands of 2 GiB or more (of codes) are NHM_ERR_UNSUPPORTED, and so are more than 2^27 - 16 features
+ * with at most 64 rows.
  * Errors: NHM_ERR_NULL, NHM_ERR_SHAPE, NHM_ERR_ALIGN, NHM_ERR_UNSUPPORTED, NHM_ERR_WORKSPACE, NHM_ERR_HIP. */
 NHM_API nhm_status nhm_mxfp4_linear(const void* a, nhm_dtype a_type, const uint8_t* a_scale, int64_t m, int64_t ld_a,
                                     const nhm_mxfp4_weight* w, void* out, nhm_dtype out_type, int64_t ld_out, void* ws,

@@ -38,3 +38,18 @@ def test_tiles(tmp_path):
         tiles = -(-n // tn) * -(-m // tm)
         assert got[:2] == (tn, tm) and -(-tiles // (256 * got[2])) == turns, (case, got, tiles)
     assert len(r.stdout.splitlines()) == len(TILE_CASES)
+
+
+def test_more_features_than_a_launch_holds():
+    """Up to 64 rows a workgroup of 512 threads takes 16 features, and a launch holds fewer than 2^32 threads: 2^27 - 15 features, whose
+    codes are still below 2 GiB, are refused on the host."""
+    import ctypes as C
+
+    import fp8_w8a8_linear_amd as nhm
+    n, k = (1 << 27) - 15, 32
+    assert n * k // 2 < 1 << 31
+    for m in (1, 4, 5, 64):
+        need = nhm.mxfp4_linear_workspace_bytes(m, n, k, nhm.NHM_BF16)
+        w = nhm._Mxfp4Weight(0x10000, 0x20000, n, k, None)
+        status = nhm.lib.nhm_mxfp4_linear(0x30000, nhm.NHM_BF16, None, m, k, C.byref(w), 0x40000, nhm.NHM_BF16, n, 0x50000, need, None)
+        assert status == 4, (m, status, nhm.lib.nhm_last_error())
