@@ -154,7 +154,7 @@ __device__ __forceinline__ v4f mfma_mx16(const v4u& a, const v4u& b, const v4f& 
 // of row r that start 32 q into the step's 128-byte line, two blocks, and their two scale codes. The waves' sums are added in LDS
 // in wave order. TM: 16-row tiles of the activations. kQuant: the activations are bf16, and every workgroup quantises them
 // into LDS, behind its first loads of the weight. Bound by latency and the weight's bytes: 1 row x 10,304 x 2,688 4.4 us (14.7 MB,
-// 3.3 TB/s), 61 rows 9.9. (Loading a step or two ahead of the products made the call up to half again as long.)
+// 3.3 TB/s), 61 rows 9.9 to 10.7. (Loading a step or two ahead of the products made the call up to half again as long.)
 constexpr int kMxWaves = 8;
 
 template <int TM, bool kQuant>
@@ -281,10 +281,12 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_rows_kernel(const MxGemmArgs
 // A lane's half of a stage's row is KB / 2 bytes, KB / 32 blocks, whose scale codes are adjacent bytes: with 128 byte
 // slices a dword of its own, which the matrix instruction takes bytes of.
 //
-// 15,360 x 10,304 x 2,688: 275 to 300 us by the clock that the power leaves (2.8 to 3.1 PFLOP/s of codes; the matrix units busy 46 %
-// of the time, the operands' way from L2 into LDS, 133 bytes a ns and CU at most, about as long). 477 x 2,688 x 4,096: 12 us, a
-// workgroup's own chain of 16 stages. Taking the activations' scale codes as rows, without the launch that packs them (2 us), is
-// no faster from 96 to 15,360 rows.
+// 15,360 x 10,304 x 2,688: 265 to 300 us by the clock that the power leaves (2.8 to 3.2 PFLOP/s of codes). No unit is busy all the time:
+// the matrix units 45 %, LDS with the operands' reads 21 % (no bank conflicts), and the way from L2 into LDS about a fifth (7.0 MB to a
+// CU, at 133 bytes a ns at most). What is left is what each stage's wait and barrier keep from overlapping, not taken apart further.
+// f32 outputs, on the 128 x 128 tile: 353 to 398 us, the matrix units 33 % busy, LDS 19 %. 477 x 2,688 x 4,096: 12 us, a workgroup's
+// own chain of 16 stages, of which the ring of two has one on its way while one is used. Taking the activations' scale codes
+// as rows, without the launch that packs them (2 us), is no faster from 96 to 15,360 rows.
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));

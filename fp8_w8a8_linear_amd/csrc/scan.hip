@@ -53,7 +53,9 @@ __device__ __forceinline__ bool has_slot(int slot, int n_slots) { return slot >=
 // 4,096 24 us, 4,096 147), and a start of 5 us again where the workgroups, three to a CU by their LDS, do not all fit at once
 // (524 tokens in 6 sequences x 2,688, 260 the longest, 22 us). Eight lanes to a channel of two states each save a sixth of
 // the instructions and take 320 us in place of 356 for 16 sequences of 960, but 646 in place of 432 for 4 of 8,192 to 1,024 (both
-// as first written), whose few waves then wait for each other's results.
+// as first written, before the chunks and the wide rows), whose few waves then wait for each other's results. More states take more
+// sums to a lane, two where d_state is up to 32 and four past that: 15,360 x 4,096 x 32 540 to 570 us (14.9 instructions a token and wave),
+// x 64 1,056 to 1,071 (25.8).
 
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float v) {
@@ -337,7 +339,8 @@ static void launch_scan_r(const ScanPrefillArgs& a, hipStream_t st) {
 // Where sequences x channels do not fill the chip, sequences are cut into chunks of at least 128 tokens, up to 64 of them, for
 // about 1,024 workgroups, at the price of forming the decays twice. us, whole and cut: 4,096 tokens x 4,096 channels (4
 // chunks) 155 and 166, x 2,048 (8) 151 and 88, x 1,024 152 and 50, x 64 149 and 18; 15,360 x 512 547 and 94; 256 x 256
-// (2 of 128 tokens) 13.5 and 14.4, 1,024 x 1,024 41 and 19.
+// (2 of 128 tokens) 13.5 and 14.4, 1,024 x 1,024 41 and 19. The host knows the sequences' number and not their lengths: one of
+// 15,000 tokens beside 31 of 11, x 4,096 channels, is not cut and takes its own chain, 520 us.
 ScanSplit scan_split(int64_t dim, int64_t n_tokens, int64_t n_seqs) {
     const ScanSplit whole{1, n_tokens > 0 ? n_tokens : 1};
     const int64_t groups = (n_seqs > 0 ? n_seqs : 1) * ((dim + 15) / 16);
@@ -450,8 +453,9 @@ nhm_status launch_scan_decode(const ScanDecodeArgs& g, int32_t batch, hipStream_
 
 // ---------------------------------------------------------------- convolution
 //
-// A thread takes eight channels. Bound by bytes: x read and u written once (15,360 tokens x 4,096 46 us, 252 MB at 5.4 TB/s;
-// 8 single tokens 2.9 us, a chain of loads).
+// A thread takes eight channels. Bound by bytes: x read and u written once (15,360 tokens x 4,096 44 to 46 us, 252 MB at 5.4 TB/s, and
+// 16 MB more: each thread also writes the zero row that a window may be taken from to private memory). 1,920 sequences of 8 tokens, whose
+// tokens follow one another in a thread, 95 us for 346 MB. 8 single tokens 2.9 us, a chain of loads.
 
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7]));
