@@ -267,3 +267,22 @@ def test_decode_of_many_rows(nhm):
     assert torch.equal(out[at], nhm.causal_conv_decode(u[at], w, b, i32([3, 0, 2, 1]), pools[1])) and torch.equal(*pools)
     out[at] = 0
     assert not out.any()
+
+
+# ---------------------------------------------------------------- batches of padding alone
+
+@pytest.mark.parametrize("tokens", [0, 7, 2000])
+def test_no_sequences(nhm, tokens):
+    """A batch without sequences: every row is behind the last one and zero, the pools stay."""
+    dim, n = 72, 16
+    r = np.random.default_rng(25)
+    lay = Layer(nhm, r, dim, n)
+    u, dt, B, C, z = (torch.full((tokens, c), float("nan"), dtype=torch.bfloat16, device="cuda") for c in (dim, dim, n, n, dim))
+    none, states, windows = i32([]), torch.randn(2, dim, n, device="cuda"), bf16(r.normal(size=(2, 3, dim)))
+    pools = states.clone(), windows.clone()
+    out = torch.full((tokens, dim), 3.0, dtype=torch.bfloat16, device="cuda")
+    nhm.selective_scan_prefill(lay.params, u, dt, B, C, i32([0]), none, none, pools[0], z=z, out=out)
+    assert not out.any()
+    out.fill_(3.0)
+    nhm.causal_conv_prefill(u, bf16(r.normal(size=(dim, 4))), None, i32([0]), none, none, pools[1], out=out)
+    assert not out.any() and torch.equal(pools[0], states) and torch.equal(pools[1], windows)
